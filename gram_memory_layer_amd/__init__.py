@@ -11,9 +11,13 @@ Functions carry the C names:
     engram_hash, engram_gather, engram_wkv, engram_wkv_gathered, engram_gate_add,
     engram_forward, engram_forward_workspace_size, engram_wkv_gathered_scratch_size,
     engram_gate_partials_supported, engram_wkv_gate_partials, engram_gate_from_partials,
-    engram_check_geometry
-plus ``Geometry`` / ``HashTables`` (the C structs) and ``EngramLayer``, a
-holder for one layer's device tables, weights and workspace.
+    engram_check_geometry,
+    engram_wkv_adapters, engram_wkv_adapters_scratch_size, engram_forward_adapted,
+    engram_forward_adapted_workspace_size, engram_norm_quant, engram_beam_select,
+    engram_beam_select_scratch_size, engram_beam_reorder
+plus ``Geometry`` / ``HashTables`` (the C structs), ``Adapters`` (the low-rank
+adapters of a layer's projection) and ``EngramLayer``, a holder for one layer's
+device tables, weights and workspace.
 """
 from __future__ import annotations
 
@@ -28,13 +32,19 @@ __all__ = [
     "engram_wkv_gathered", "engram_wkv_gathered_scratch_size",
     "engram_gate_partials_supported", "engram_wkv_gate_partials", "engram_gate_from_partials",
     "engram_gate_add", "engram_forward", "engram_forward_hashed", "engram_forward_workspace_size",
-    "ERRBIT_TOKEN", "ERRBIT_HASH", "ERRBIT_ROW",
+    "Adapters", "engram_wkv_adapters", "engram_wkv_adapters_scratch_size",
+    "engram_forward_adapted", "engram_forward_adapted_workspace_size", "engram_norm_quant",
+    "engram_beam_select", "engram_beam_select_scratch_size", "engram_beam_reorder",
+    "ERRBIT_TOKEN", "ERRBIT_HASH", "ERRBIT_ROW", "ERRBIT_ADAPTER", "ERRBIT_LOGIT",
+    "ERRBIT_PARENT",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libengram.so")
 
 ERRBIT_TOKEN, ERRBIT_HASH, ERRBIT_ROW = 0x1, 0x2, 0x4
+ERRBIT_ADAPTER, ERRBIT_LOGIT, ERRBIT_PARENT = 0x8, 0x10, 0x20
+_SCALE_FORMATS = {"e8m0_32": 0, "f32_128": 1, "f32_row": 2}
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported geometry",
            3: "workspace missing or too small", 4: "HIP runtime error",
            5: "call needs more than the fixed scratch array holds"}
@@ -75,6 +85,11 @@ class Geometry(C.Structure):
 class HashTables(C.Structure):
     _fields_ = [("token_map", C.c_void_p), ("mult", C.c_void_p), ("prime", C.c_void_p),
                 ("offset", C.c_void_p)]
+
+
+class _CAdapters(C.Structure):
+    _fields_ = [("down", C.c_void_p), ("up", C.c_void_p), ("scale", C.c_void_p),
+                ("n", C.c_int32), ("rank", C.c_int32)]
 
 
 _lib = None
@@ -129,6 +144,25 @@ def load():
     L.engram_fixed_scratch_bytes.argtypes = []
     L.engram_forward_noalloc.restype = C.c_int
     L.engram_forward_noalloc.argtypes = [G, HT, P, P, P, P, P, P, P, P, P, i32, i32, P, P, P, P]
+    A = C.POINTER(_CAdapters)
+    L.engram_wkv_adapters_scratch_size.restype = C.c_size_t
+    L.engram_wkv_adapters_scratch_size.argtypes = [G, A, i64]
+    L.engram_wkv_adapters.restype = C.c_int
+    L.engram_wkv_adapters.argtypes = [G, A, P, P, P, i64, P, P, C.c_size_t, P, P]
+    L.engram_forward_adapted_workspace_size.restype = C.c_size_t
+    L.engram_forward_adapted_workspace_size.argtypes = [G, A, i64]
+    L.engram_forward_adapted.restype = C.c_int
+    L.engram_forward_adapted.argtypes = [G, HT, A, P, P, P, P, P, P, P, P, P, P, i32, i32, P, P, P,
+                                         C.c_size_t, P, P]
+    L.engram_norm_quant.restype = C.c_int
+    L.engram_norm_quant.argtypes = [P, P, P, i64, i32, C.c_float, i32, P, P, P, P]
+    L.engram_beam_select_scratch_size.restype = C.c_size_t
+    L.engram_beam_select_scratch_size.argtypes = [i32, i32, i32]
+    L.engram_beam_select.restype = C.c_int
+    L.engram_beam_select.argtypes = [P, i32, i64, P, P, i32, i32, i32, i32, i32, P, P, P, P, P,
+                                     C.c_size_t, P, P]
+    L.engram_beam_reorder.restype = C.c_int
+    L.engram_beam_reorder.argtypes = [P, P, i32, P, i32, i32, P, P]
     _lib = L
     return L
 
@@ -524,10 +558,250 @@ def engram_forward_noalloc(g: Geometry, tables: dict, table, scales, w, q, k, x,
     return out
 
 
+# ------------------------------------------------------------------ around the layer
+def _launch(name, fn, dev, *args):
+    """Call a C entry on `dev`'s current stream, with `dev` the current device."""
+    if torch.cuda.current_device() == dev.index:
+        _check(name, fn(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            _check(name, fn(*args, _stream(dev)))
+
+
+class Adapters:
+    """Low-rank adapters of a layer's wkv projection, on the device: down bf16
+    [n, rank, K], up bf16 [n, N, rank], scale fp32 [n] or None (1 for all).
+    Position m with adapter j gets scale[j] * up[j] (down[j] a[m]) added."""
+
+    def __init__(self, down, up, scale=None):
+        _dev(down, "down", torch.bfloat16)
+        if down.dim() != 3:
+            raise ValueError("down must be [n, rank, K]")
+        n, rank, K = down.shape
+        _dev(up, "up", torch.bfloat16, None, down.device)
+        if up.dim() != 3 or up.shape[0] != n or up.shape[2] != rank:
+            raise ValueError("up must be [n, N, rank]")
+        if scale is not None:
+            _dev(scale, "scale", torch.float32, (n,), down.device)
+        self.down, self.up, self.scale = down, up, scale
+        self.n, self.rank, self.K, self.N = n, rank, K, up.shape[1]
+        self._c = _CAdapters(down.data_ptr(), up.data_ptr(), _ptr(scale), n, rank)
+
+    def _for(self, g: Geometry, dev):
+        if self.K != g.K or self.N != g.N:
+            raise ValueError("adapters of a [%d -> %d] projection, the geometry's is [%d -> %d]" % (
+                self.K, self.N, g.K, g.N))
+        if self.down.device != dev:
+            raise ValueError("adapters are on %s, expected %s" % (self.down.device, dev))
+        return C.byref(self._c)
+
+
+def engram_wkv_adapters_scratch_size(g: Geometry, adapters: Adapters, M: int) -> int:
+    return load().engram_wkv_adapters_scratch_size(C.byref(g), C.byref(adapters._c), int(M))
+
+
+def engram_wkv_adapters(g: Geometry, adapters: Adapters, a, w, adapter_ids, kv=None, scratch=None,
+                        err=None):
+    """The projection with each position's own adapter: a bf16 [M, K], w bf16
+    [N, K], adapter_ids int32 [M] (-1: none) -> kv bf16 [M, N]."""
+    L = load()
+    dev = a.device
+    _dev(a, "a", torch.bfloat16, None, dev)
+    if a.dim() != 2 or a.shape[1] != g.K:
+        raise ValueError("a must be [M, %d]" % g.K)
+    M = a.shape[0]
+    _dev(w, "w", torch.bfloat16, (g.N, g.K), dev)
+    ad = adapters._for(g, dev)
+    _dev(adapter_ids, "adapter_ids", torch.int32, (M,), dev)
+    if kv is None:
+        kv = torch.empty((M, g.N), dtype=torch.bfloat16, device=dev)
+    _dev(kv, "kv", torch.bfloat16, (M, g.N), dev)
+    if scratch is None:
+        scratch = torch.empty(max(engram_wkv_adapters_scratch_size(g, adapters, M), 1),
+                              dtype=torch.uint8, device=dev)
+    _dev(scratch, "scratch", torch.uint8, None, dev)
+    if err is not None:
+        _dev(err, "err", torch.int32, (1,), dev)
+    _launch("engram_wkv_adapters", L.engram_wkv_adapters, dev, C.byref(g), ad, a.data_ptr(),
+            w.data_ptr(), adapter_ids.data_ptr(), M, kv.data_ptr(), scratch.data_ptr(),
+            scratch.numel(), _ptr(err))
+    return kv
+
+
+def engram_forward_adapted_workspace_size(g: Geometry, adapters: Adapters, n_tok: int) -> int:
+    return load().engram_forward_adapted_workspace_size(C.byref(g), C.byref(adapters._c),
+                                                        int(n_tok))
+
+
+def engram_forward_adapted(g: Geometry, tables: dict, adapters: Adapters, table, scales, w, q, k,
+                           x, ids, adapter_ids, mask=None, state=None, out=None, gate=None,
+                           workspace=None, err=None):
+    """The whole forward with adapters: as engram_forward, adapter_ids int32 [B]
+    naming each sequence's adapter (-1: none)."""
+    L = load()
+    dev = x.device
+    _dev(ids, "ids", torch.int32, None, dev)
+    if ids.dim() != 2:
+        raise ValueError("ids must be [B, T]")
+    B, T = ids.shape
+    _dev(x, "x", torch.bfloat16, (B, T, g.hc_mult, g.dim), dev)
+    ht = _tables(tables, g, dev)
+    ad = adapters._for(g, dev)
+    _dev(adapter_ids, "adapter_ids", torch.int32, (B,), dev)
+    _dev(table, "table", torch.uint8, (g.num_embeddings, g.head_dim), dev)
+    _dev(scales, "scales", torch.uint8, (g.num_embeddings, g.head_dim // 32), dev)
+    _dev(w, "w", torch.bfloat16, (g.N, g.K), dev)
+    _dev(q, "q", torch.bfloat16, (g.hc_mult, g.dim), dev)
+    _dev(k, "k", torch.bfloat16, (g.hc_mult, g.dim), dev)
+    if state is not None:
+        _dev(state, "state", torch.int32, (B, g.max_ngram_size - 1), dev)
+    m = _mask(mask, B * T, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    _dev(out, "out", torch.bfloat16, (B, T, g.hc_mult, g.dim), dev)
+    if gate is not None:
+        _dev(gate, "gate", torch.float32, (B, T, g.hc_mult), dev)
+    if workspace is None:
+        workspace = torch.empty(max(engram_forward_adapted_workspace_size(g, adapters, B * T), 1),
+                                dtype=torch.uint8, device=dev)
+    _dev(workspace, "workspace", torch.uint8, None, dev)
+    if err is not None:
+        _dev(err, "err", torch.int32, (1,), dev)
+    _launch("engram_forward_adapted", L.engram_forward_adapted, dev, C.byref(g), C.byref(ht), ad,
+            table.data_ptr(), scales.data_ptr(), w.data_ptr(), q.data_ptr(), k.data_ptr(),
+            _ptr(state), x.data_ptr(), ids.data_ptr(), adapter_ids.data_ptr(), _ptr(m), B, T,
+            out.data_ptr(), _ptr(gate), workspace.data_ptr(), workspace.numel(), _ptr(err))
+    return out
+
+
+def engram_norm_quant(x, weight=None, residual=None, eps=1e-6, scale_format="e8m0_32", codes=None,
+                      scales=None, total=None):
+    """Root-mean-square norm of h = x + residual with an e4m3 output: x bf16
+    [..., dim], residual the same or None, weight bf16 [dim] or None ->
+    (codes uint8 like x, scales, total).  scale_format "e8m0_32": scales uint8
+    [..., ceil(dim/32)]; "f32_128": fp32 [..., ceil(dim/128)]; "f32_row": fp32
+    [..., 1].  total = bf16(h) (may be x or residual; None without a residual
+    unless given)."""
+    L = load()
+    if scale_format not in _SCALE_FORMATS:
+        raise ValueError("scale_format must be one of %s" % ", ".join(_SCALE_FORMATS))
+    _dev(x, "x", torch.bfloat16)
+    dev, shape = x.device, tuple(x.shape)
+    if x.dim() < 1 or shape[-1] == 0:
+        raise ValueError("x must be [..., dim]")
+    dim = shape[-1]
+    if weight is not None:
+        _dev(weight, "weight", torch.bfloat16, (dim,), dev)
+    if residual is not None:
+        _dev(residual, "residual", torch.bfloat16, shape, dev)
+        if total is None:
+            total = torch.empty_like(x)
+    if total is not None:
+        _dev(total, "total", torch.bfloat16, shape, dev)
+    if codes is None:
+        codes = torch.empty(shape, dtype=torch.uint8, device=dev)
+    _dev(codes, "codes", torch.uint8, shape, dev)
+    group = 32 if scale_format == "e8m0_32" else 128 if scale_format == "f32_128" else dim
+    kind = torch.uint8 if scale_format == "e8m0_32" else torch.float32
+    s_shape = shape[:-1] + ((dim + group - 1) // group,)
+    if scales is None:
+        scales = torch.empty(s_shape, dtype=kind, device=dev)
+    _dev(scales, "scales", kind, s_shape, dev)
+    _launch("engram_norm_quant", L.engram_norm_quant, dev, x.data_ptr(), _ptr(residual),
+            _ptr(weight), x.numel() // dim, dim, float(eps), _SCALE_FORMATS[scale_format],
+            _ptr(total), codes.data_ptr(), scales.data_ptr())
+    return codes, scales, total
+
+
+def engram_beam_select_scratch_size(B: int, W: int, V: int) -> int:
+    return load().engram_beam_select_scratch_size(int(B), int(W), int(V))
+
+
+def engram_beam_select(logits, scores, finished=None, eos_id=-1, pad_id=0, tokens=None,
+                       parents=None, new_scores=None, new_finished=None, scratch=None, err=None):
+    """Beam search's selection: logits bf16 or fp32 [B*W, V] (or [B, W, V]; rows
+    may be strided), scores fp32 [B, W], finished bool/uint8 [B, W] or None ->
+    (tokens int32, parents int32, new_scores fp32, new_finished uint8), all
+    [B, W], best first.  new_scores may be scores, new_finished finished."""
+    L = load()
+    dev = logits.device
+    _dev(scores, "scores", torch.float32, None, dev)
+    if scores.dim() != 2:
+        raise ValueError("scores must be [B, W]")
+    B, W = shape = tuple(scores.shape)
+    if logits.device.type != "cuda":
+        raise ValueError("logits must be a device tensor (got %s)" % logits.device)
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits must be torch.float32 or torch.bfloat16 (got %s)" % logits.dtype)
+    V = logits.shape[-1] if logits.dim() else 0
+    if tuple(logits.shape) not in ((B * W, V), (B, W, V)):
+        raise ValueError("logits must be [B*W, V] or [B, W, V]")
+    ld = logits.stride(-2) if B * W > 1 else V
+    if logits.dim() == 3 and W == 1 and B > 1:
+        ld = logits.stride(0)
+    if (V > 1 and logits.stride(-1) != 1) or ld < V or (
+            logits.dim() == 3 and B > 1 and W > 1 and logits.stride(0) != W * ld):
+        raise ValueError("logits must have contiguous rows, evenly apart")
+    if finished is not None:
+        if finished.dtype == torch.bool:
+            finished = finished.view(torch.uint8)
+        _dev(finished, "finished", torch.uint8, shape, dev)
+
+    def buf(t, name, dtype):
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        return _dev(t, name, dtype, shape, dev)
+    tokens = buf(tokens, "tokens", torch.int32)
+    parents = buf(parents, "parents", torch.int32)
+    new_scores = buf(new_scores, "new_scores", torch.float32)
+    new_finished = buf(new_finished, "new_finished", torch.uint8)
+    if scratch is None:
+        scratch = torch.empty(max(engram_beam_select_scratch_size(B, W, V), 1), dtype=torch.uint8,
+                              device=dev)
+    _dev(scratch, "scratch", torch.uint8, None, dev)
+    if err is not None:
+        _dev(err, "err", torch.int32, (1,), dev)
+    _launch("engram_beam_select", L.engram_beam_select, dev, logits.data_ptr(),
+            int(logits.dtype == torch.float32), ld, scores.data_ptr(), _ptr(finished), B, W, V,
+            int(eos_id), int(pad_id), tokens.data_ptr(), parents.data_ptr(),
+            new_scores.data_ptr(), new_finished.data_ptr(), scratch.data_ptr(), scratch.numel(),
+            _ptr(err))
+    return tokens, parents, new_scores, new_finished
+
+
+def engram_beam_reorder(states, parents, err=None):
+    """state[b][w] = state[b][parents[b][w]] in place for every tensor of the
+    list `states` (any dtype, [B*W, ...] or [B, W, ...], contiguous, rows of a
+    multiple of 4 bytes; for instance each layer's engram_hash state);
+    parents int32 [B, W]."""
+    L = load()
+    dev = parents.device
+    _dev(parents, "parents", torch.int32, None, dev)
+    if parents.dim() != 2:
+        raise ValueError("parents must be [B, W]")
+    B, W = parents.shape
+    n = len(states)
+    size = []
+    for st in states:
+        _dev(st, "state", st.dtype if isinstance(st, torch.Tensor) else None, None, dev)
+        if not st.dim() or (st.shape[0] != B * W and tuple(st.shape[:2]) != (B, W)):
+            raise ValueError("a state must be [B*W, ...] or [B, W, ...] (got %s)" % (tuple(st.shape),))
+        size.append(st.numel() * st.element_size() // max(B * W, 1))
+    if err is not None:
+        _dev(err, "err", torch.int32, (1,), dev)
+    if B * W == 0:
+        return states
+    _launch("engram_beam_reorder", L.engram_beam_reorder, dev,
+            (C.c_void_p * n)(*[st.data_ptr() for st in states]), (C.c_int64 * n)(*size), n,
+            parents.data_ptr(), B, W, _ptr(err))
+    return states
+
+
 class EngramLayer:
     """One Engram layer's device-resident inputs: geometry, hash tables, the
     fp8 table and scales, the wkv weight and q/k weights, plus a reusable
-    workspace.  `forward` is engram_forward."""
+    workspace.  `forward` is engram_forward, or with adapters
+    engram_forward_adapted."""
 
     def __init__(self, g: Geometry, tables: dict, table, scales, w, q, k):
         self.g, self.tables = g, tables
@@ -540,7 +814,16 @@ class EngramLayer:
             self._ws = torch.empty(need, dtype=torch.uint8, device=self.w.device)
         return self._ws
 
-    def forward(self, x, ids, mask=None, state=None, out=None, gate=None, err=None):
+    def forward(self, x, ids, mask=None, state=None, out=None, gate=None, err=None, adapters=None,
+                adapter_ids=None):
+        if adapters is not None:
+            need = max(engram_forward_adapted_workspace_size(self.g, adapters, ids.numel()), 1)
+            if self._ws is None or self._ws.numel() < need:
+                self._ws = torch.empty(need, dtype=torch.uint8, device=self.w.device)
+            return engram_forward_adapted(self.g, self.tables, adapters, self.table, self.scales,
+                                          self.w, self.q, self.k, x, ids, adapter_ids, mask=mask,
+                                          state=state, out=out, gate=gate, workspace=self._ws,
+                                          err=err)
         return engram_forward(self.g, self.tables, self.table, self.scales, self.w, self.q, self.k,
                               x, ids, mask=mask, state=state, out=out, gate=gate,
                               workspace=self.workspace(ids.numel()), err=err)

@@ -443,4 +443,172 @@ engram_status engram_forward_hashed(const engram_geometry* g, const uint8_t* tab
     return from_hip(e);
 }
 
+// ---------------------------------------------------------------- around the layer
+
+static engram_status adapters_check(const engram_adapters* ad) {
+    if (ad == nullptr || !ad->down || !ad->up) return ENGRAM_ERR_INVALID_ARG;
+    if (!aligned16(ad->down) || !aligned16(ad->up) || ((uintptr_t)ad->scale & 3u) != 0)
+        return ENGRAM_ERR_INVALID_ARG;
+    if (ad->n < 1 || ad->n > 65536 || ad->rank < 8 || ad->rank > 128 || ad->rank % 8 != 0)
+        return ENGRAM_ERR_UNSUPPORTED;
+    return ENGRAM_OK;
+}
+
+static engram::Adapters adapters_of(const engram_adapters& ad) {
+    return engram::Adapters{ad.down, ad.up, ad.scale, ad.n, ad.rank};
+}
+
+size_t engram_wkv_adapters_scratch_size(const engram_geometry* g, const engram_adapters* ad,
+                                        int64_t M) {
+    if (engram_check_geometry(g) != ENGRAM_OK || adapters_check(ad) != ENGRAM_OK || M <= 0) return 0;
+    return align256(engram::adapters_scratch_bytes(ad->rank, M));
+}
+
+engram_status engram_wkv_adapters(const engram_geometry* g, const engram_adapters* ad,
+                                  const uint16_t* a, const uint16_t* w,
+                                  const int32_t* adapter_ids, int64_t M, uint16_t* kv,
+                                  void* scratch, size_t scratch_bytes, uint32_t* err,
+                                  void* stream) {
+    engram_status st = engram_check_geometry(g);
+    if (st != ENGRAM_OK) return st;
+    if ((st = adapters_check(ad)) != ENGRAM_OK) return st;
+    if (M < 0 || M >= kMaxTokens) return ENGRAM_ERR_INVALID_ARG;
+    if (M == 0) return ENGRAM_OK;
+    if (!a || !w || !adapter_ids || !kv) return ENGRAM_ERR_INVALID_ARG;
+    if (!aligned16(a) || !aligned16(w) || !aligned16(kv) || ((uintptr_t)adapter_ids & 3u) != 0)
+        return ENGRAM_ERR_INVALID_ARG;
+    if (scratch == nullptr || scratch_bytes < engram_wkv_adapters_scratch_size(g, ad, M) ||
+        ((uintptr_t)scratch & 255u) != 0)
+        return ENGRAM_ERR_WORKSPACE;
+    const Geom gg = engram::make_geom(*g);
+    return from_hip(engram::launch_wkv_adapters(a, w, adapters_of(*ad), adapter_ids, 1, M, gg.N,
+                                                gg.K, kv, scratch, err, (hipStream_t)stream));
+}
+
+size_t engram_forward_adapted_workspace_size(const engram_geometry* g, const engram_adapters* ad,
+                                             int64_t n_tok) {
+    if (engram_check_geometry(g) != ENGRAM_OK || adapters_check(ad) != ENGRAM_OK || n_tok <= 0)
+        return 0;
+    return engram_forward_workspace_size(g, n_tok) +
+           align256(engram::adapters_scratch_bytes(ad->rank, n_tok));
+}
+
+engram_status engram_forward_adapted(const engram_geometry* g, const engram_hash_tables* t,
+                                     const engram_adapters* ad, const uint8_t* table,
+                                     const uint8_t* scales, const uint16_t* w, const uint16_t* q,
+                                     const uint16_t* k, int32_t* state, const uint16_t* x,
+                                     const int32_t* ids, const int32_t* adapter_ids,
+                                     const uint8_t* mask, int32_t B, int32_t T, uint16_t* out,
+                                     float* gate, void* workspace, size_t workspace_bytes,
+                                     uint32_t* err, void* stream) {
+    engram_status st = engram_check_geometry(g);
+    if (st != ENGRAM_OK) return st;
+    if ((st = adapters_check(ad)) != ENGRAM_OK) return st;
+    st = engram::forward_check(g, t, table, scales, w, q, k, x, ids, B, T, out);
+    const int64_t n_tok = (int64_t)B * T;
+    if (st != ENGRAM_OK || n_tok == 0) return st;
+    if (!adapter_ids || ((uintptr_t)adapter_ids & 3u) != 0) return ENGRAM_ERR_INVALID_ARG;
+    if (workspace == nullptr ||
+        workspace_bytes < engram_forward_adapted_workspace_size(g, ad, n_tok) ||
+        ((uintptr_t)workspace & 255u) != 0)
+        return ENGRAM_ERR_WORKSPACE;
+    const Geom gg = engram::make_geom(*g);
+    const FwdWorkspace f = carve(gg, n_tok, workspace);
+    void* low = (char*)workspace + engram_forward_workspace_size(g, n_tok);
+    hipStream_t s = (hipStream_t)stream;
+    hipError_t e = engram::launch_hash(gg, *t, state, ids, B, T, f.hash_ids, err, s);
+    if (e == hipSuccess)
+        e = engram::launch_gather(gg, table, scales, f.hash_ids, n_tok, f.rows, err, s);
+    if (e == hipSuccess)
+        e = engram::launch_wkv_adapters(f.rows, w, adapters_of(*ad), adapter_ids, T, n_tok, gg.N,
+                                        gg.K, f.kv, low, err, s);
+    if (e == hipSuccess)
+        e = engram::launch_gate_add(gg, x, f.kv, q, k, mask, n_tok, out, gate, s);
+    return from_hip(e);
+}
+
+engram_status engram_norm_quant(const uint16_t* x, const uint16_t* residual,
+                                const uint16_t* weight, int64_t rows, int32_t dim, float eps,
+                                int32_t scale_format, uint16_t* total, uint8_t* codes,
+                                void* scales, void* stream) {
+    if (rows < 0 || rows >= kMaxTokens || !(eps >= 0.0f) || !isfinite(eps))
+        return ENGRAM_ERR_INVALID_ARG;
+    if (scale_format < ENGRAM_SCALE_E8M0_32 || scale_format > ENGRAM_SCALE_F32_ROW)
+        return ENGRAM_ERR_INVALID_ARG;
+    if (dim < 8 || dim > 32768 || dim % 8 != 0) return ENGRAM_ERR_UNSUPPORTED;
+    if (rows == 0) return ENGRAM_OK;
+    if (!x || !codes || !scales) return ENGRAM_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(total) ||
+        ((uintptr_t)codes & 7u) != 0 ||
+        (scale_format != ENGRAM_SCALE_E8M0_32 && ((uintptr_t)scales & 3u) != 0))
+        return ENGRAM_ERR_INVALID_ARG;
+    return from_hip(engram::launch_norm_quant(x, residual, weight, rows, dim, eps, scale_format,
+                                              total, codes, scales, (hipStream_t)stream));
+}
+
+// the sizes a selection takes: 0, or the status that refuses them
+static engram_status beam_check(int32_t B, int32_t W, int32_t V) {
+    if (B < 0 || W < 1 || V < 1) return ENGRAM_ERR_INVALID_ARG;
+    if (W > 32 || W > V || V > (1 << 30) || (int64_t)W * V >= ((int64_t)1 << 31) ||
+        (int64_t)B * W > 65535)
+        return ENGRAM_ERR_UNSUPPORTED;
+    return ENGRAM_OK;
+}
+
+size_t engram_beam_select_scratch_size(int32_t B, int32_t W, int32_t V) {
+    if (beam_check(B, W, V) != ENGRAM_OK || B == 0) return 0;
+    return engram::beam_scratch_bytes((int64_t)B * W, W, V);
+}
+
+engram_status engram_beam_select(const void* logits, int32_t logits_f32, int64_t ld,
+                                 const float* scores, const uint8_t* finished, int32_t B,
+                                 int32_t W, int32_t V, int32_t eos_id, int32_t pad_id,
+                                 int32_t* tokens, int32_t* parents, float* new_scores,
+                                 uint8_t* new_finished, void* scratch, size_t scratch_bytes,
+                                 uint32_t* err, void* stream) {
+    const engram_status st = beam_check(B, W, V);
+    if (st != ENGRAM_OK) return st;
+    if (ld < V || ld >= ((int64_t)1 << 40) || pad_id < 0 || pad_id >= V || eos_id < -1 ||
+        (logits_f32 != 0 && logits_f32 != 1))
+        return ENGRAM_ERR_INVALID_ARG;
+    if (B == 0) return ENGRAM_OK;
+    if (!logits || !scores || !tokens || !parents || !new_scores) return ENGRAM_ERR_INVALID_ARG;
+    if (((uintptr_t)logits & (logits_f32 ? 3u : 1u)) != 0 || ((uintptr_t)scores & 3u) != 0 ||
+        ((uintptr_t)tokens & 3u) != 0 || ((uintptr_t)parents & 3u) != 0 ||
+        ((uintptr_t)new_scores & 3u) != 0)
+        return ENGRAM_ERR_INVALID_ARG;
+    if (scratch == nullptr || scratch_bytes < engram_beam_select_scratch_size(B, W, V) ||
+        ((uintptr_t)scratch & 255u) != 0)
+        return ENGRAM_ERR_WORKSPACE;
+    return from_hip(engram::launch_beam_select(logits, logits_f32 != 0, ld, scores, finished, B, W,
+                                               V, eos_id, pad_id, tokens, parents, new_scores,
+                                               new_finished, scratch, err, (hipStream_t)stream));
+}
+
+engram_status engram_beam_reorder(void* const* states, const int64_t* row_bytes,
+                                  int32_t n_states, const int32_t* parents, int32_t B, int32_t W,
+                                  uint32_t* err, void* stream) {
+    if (states == nullptr || row_bytes == nullptr || B < 0 || W < 1) return ENGRAM_ERR_INVALID_ARG;
+    if (n_states < 1 || n_states > engram::kMaxStates) return ENGRAM_ERR_INVALID_ARG;
+    if (W > 32 || B > 65535) return ENGRAM_ERR_UNSUPPORTED;
+    for (int i = 0; i < n_states; ++i) {
+        if (row_bytes[i] < 4 || row_bytes[i] % 4 != 0) return ENGRAM_ERR_INVALID_ARG;
+        if (row_bytes[i] >= ((int64_t)1 << 36)) return ENGRAM_ERR_UNSUPPORTED;
+    }
+    if (B == 0) return ENGRAM_OK;
+    if (!parents || ((uintptr_t)parents & 3u) != 0) return ENGRAM_ERR_INVALID_ARG;
+    for (int i = 0; i < n_states; ++i) {
+        if (states[i] == nullptr || ((uintptr_t)states[i] & 3u) != 0) return ENGRAM_ERR_INVALID_ARG;
+        const char* at = (const char*)states[i];
+        for (int j = 0; j < i; ++j) {  // changed in place: no two may overlap
+            const char* other = (const char*)states[j];
+            if (at < other + (int64_t)B * W * row_bytes[j] &&
+                other < at + (int64_t)B * W * row_bytes[i])
+                return ENGRAM_ERR_INVALID_ARG;
+        }
+    }
+    return from_hip(engram::launch_beam_reorder(states, row_bytes, n_states, parents, B, W, err,
+                                                (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -177,6 +177,38 @@ hipError_t launch_gate_add(const Geom& g, const uint16_t* x, const uint16_t* kv,
                            const uint16_t* q, const uint16_t* k, const uint8_t* mask,
                            int64_t n_tok, uint16_t* out, float* gate, hipStream_t s);
 
+// The projection with low-rank adapters: position m takes adapter ids[m / seg]
+// (none for -1); scratch of adapters_scratch_bytes holds the first product.
+struct Adapters {
+    const uint16_t* down;  // [n][rank][K]
+    const uint16_t* up;    // [n][N][rank]
+    const float* scale;    // [n] or null (all 1)
+    int n, rank;
+};
+size_t adapters_scratch_bytes(int rank, int64_t M);
+hipError_t launch_wkv_adapters(const uint16_t* a, const uint16_t* w, const Adapters& ad,
+                               const int32_t* ids, int seg, int64_t M, int N, int K, uint16_t* kv,
+                               void* scratch, uint32_t* err, hipStream_t s);
+// the projection with the adapters' second product (u from the first) added
+struct AddAdapters;
+hipError_t launch_wkv_added(const uint16_t* a, const uint16_t* w, int64_t M, int N, int K,
+                            const AddAdapters& ad, uint16_t* kv, hipStream_t s);
+
+hipError_t launch_norm_quant(const uint16_t* x, const uint16_t* res, const uint16_t* weight,
+                             int64_t rows, int dim, float eps, int scale_format, uint16_t* total,
+                             uint8_t* codes, void* scales, hipStream_t s);
+
+size_t beam_scratch_bytes(int64_t rows, int W, int V);
+hipError_t launch_beam_select(const void* logits, bool f32, int64_t ld, const float* cum,
+                              const uint8_t* finished, int64_t B, int W, int V, int32_t eos_id,
+                              int32_t pad_id, int32_t* tokens, int32_t* parents, float* new_cum,
+                              uint8_t* new_finished, void* scratch, uint32_t* err, hipStream_t s);
+
+constexpr int kMaxStates = 32;
+hipError_t launch_beam_reorder(void* const* states, const int64_t* row_bytes, int n,
+                               const int32_t* parents, int64_t B, int W, uint32_t* err,
+                               hipStream_t s);
+
 // engram_forward split at its workspace: every other argument check, and the
 // launches given a workspace of engram_forward_workspace_size bytes.
 engram_status forward_check(const engram_geometry* g, const engram_hash_tables* t,

@@ -21,7 +21,7 @@
 //    masked on store; no access leaves the operands.
 #include <type_traits>
 
-#include "tiles.h"
+#include "adapters.h"
 
 namespace engram {
 namespace {
@@ -33,10 +33,12 @@ __device__ __forceinline__ int swz(int row, int ch) {
     return ch ^ ((row & 7) ^ ((row >> 3) & 1));
 }
 
-template <int BM, int BN, int WM, int WN>
+// D: NoAdapters, or AddAdapters (a low-rank adapter's product added to the
+// accumulators before they are rounded).
+template <int BM, int BN, int WM, int WN, class D>
 __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64, 1)
 wkv_kernel(const uint16_t* __restrict__ A, const uint16_t* __restrict__ W, int64_t M, int N,
-           int K, uint16_t* __restrict__ C, int tiles_m, int tiles_n, int per_xcd) {
+           int K, uint16_t* __restrict__ C, int tiles_m, int tiles_n, int per_xcd, const D ad) {
     constexpr int WAVES_N = BN / WN;
     constexpr int NT = (BM / WM) * WAVES_N * 64;
     constexpr int TM = WM / 32, TN = WN / 32;
@@ -145,6 +147,8 @@ wkv_kernel(const uint16_t* __restrict__ A, const uint16_t* __restrict__ W, int64
         __syncthreads();
     }
 
+    if constexpr (D::on) ad.template add<TM, TN>(acc, m0 + wm * WM, M, n0 + wn * WN, N, lane);
+
     // ---- epilogue: D[n][m]; lane holds m = lane%32, n = 8*(v/4) + 4*(lane/32) + v%4
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
@@ -164,16 +168,16 @@ wkv_kernel(const uint16_t* __restrict__ A, const uint16_t* __restrict__ W, int64
     }
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, class D>
 hipError_t run(const uint16_t* a, const uint16_t* w, int64_t M, int N, int K, uint16_t* kv,
-               hipStream_t s) {
+               const D& ad, hipStream_t s) {
     constexpr int NT = (BM / WM) * (BN / WN) * 64;
     const int tiles_m = (int)((M + BM - 1) / BM);
     const int tiles_n = (N + BN - 1) / BN;
     const int total = tiles_m * tiles_n;
     const int per_xcd = (total + N_XCD - 1) / N_XCD;
-    wkv_kernel<BM, BN, WM, WN>
-        <<<dim3(per_xcd * N_XCD), dim3(NT), 0, s>>>(a, w, M, N, K, kv, tiles_m, tiles_n, per_xcd);
+    wkv_kernel<BM, BN, WM, WN, D><<<dim3(per_xcd * N_XCD), dim3(NT), 0, s>>>(
+        a, w, M, N, K, kv, tiles_m, tiles_n, per_xcd, ad);
     return hipGetLastError();
 }
 
@@ -197,11 +201,11 @@ constexpr bool WAVES8 = true;
 // BT x BT output tiles (BT = 256: 128 x 128 per wave; BT = 128: 64 x 64 per
 // wave).  Columns [0, N) of this launch start at W row 0 and C column 0; C
 // rows are `ldc` elements apart.
-template <int BT, int WMV = 2, int WNV = 2>
+template <int BT, int WMV, int WNV, class D>
 __device__ __forceinline__ void wkv_tile(const uint16_t* __restrict__ A,
                                          const uint16_t* __restrict__ W, int64_t M, int N, int K,
                                          uint16_t* __restrict__ C, int64_t ldc, int tiles_m,
-                                         int tiles_n, int per_xcd, uint8_t* smem) {
+                                         int tiles_n, int per_xcd, const D& ad, uint8_t* smem) {
     constexpr int NW = WMV * WNV;              // waves: WMV along m, WNV along n
     constexpr int BM = BT, BN = BT, WM = BT / WMV, WN = BT / WNV;
     constexpr int TI = WM / 32, TJ = WN / 32;  // 32 x 32 MFMA tiles per wave
@@ -354,6 +358,7 @@ __device__ __forceinline__ void wkv_tile(const uint16_t* __restrict__ A,
     for (int kt = 0; kt + 1 < nk; ++kt) k_tile(kt, T{});
     k_tile(nk - 1, F{});
     __syncthreads();  // every wave is done with the operand stages
+    if constexpr (D::on) ad.template add<TI, TJ>(acc, m0 + wm * WM, M, n0 + wn * WN, N, lane);
 
     // ---- epilogue through LDS.  D[n][m]: lane holds m = lane%32 (+32 i) and
     // n = 32 j + 8 (v/4) + 4 (lane/32) + v%4.  Each wave writes its WM x WN
@@ -390,42 +395,52 @@ __device__ __forceinline__ void wkv_tile(const uint16_t* __restrict__ A,
     }
 }
 
+template <class D>
 __global__ void __launch_bounds__(F_NT, 1)
 wkv_fast_256(const uint16_t* __restrict__ A, const uint16_t* __restrict__ W, int64_t M, int N,
-             int K, uint16_t* __restrict__ C, int64_t ldc, int tiles_m, int tiles_n, int per_xcd) {
+             int K, uint16_t* __restrict__ C, int64_t ldc, int tiles_m, int tiles_n, int per_xcd,
+             const D ad) {
     __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * (256 + 256) * 128];
-    wkv_tile<256>(A, W, M, N, K, C, ldc, tiles_m, tiles_n, per_xcd, smem);
+    wkv_tile<256, 2, 2>(A, W, M, N, K, C, ldc, tiles_m, tiles_n, per_xcd, ad, smem);
 }
 
+template <class D>
 __global__ void __launch_bounds__(2 * F_NT, 1)
 wkv_fast_256w8(const uint16_t* __restrict__ A, const uint16_t* __restrict__ W, int64_t M, int N,
                int K, uint16_t* __restrict__ C, int64_t ldc, int tiles_m, int tiles_n,
-               int per_xcd) {
+               int per_xcd, const D ad) {
     __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * (256 + 256) * 128];
-    wkv_tile<256, 2, 4>(A, W, M, N, K, C, ldc, tiles_m, tiles_n, per_xcd, smem);
+    wkv_tile<256, 2, 4>(A, W, M, N, K, C, ldc, tiles_m, tiles_n, per_xcd, ad, smem);
 }
 
+template <class D>
 __global__ void __launch_bounds__(F_NT, 1)
 wkv_fast_128(const uint16_t* __restrict__ A, const uint16_t* __restrict__ W, int64_t M, int N,
-             int K, uint16_t* __restrict__ C, int64_t ldc, int tiles_m, int tiles_n, int per_xcd) {
+             int K, uint16_t* __restrict__ C, int64_t ldc, int tiles_m, int tiles_n, int per_xcd,
+             const D ad) {
     __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * (128 + 128) * 128];
-    wkv_tile<128>(A, W, M, N, K, C, ldc, tiles_m, tiles_n, per_xcd, smem);
+    wkv_tile<128, 2, 2>(A, W, M, N, K, C, ldc, tiles_m, tiles_n, per_xcd, ad, smem);
 }
 
-template <int BT>
+template <int BT, class D>
 hipError_t run_fast(const uint16_t* a, const uint16_t* w, int64_t M, int N, int K, uint16_t* c,
-                    int64_t ldc, hipStream_t s) {
+                    int64_t ldc, const D& ad, hipStream_t s) {
     const int tiles_m = (int)((M + BT - 1) / BT);
     const int tiles_n = (N + BT - 1) / BT;
     const int total = tiles_m * tiles_n;
     const int per_xcd = (total + N_XCD - 1) / N_XCD;
-    if (BT == 256 && WAVES8) {
-        wkv_fast_256w8<<<dim3(per_xcd * N_XCD), dim3(2 * F_NT), 0, s>>>(a, w, M, N, K, c, ldc,
-                                                                       tiles_m, tiles_n, per_xcd);
+    if constexpr (BT == 256 && WAVES8) {
+        wkv_fast_256w8<D><<<dim3(per_xcd * N_XCD), dim3(2 * F_NT), 0, s>>>(
+            a, w, M, N, K, c, ldc, tiles_m, tiles_n, per_xcd, ad);
     } else {
-        auto kern = BT == 256 ? wkv_fast_256 : wkv_fast_128;
-        kern<<<dim3(per_xcd * N_XCD), dim3(F_NT), 0, s>>>(a, w, M, N, K, c, ldc, tiles_m, tiles_n,
-                                                          per_xcd);
+        auto launch = [&](auto kern) {
+            kern<<<dim3(per_xcd * N_XCD), dim3(F_NT), 0, s>>>(a, w, M, N, K, c, ldc, tiles_m,
+                                                              tiles_n, per_xcd, ad);
+        };
+        if constexpr (BT == 256)
+            launch(wkv_fast_256<D>);
+        else
+            launch(wkv_fast_128<D>);
     }
     return hipGetLastError();
 }
@@ -436,8 +451,9 @@ hipError_t run_fast(const uint16_t* a, const uint16_t* w, int64_t M, int N, int 
 // tiles when those fit in one round (T=4096, N=25600: 1536 big tiles = 6
 // rounds, then 256 small tiles, instead of 7 rounds with the last one a
 // quarter full).
+template <class D>
 hipError_t run_main(const uint16_t* a, const uint16_t* w, int64_t M, int N, int K, uint16_t* kv,
-                    hipStream_t s) {
+                    const D& ad, hipStream_t s) {
     const int cus = cu_count();
     const int tiles_m = (int)((M + 255) / 256);
     const int tiles_n = (N + 255) / 256;
@@ -450,10 +466,22 @@ hipError_t run_main(const uint16_t* a, const uint16_t* w, int64_t M, int N, int 
             if (small <= cus) nb = cand;
         }
     }
-    hipError_t e = run_fast<256>(a, w, M, nb * 256 < N ? nb * 256 : N, K, kv, N, s);
+    hipError_t e = run_fast<256>(a, w, M, nb * 256 < N ? nb * 256 : N, K, kv, N, ad, s);
     if (e != hipSuccess || nb * 256 >= N) return e;
+    D rest = ad;  // the adapters' columns from nb * 256 on
+    if constexpr (D::on) rest.up += (int64_t)nb * 256 * ad.rank;
     return run_fast<128>(a, w + (int64_t)nb * 256 * K, M, N - nb * 256, K, kv + (int64_t)nb * 256, N,
-                         s);
+                         rest, s);
+}
+
+template <class D>
+hipError_t project(const uint16_t* a, const uint16_t* w, int64_t M, int N, int K, uint16_t* kv,
+                   const D& ad, hipStream_t s) {
+    if (M == 0) return hipSuccess;
+    if (M >= 1024 && K % BK == 0 && (int64_t)K * 2 * 256 < (1ll << 31))
+        return run_main(a, w, M, N, K, kv, ad, s);
+    if (M >= 1024) return run<256, 256, 128, 64>(a, w, M, N, K, kv, ad, s);
+    return run<64, 64, 32, 32>(a, w, M, N, K, kv, ad, s);
 }
 
 }  // namespace
@@ -474,11 +502,12 @@ int cu_count() {
 
 hipError_t launch_wkv(const uint16_t* a, const uint16_t* w, int64_t M, int N, int K,
                       uint16_t* kv, hipStream_t s) {
-    if (M == 0) return hipSuccess;
-    if (M >= 1024 && K % BK == 0 && (int64_t)K * 2 * 256 < (1ll << 31))
-        return run_main(a, w, M, N, K, kv, s);
-    if (M >= 1024) return run<256, 256, 128, 64>(a, w, M, N, K, kv, s);
-    return run<64, 64, 32, 32>(a, w, M, N, K, kv, s);
+    return project(a, w, M, N, K, kv, NoAdapters{}, s);
+}
+
+hipError_t launch_wkv_added(const uint16_t* a, const uint16_t* w, int64_t M, int N, int K,
+                            const AddAdapters& ad, uint16_t* kv, hipStream_t s) {
+    return project(a, w, M, N, K, kv, ad, s);
 }
 
 }  // namespace engram

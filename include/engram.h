@@ -45,6 +45,9 @@ typedef enum engram_status {
 #define ENGRAM_ERRBIT_TOKEN 0x1u  /* a token id outside [0, vocab) (used as pad) */
 #define ENGRAM_ERRBIT_HASH  0x2u  /* a computed hash id outside [0, num_embeddings) */
 #define ENGRAM_ERRBIT_ROW   0x4u  /* gather saw a row id outside [0, num_embeddings) */
+#define ENGRAM_ERRBIT_ADAPTER 0x8u  /* an adapter id outside [-1, n) (used as none) */
+#define ENGRAM_ERRBIT_LOGIT  0x10u  /* a NaN or +infinity in a live beam's logits or scores */
+#define ENGRAM_ERRBIT_PARENT 0x20u  /* a parent outside [0, W) (its row is left as it was) */
 
 /* Geometry of one Engram layer ([block] constructor: ModelArgs dim, hc_mult,
  * norm_eps; EngramLayout num_embeddings, head_dim, max_ngram_size, n_heads).
@@ -280,6 +283,120 @@ engram_status engram_forward_noalloc(const engram_geometry* g, const engram_hash
                                      int32_t* state, const uint16_t* x, const int32_t* ids,
                                      const uint8_t* mask, int32_t B, int32_t T, uint16_t* out,
                                      float* gate, uint32_t* err, void* stream);
+
+/* ---- Around the layer in serving: adapters, the next product's input, beams.
+ * These calls extend the pages' path; the pages do not describe them. */
+
+/* Low-rank adapters of the wkv projection.  rank % 8 == 0, 8 <= rank <= 128
+ * (smaller ones are padded with zeros); 1 <= n <= 65536. */
+typedef struct engram_adapters {
+    const uint16_t* down;  /* bf16 [n, rank, K] */
+    const uint16_t* up;    /* bf16 [n, N, rank] */
+    const float* scale;    /* fp32 [n], or NULL: 1 for all */
+    int32_t n;
+    int32_t rank;
+} engram_adapters;
+
+/* Stage 3 with each position's own adapter:
+ *   kv[m] = bf16( w a[m] + scale[j] * up[j] (down[j] a[m]) ),  j = adapter_ids[m],
+ * and the projection alone for j = -1; sums in fp32 (down's result enters the
+ * second product as fp32 or as a bf16 pair that holds 16 of its bits), one
+ * rounding to bf16.  A position's output depends on its own adapter alone: a
+ * NaN or an infinity in another one does not reach it.
+ *   a, w, kv as in engram_wkv; adapter_ids int32 [M], in any order;
+ *   scratch  device memory of engram_wkv_adapters_scratch_size bytes,
+ *            256-byte aligned; contents on entry do not matter.
+ * An id outside [-1, n) counts as -1 and sets ENGRAM_ERRBIT_ADAPTER. */
+size_t engram_wkv_adapters_scratch_size(const engram_geometry* g, const engram_adapters* ad,
+                                        int64_t M);
+engram_status engram_wkv_adapters(const engram_geometry* g, const engram_adapters* ad,
+                                  const uint16_t* a, const uint16_t* w,
+                                  const int32_t* adapter_ids, int64_t M, uint16_t* kv,
+                                  void* scratch, size_t scratch_bytes, uint32_t* err,
+                                  void* stream);
+
+/* The forward with adapters: stages 1 and 2, the projection of
+ * engram_wkv_adapters, stage 4.  adapter_ids int32 [B], one for each sequence;
+ * the other arguments as in engram_forward; workspace of
+ * engram_forward_adapted_workspace_size bytes, 256-byte aligned. */
+size_t engram_forward_adapted_workspace_size(const engram_geometry* g, const engram_adapters* ad,
+                                             int64_t n_tok);
+engram_status engram_forward_adapted(const engram_geometry* g, const engram_hash_tables* t,
+                                     const engram_adapters* ad, const uint8_t* table,
+                                     const uint8_t* scales, const uint16_t* w, const uint16_t* q,
+                                     const uint16_t* k, int32_t* state, const uint16_t* x,
+                                     const int32_t* ids, const int32_t* adapter_ids,
+                                     const uint8_t* mask, int32_t B, int32_t T, uint16_t* out,
+                                     float* gate, void* workspace, size_t workspace_bytes,
+                                     uint32_t* err, void* stream);
+
+/* Root-mean-square norm with the residual's addition and an 8-bit output, per
+ * row of dim values (for instance one stream of one position):
+ *   h = x + residual;  total = bf16(h);
+ *   y = h * rsqrt(mean(h^2) + eps) * weight;  codes = e4m3(y / scale),
+ * in fp32, each output rounded once (to nearest even).  The scales:
+ *   ENGRAM_SCALE_E8M0_32   uint8 [rows, ceil(dim/32)]: for each 32 values the
+ *                          smallest code c >= 0 with max |y| <= 448 * 2^(c-127)
+ *                          (the embedding table's format);
+ *   ENGRAM_SCALE_F32_128   fp32 [rows, ceil(dim/128)]: max |y| / 448 of 128 values;
+ *   ENGRAM_SCALE_F32_ROW   fp32 [rows]: max |y| / 448 of the row.
+ * The last group of a row may be short.  A group of zeros has scale code 0 (or
+ * scale 0) and codes 0.  A NaN or an infinity in y has code 0x7F (NaN); the
+ * maximum passes NaN over.
+ *   x bf16 [rows, dim]; residual the same or NULL (h = x); weight bf16 [dim] or
+ *   NULL (1); total bf16 [rows, dim] or NULL, may be x or residual; codes uint8
+ *   [rows, dim].  dim % 8 == 0, 8 <= dim <= 32768.  x, residual, weight and
+ *   total 16-byte aligned, codes 8, fp32 scales 4. */
+#define ENGRAM_SCALE_E8M0_32 0
+#define ENGRAM_SCALE_F32_128 1
+#define ENGRAM_SCALE_F32_ROW 2
+engram_status engram_norm_quant(const uint16_t* x, const uint16_t* residual,
+                                const uint16_t* weight, int64_t rows, int32_t dim, float eps,
+                                int32_t scale_format, uint16_t* total, uint8_t* codes,
+                                void* scales, void* stream);
+
+/* Beam search's selection: per sequence the W best of W * V continuations.
+ *   score(w, v) = scores[w] + logits[w][v] - log sum_v' exp(logits[w][v'])
+ * in order of falling score, equal scores by the lowest w * V + v; compared and
+ * summed in 64 bits, new_scores rounded to fp32.
+ *   logits   bf16 (logits_f32 = 0) or fp32 [B * W] rows of V, ld >= V elements
+ *            apart; rows may start at any element.
+ *   scores   fp32 [B, W]; a beam at -infinity is dead and offers nothing (the
+ *            first step: one live beam a sequence).
+ *   finished uint8 [B, W] or NULL: such a beam offers one continuation, pad_id
+ *            at its score.
+ *   tokens, parents int32, new_scores fp32, new_finished uint8 (or NULL) [B, W]
+ *            out: the token (to feed engram_hash), the beam it continues, the
+ *            score, and whether that beam was finished or the token is eos_id.
+ *            Where fewer than W continuations are offered, the slots behind
+ *            them get pad_id, their own index, -infinity and 0.
+ *            new_scores may be scores, new_finished may be finished.
+ * A logit of -infinity is never chosen.  A beam with a NaN or +infinity among
+ * its logits or as its score offers nothing and sets ENGRAM_ERRBIT_LOGIT; one
+ * whose logits are all -infinity offers nothing.
+ * 1 <= W <= 32, B * W <= 65535, W <= V, 1 <= V <= 2^30, W * V < 2^31,
+ * 0 <= pad_id < V; eos_id -1: none.  scratch: engram_beam_select_scratch_size
+ * bytes, 256-byte aligned; contents on entry do not matter. */
+size_t engram_beam_select_scratch_size(int32_t B, int32_t W, int32_t V);
+engram_status engram_beam_select(const void* logits, int32_t logits_f32, int64_t ld,
+                                 const float* scores, const uint8_t* finished, int32_t B,
+                                 int32_t W, int32_t V, int32_t eos_id, int32_t pad_id,
+                                 int32_t* tokens, int32_t* parents, float* new_scores,
+                                 uint8_t* new_finished, void* scratch, size_t scratch_bytes,
+                                 uint32_t* err, void* stream);
+
+/* The carried states follow the chosen beams, in place:
+ *   state[b][w] = (the state before the call)[b][parents[b][w]].
+ *   states    host array of n_states device pointers, [B, W] rows of row_bytes[i]
+ *             bytes each (engram_hash's state of a layer with B * W sequences:
+ *             (max_ngram_size - 1) * 4); 4-byte aligned, no two overlapping.
+ *   row_bytes host array, multiples of 4, >= 4.
+ *   parents   int32 [B, W]; one outside [0, W) leaves its row as it was and sets
+ *             ENGRAM_ERRBIT_PARENT.
+ * 1 <= n_states <= 32, 1 <= W <= 32, B <= 65535. */
+engram_status engram_beam_reorder(void* const* states, const int64_t* row_bytes,
+                                  int32_t n_states, const int32_t* parents, int32_t B, int32_t W,
+                                  uint32_t* err, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,159 @@
+"""engram_norm_quant against the formula in 64 bits.
+
+h = x + r is formed in fp32 and total is its bf16 (both exactly those of
+numpy's fp32 addition).  y in fp32 is off by at most d = (dim / 2 + 8) 2^-23 of
+itself: the sum of squares by dim 2^-24 (all terms positive), halved by the
+square root, the mean, eps, root and the two products by a few steps.  Then:
+  code         |e4m3 * scale - y| <= 2^-4 |y| (1 + ...) + 2^-10 scale + d |y|
+               (half a step of a normal; half the subnormal step 2^-9)
+  e8m0 scale   the smallest power of two with max |y| <= 448 scale, for some
+               max within (1 +- d) of the exact one
+  fp32 scale   max |y| / 448 to d + 2^-23.
+"""
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = ("e8m0_32", "f32_128", "f32_row")
+
+
+@pytest.fixture(scope="module")
+def ge():
+    import gram_memory_layer_amd as ge
+    ge.load()
+    return ge
+
+
+def check(x, r, w, eps, fmt, codes, scales, total):
+    x32 = x.float().cpu().numpy().reshape(-1, x.shape[-1])
+    h32 = x32 if r is None else x32 + r.float().cpu().numpy().reshape(x32.shape)
+    if total is not None:
+        want = torch.from_numpy(h32).to(torch.bfloat16)
+        assert torch.equal(total.cpu().reshape(want.shape).view(torch.int16), want.view(torch.int16))
+    rows, dim = h32.shape
+    h = h32.astype(np.float64)
+    ww = np.ones(dim) if w is None else w.double().cpu().numpy()
+    y = h / np.sqrt((h * h).mean(1, keepdims=True) + eps) * ww
+    d = (dim / 2 + 8) * 2.0 ** -23
+    group = {"e8m0_32": 32, "f32_128": 128, "f32_row": dim}[fmt]
+    ng = -(-dim // group)
+    yp = np.zeros((rows, ng * group))
+    yp[:, :dim] = np.abs(y)
+    top = yp.reshape(rows, ng, group).max(2)
+    s = scales.cpu().reshape(rows, ng)
+    if fmt == "e8m0_32":
+        c = s.numpy().astype(np.int64)
+        scale = np.exp2(c - 127.0)
+        assert (top * (1 - d) <= 448 * scale).all()
+        assert ((c == 0) | (top * (1 + d) > 224 * scale)).all()
+    else:
+        scale = s.double().numpy()
+        assert (np.abs(scale - top / 448) <= (d + 2.0 ** -23) * top / 448 + 2.0 ** -149).all()
+    wide = np.repeat(scale, group, axis=1)[:, :dim]
+    v = codes.cpu().view(torch.float8_e4m3fn).double().numpy().reshape(rows, dim)
+    assert np.isfinite(v).all()
+    off = np.abs(v * wide - y)
+    bound = 2.0 ** -4 * np.abs(y) * (1 + d) + 2.0 ** -10 * wide * (1 + 2.0 ** -20) + d * np.abs(y)
+    bound += 448 * 2.0 ** -150  # a subnormal fp32 scale is off by half its step
+    worst = (off / bound).max()
+    assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows,dim", [(1, 8), (3, 16), (1, 32), (17, 40), (5, 128), (300, 136), (2, 256),
+                                      (9, 1032), (4, 2056), (4, 5120), (33, 5120), (2, 16392), (1, 32768),
+                                      (700, 520)])
+def test_norm_quant(ge, fmt, rows, dim):
+    dev = torch.device("cuda:0")
+    say("norm", fmt, rows, dim)
+    g = torch.Generator(device=dev)
+    g.manual_seed(rows * 7 + dim)
+    r = lambda *s, std=1.0: (torch.randn(s, generator=g, device=dev) * std).to(torch.bfloat16)  # noqa: E731
+    x, res, w = r(rows, dim, std=3.0), r(rows, dim), r(dim, std=0.2) + 1
+    x[:, ::37] *= 50
+    for residual in (None, res):
+        for weight in (None, w):
+            codes, scales, total = ge.engram_norm_quant(x, weight, residual=residual, scale_format=fmt)
+            check(x, residual, weight, 1e-6, fmt, codes, scales, total)
+            assert (total is None) == (residual is None)
+    # any leading shape; bytes behind the last row stay
+    buf = torch.full((rows + 1, dim), 77, dtype=torch.uint8, device=dev)
+    c2, s2, _ = ge.engram_norm_quant(x.view(1, rows, dim), w, residual=res.view(1, rows, dim),
+                                     scale_format=fmt, codes=buf[:rows].view(1, rows, dim))
+    assert torch.equal(c2.view(rows, dim), codes) and torch.equal(s2.reshape(scales.shape), scales)
+    assert (buf[rows] == 77).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_total_may_be_an_input(ge, fmt):
+    dev = torch.device("cuda:0")
+    say("norm in place", fmt)
+    x = torch.randn(50, 1032, device=dev).to(torch.bfloat16)
+    r = torch.randn(50, 1032, device=dev).to(torch.bfloat16)
+    want = ge.engram_norm_quant(x, residual=r, scale_format=fmt)
+    for which in (0, 1):
+        a, b = x.clone(), r.clone()
+        got = ge.engram_norm_quant(a, residual=b, scale_format=fmt, total=(a, b)[which])
+        assert all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(got, want))
+        assert torch.equal((a, b)[1 - which], (x, r)[1 - which])
+    one = x.clone()  # x twice
+    got = ge.engram_norm_quant(one, residual=one, scale_format=fmt, total=one)
+    check(x, x, None, 1e-6, fmt, *got)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_zeros_and_extremes(ge, fmt):
+    dev = torch.device("cuda:0")
+    say("norm extremes", fmt)
+    x = torch.randn(6, 256, device=dev).to(torch.bfloat16)
+    x[0] = 0                       # a row of zeros
+    x[1, :128] = 0                 # groups of zeros
+    x[2] *= 2.0 ** -60             # eps outweighs the mean of squares
+    x[3] = 2.0 ** -133             # subnormals
+    x[4] *= 2.0 ** 55
+    x[5] = 1.0                     # all equal
+    codes, scales, _ = ge.engram_norm_quant(x, scale_format=fmt)
+    check(x, None, None, 1e-6, fmt, codes, scales, None)
+    assert (codes[0] == 0).all() and (scales[0] == 0).all()
+    # without eps a row of zeros is 0 * inf
+    codes, _, _ = ge.engram_norm_quant(x[:1], scale_format=fmt, eps=0.0)
+    assert (codes == 0x7F).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_nan_and_infinity_stay_in_their_row(ge, fmt):
+    dev = torch.device("cuda:0")
+    say("norm NaN", fmt)
+    x = torch.randn(5, 264, device=dev).to(torch.bfloat16)
+    want = ge.engram_norm_quant(x, scale_format=fmt)
+    y = x.clone()
+    y[1, 7] = float("nan")
+    y[3, 200] = float("-inf")
+    codes, scales, _ = ge.engram_norm_quant(y, scale_format=fmt)
+    for row in (0, 2, 4):
+        assert torch.equal(codes[row], want[0][row]) and torch.equal(scales[row], want[1][row])
+    assert (codes[1] == 0x7F).all()
+    rest = torch.arange(264, device=dev) != 200
+    assert int(codes[3, 200]) == 0x7F and ((codes[3, rest] & 0x7F) == 0).all()  # finite / inf = 0
+
+
+def test_refusals(ge):
+    dev = torch.device("cuda:0")
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device=dev)
+    with pytest.raises(TypeError):
+        ge.engram_norm_quant(x.float())
+    with pytest.raises(ValueError):
+        ge.engram_norm_quant(x[:, ::2])
+    with pytest.raises(ValueError):
+        ge.engram_norm_quant(x, residual=x[:2])
+    with pytest.raises(TypeError):
+        ge.engram_norm_quant(x, scales=torch.empty(4, 2, device=dev))
+    with pytest.raises(ge.EngramError) as e:
+        ge.engram_norm_quant(torch.zeros(4, 12, dtype=torch.bfloat16, device=dev))
+    assert e.value.status == 2
+    codes, scales, total = ge.engram_norm_quant(x[:0], residual=x[:0])
+    assert codes.shape == (0, 64) and scales.shape == (0, 2) and total.shape == (0, 64)
