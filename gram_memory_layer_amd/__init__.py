@@ -177,6 +177,10 @@ def _ptr(t):
 
 
 def _dev(t, name, dtype, shape=None, device=None):
+    # what nearly every call passes, in a few comparisons; the rest below says what is wrong
+    if (type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape) and (device is None or t.device == device)):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.device.type != "cuda":
@@ -559,13 +563,21 @@ def engram_forward_noalloc(g: Geometry, tables: dict, table, scales, w, q, k, x,
 
 
 # ------------------------------------------------------------------ around the layer
+# the current stream's handle without a Stream object around it (2 us a call), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(name, fn, dev, *args):
     """Call a C entry on `dev`'s current stream, with `dev` the current device."""
-    if torch.cuda.current_device() == dev.index:
-        _check(name, fn(*args, _stream(dev)))
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            _check(name, fn(*args, _stream(dev)))
+            status = fn(*args, _raw_stream(index))
+    if status != 0:
+        raise EngramError(name, status)
 
 
 class Adapters:
@@ -769,6 +781,20 @@ def engram_beam_select(logits, scores, finished=None, eos_id=-1, pad_id=0, token
     return tokens, parents, new_scores, new_finished
 
 
+_array_types: dict = {}  # ctypes array types (making one takes longer than filling it)
+
+
+def _ptr_array(n):
+    if n not in _array_types:
+        _array_types[n] = (C.c_void_p * n, C.c_int64 * n)
+    return _array_types[n][0]
+
+
+def _size_array(n):
+    _ptr_array(n)
+    return _array_types[n][1]
+
+
 def engram_beam_reorder(states, parents, err=None):
     """state[b][w] = state[b][parents[b][w]] in place for every tensor of the
     list `states` (any dtype, [B*W, ...] or [B, W, ...], contiguous, rows of a
@@ -780,20 +806,21 @@ def engram_beam_reorder(states, parents, err=None):
     if parents.dim() != 2:
         raise ValueError("parents must be [B, W]")
     B, W = parents.shape
-    n = len(states)
-    size = []
+    rows, n = B * W, len(states)
+    ptr, size = [], []
     for st in states:
         _dev(st, "state", st.dtype if isinstance(st, torch.Tensor) else None, None, dev)
-        if not st.dim() or (st.shape[0] != B * W and tuple(st.shape[:2]) != (B, W)):
-            raise ValueError("a state must be [B*W, ...] or [B, W, ...] (got %s)" % (tuple(st.shape),))
-        size.append(st.numel() * st.element_size() // max(B * W, 1))
+        shape = st.shape
+        if not len(shape) or (shape[0] != rows and tuple(shape[:2]) != (B, W)):
+            raise ValueError("a state must be [B*W, ...] or [B, W, ...] (got %s)" % (tuple(shape),))
+        ptr.append(st.data_ptr())
+        size.append(st.nbytes // rows if rows else 0)
     if err is not None:
         _dev(err, "err", torch.int32, (1,), dev)
-    if B * W == 0:
+    if rows == 0:
         return states
-    _launch("engram_beam_reorder", L.engram_beam_reorder, dev,
-            (C.c_void_p * n)(*[st.data_ptr() for st in states]), (C.c_int64 * n)(*size), n,
-            parents.data_ptr(), B, W, _ptr(err))
+    _launch("engram_beam_reorder", L.engram_beam_reorder, dev, _ptr_array(n)(*ptr),
+            _size_array(n)(*size), n, parents.data_ptr(), B, W, _ptr(err))
     return states
 
 

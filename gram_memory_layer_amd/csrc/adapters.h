@@ -2,44 +2,55 @@
 // kernels need to add one to their output tiles.
 //
 //   kv[m][n] = bf16( sum_k a[m][k] w[n][k] + sum_r up[j][n][r] * u[m][r] ),
-//   u[m][r]  = scale[j] * sum_k down[j][r][k] a[m][k],   j = ids[m / seg],
+//   u[m][r]  = scale[j] * sum_k down[j][r][k] a[m][k],   j = ids[(m0 + m) / seg].
 //
-// with u in fp32 (adapters.hip) and one rounding to bf16 at the end.
+// u comes from a kernel of its own (adapters.hip) in fp32 and is kept as a bf16
+// pair, hi = bf16(u) and lo = bf16(u - hi), which leaves 2^-16 of it: the second
+// product then runs on the matrix cores, up . hi + up . lo on top of the
+// projection's fp32 accumulators, and there is one rounding to bf16 at the end.
+//
+// A position's output never touches another adapter's weights, so that a NaN
+// or an infinity in them stays with the requests that use them: where the 32
+// (or 16) positions of an MFMA do not all have the adapter, the product goes to
+// a copy of the accumulators and only the lanes that ask for it take it over.
+// The sum is the same either way, whatever the positions around it ask for.
 #pragma once
 
 #include "tiles.h"
 
 namespace engram {
 
-// No adapters: the projection alone.
+// No adapters: the projection alone, rows in order.
 struct NoAdapters {
     static constexpr bool on = false;
 };
 
-// The second product of the adapters, added to a wave's 32 x 32 MFMA
-// accumulators before they are rounded and stored.
-//
-// u is taken as a bf16 pair (hi = bf16(u), lo = bf16(u - hi)), which leaves
-// 2^-16 of it, so that the product runs on the matrix cores at fp32-like
-// accuracy.  One adapter of the wave's 32 positions at a time: its product is
-// formed for all 32 positions and added to the lanes (one position each) that
-// ask for it, so a position's output never touches another adapter's weights
-// (a NaN or an infinity in them stays with the requests that use them).
 struct AddAdapters {
     static constexpr bool on = true;
-    const uint16_t* up;  // [n][n_out][rank], at this launch's first column
-    const float* u;      // [M][rp]
-    const int32_t* ids;
+    const uint16_t* up;   // [n][n_out][rank], at this launch's first column
+    const uint16_t* u;    // [M][rp / 8][hi, lo][8]
+    const int32_t* ids;   // position m of this launch takes ids[(first + m) / seg]
+    const int32_t* perm;  // [M]: tile row -> position, positions of one adapter
+                          // together (null: in order)
+    int64_t first;
     int n, rank, rp, seg;
     int64_t up_stride;  // n_out * rank
 
     __device__ __forceinline__ int id_of(int64_t m) const {
-        const int j = ids[seg == 1 ? m : m / seg];
+        const int j = ids[seg == 1 ? first + m : (first + m) / seg];
         return j >= 0 && j < n ? j : -1;
     }
+    // position of tile row p < M
+    __device__ __forceinline__ int64_t row(int64_t p) const { return perm ? perm[p] : p; }
 
-    // acc[jt][it]: output columns n0 + 32 jt .. (of N) and positions
-    // m0 + 32 it .. (of M); lane: position m0 + 32 it + lane % 32, columns
+    // u's 8 ranks from r on, as hi or lo
+    __device__ __forceinline__ const uint16_t* pair(int64_t m, int r, int lo) const {
+        return u + (m * rp + r) * 2 + lo * 8;
+    }
+
+    // For the kernels without a free LDS stage: straight from memory.
+    // acc[jt][it]: output columns n0 + 32 jt .. (of N) and rows
+    // m0 + 32 it .. (of M); lane: row m0 + 32 it + lane % 32, columns
     // 8 (v / 4) + 4 (lane / 32) + v % 4
     template <int TI, int TJ>
     __device__ __forceinline__ void add(f32x16 (&acc)[TJ][TI], int64_t m0, int64_t M, int n0, int N,
@@ -47,38 +58,145 @@ struct AddAdapters {
         const int lrow = lane & 31, lhalf = lane >> 5;
 #pragma unroll
         for (int i = 0; i < TI; ++i) {
-            const int64_t m = m0 + i * 32 + lrow;
-            const int mine = m < M ? id_of(m) : -1;
-            const float* um = u + (m < M ? m : M - 1) * rp + 8 * lhalf;
+            const int64_t p = m0 + i * 32 + lrow;
+            const int64_t m = row(p < M ? p : M - 1);
+            const int mine = p < M ? id_of(m) : -1;
             uint64_t todo = __ballot(mine >= 0);
             while (todo) {
                 const int j = __builtin_amdgcn_readlane(mine, __builtin_ctzll(todo));
                 const bool hit = mine == j;
                 todo &= ~__ballot(hit);
                 const uint16_t* upj = up + j * up_stride;
-                f32x16 d[TJ];
 #pragma unroll
-                for (int t = 0; t < TJ; ++t)
-#pragma unroll
-                    for (int v = 0; v < 16; ++v) d[t][v] = 0.0f;
-                for (int r0 = 0; r0 < rp; r0 += 16) {
-                    const float4 f0 = *reinterpret_cast<const float4*>(um + r0);
-                    const float4 f1 = *reinterpret_cast<const float4*>(um + r0 + 4);
-                    const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-                    bf16x8 hi, lo;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        hi[e] = (__bf16)f[e];
-                        const float rest = f[e] - (float)hi[e];
-                        lo[e] = (__bf16)(__builtin_fabsf((float)hi[e]) < INFINITY ? rest : 0.0f);
+                for (int t = 0; t < TJ; ++t) {
+                    const int col = n0 + t * 32 + lrow;
+                    f32x16 d = acc[t][i];
+                    for (int r0 = 0; r0 < rp; r0 += 16) {
+                        const int r = r0 + 8 * lhalf;
+                        const bf16x8 hi = *reinterpret_cast<const bf16x8*>(pair(m, r, 0));
+                        const bf16x8 lo = *reinterpret_cast<const bf16x8*>(pair(m, r, 1));
+                        bf16x8 b = {};
+                        if (col < N && r < rank)
+                            b = *reinterpret_cast<const bf16x8*>(upj + (int64_t)col * rank + r);
+                        d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, hi, d, 0, 0, 0);
+                        d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, lo, d, 0, 0, 0);
                     }
 #pragma unroll
+                    for (int v = 0; v < 16; ++v) acc[t][i][v] = hit ? d[v] : acc[t][i][v];
+                }
+            }
+        }
+    }
+};
+
+// 16-byte slot of logical chunk c in an LDS row of 4 (the pairs of 16 ranks) or 2
+// chunks (an up row's 16 ranks): XORed with the row so that one chunk of
+// consecutive rows is spread over the banks.
+__device__ __forceinline__ int slot_pair(int row, int c) {
+    return c ^ (((row >> 1) & 3) ^ ((row >> 3) & 1));
+}
+__device__ __forceinline__ int slot_up(int row, int c) { return c ^ ((row >> 2) & 1); }
+
+// The adapters of a whole BT x BT tile (rows p0 .. of M, columns n0 .. of N),
+// through LDS: per adapter of the tile's rows and up to 64 ranks, the rows'
+// pairs and the adapter's up rows arrive by DMA in groups of 16 ranks (whole
+// 1 KiB pieces; loaded straight into the fragment layout, every wave fetches 32
+// lines a load), then each wave multiplies as in the projection's own k-steps.
+//   ids[k]: the adapter of row p0 + 64 k + lane (-1: none, or past M)
+//   pos[k]: its position
+// NW waves, the calling one at rows wm * 32 TI, columns wn * 32 TJ; smem
+// (4 groups of BT * 96 bytes) is free, before and after.
+template <int BT, int NW, int TI, int TJ>
+__device__ __forceinline__ void add_tile(const AddAdapters& ad, f32x16 (&acc)[TJ][TI],
+                                         const int (&ids)[BT / 64], const int (&pos)[BT / 64],
+                                         int64_t M, int n0, int N, int wm, int wn, int wave,
+                                         int lane, uint8_t* smem) {
+    constexpr int GROUP = BT * 96, UP = BT * 64;  // bytes of a group; its up rows start at UP
+    constexpr int LU = BT / 16, LB = BT / 32;     // DMA instructions of a group
+    static_assert(LU % NW == 0 && LB % NW == 0, "DMA shares");
+    const int lrow = lane & 31, lhalf = lane >> 5;
+    const __amdgpu_buffer_rsrc_t ru = make_rsrc(ad.u, (uint32_t)(M * ad.rp * 4));
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < BT / 64; ++k) any |= __ballot(ids[k] >= 0) != 0;
+    if (!any) return;  // (every wave holds the same ids)
+    for (int r0 = 0; r0 < ad.rp; r0 += 64) {
+        const int groups = min(4, (ad.rp - r0) / 16);
+#pragma unroll
+        for (int i = 0; i < LU / NW; ++i) {
+            const int seg = (LU / NW) * wave + i;  // 16 rows of 4 chunks
+            const int row = seg * 16 + (lane >> 2);
+            const int c = slot_pair(row, lane & 3);
+            int m = 0;
+#pragma unroll
+            for (int k = 0; k < BT / 64; ++k) {
+                const int x = __shfl(pos[k], row & 63, 64);
+                m = (row >> 6) == k ? x : m;
+            }
+            const uint32_t off = (uint32_t)m * (uint32_t)(ad.rp * 4) + (uint32_t)(r0 * 4 + c * 16);
+            for (int g = 0; g < groups; ++g)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    ru, (lds_void*)(smem + g * GROUP + seg * 1024), 16, off, g * 64, 0, 0);
+        }
+        uint64_t todo[BT / 64];
+#pragma unroll
+        for (int k = 0; k < BT / 64; ++k) todo[k] = __ballot(ids[k] >= 0);
+        for (;;) {
+            int j = -1;
+#pragma unroll
+            for (int k = BT / 64 - 1; k >= 0; --k)
+                if (todo[k]) j = __builtin_amdgcn_readlane(ids[k], __builtin_ctzll(todo[k]));
+            if (j < 0) break;
+            uint64_t has[BT / 64];
+#pragma unroll
+            for (int k = 0; k < BT / 64; ++k) {
+                has[k] = __ballot(ids[k] == j);
+                todo[k] &= ~has[k];
+            }
+            const __amdgpu_buffer_rsrc_t rb =
+                make_rsrc(ad.up + j * ad.up_stride + (int64_t)n0 * ad.rank,
+                          (uint32_t)(min(BT, N - n0) * ad.rank * 2));
+#pragma unroll
+            for (int i = 0; i < LB / NW; ++i) {
+                const int seg = (LB / NW) * wave + i;  // 32 rows of 2 chunks
+                const int row = seg * 32 + (lane >> 1);
+                const int c = slot_up(row, lane & 1);
+                for (int g = 0; g < groups; ++g) {
+                    // (ranks past the last read as zeros)
+                    const int r = r0 + 16 * g + 8 * c;
+                    const uint32_t off =
+                        r < ad.rank ? (uint32_t)(row * ad.rank + r) * 2u : 0xFFFFFFF0u;
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                        rb, (lds_void*)(smem + g * GROUP + UP + seg * 1024), 16, off, 0, 0, 0);
+                }
+            }
+            __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < TI; ++i) {
+                const int first = (wm * TI + i) * 32;  // this wave's 32 rows
+                uint64_t h = 0;
+#pragma unroll
+                for (int k = 0; k < BT / 64; ++k) h = (first >> 6) == k ? has[k] : h;
+                const uint32_t mask = (uint32_t)(h >> (first & 32));
+                if (mask == 0) continue;
+                const bool hit = (mask >> lrow) & 1;
+                const int row = first + lrow;
+                f32x16 d[TJ];
+#pragma unroll
+                for (int t = 0; t < TJ; ++t) d[t] = acc[t][i];
+#pragma unroll 1
+                for (int g = 0; g < groups; ++g) {
+                    const uint8_t* at = smem + g * GROUP;
+                    const bf16x8 hi = *reinterpret_cast<const bf16x8*>(
+                        at + row * 64 + slot_pair(row, 2 * lhalf) * 16);
+                    const bf16x8 lo = *reinterpret_cast<const bf16x8*>(
+                        at + row * 64 + slot_pair(row, 2 * lhalf + 1) * 16);
+#pragma unroll
                     for (int t = 0; t < TJ; ++t) {
-                        const int col = n0 + t * 32 + lrow;
-                        bf16x8 b = {};
-                        if (col < N && r0 + 8 * lhalf < rank)
-                            b = *reinterpret_cast<const bf16x8*>(upj + (int64_t)col * rank + r0 +
-                                                                 8 * lhalf);
+                        const int brow = (wn * TJ + t) * 32 + lrow;
+                        const bf16x8 b = *reinterpret_cast<const bf16x8*>(
+                            at + UP + brow * 32 + slot_up(brow, lhalf) * 16);
                         d[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, hi, d[t], 0, 0, 0);
                         d[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, lo, d[t], 0, 0, 0);
                     }
@@ -86,10 +204,11 @@ struct AddAdapters {
 #pragma unroll
                 for (int t = 0; t < TJ; ++t)
 #pragma unroll
-                    for (int v = 0; v < 16; ++v) acc[t][i][v] += hit ? d[t][v] : 0.0f;
+                    for (int v = 0; v < 16; ++v) acc[t][i][v] = hit ? d[t][v] : acc[t][i][v];
             }
+            __syncthreads();  // the up rows are read (and, behind the last one, all of it)
         }
     }
-};
+}
 
 }  // namespace engram

@@ -14,7 +14,7 @@
 namespace engram {
 namespace {
 
-constexpr int kWaves = 4;  // waves of a workgroup
+constexpr int kWaves = 4;  // waves of a workgroup that takes parts
 
 // LDS written by lanes of this wave is read by others of it afterwards (LDS
 // accesses of a wave are performed in order; this keeps the compiler to it)
@@ -23,33 +23,31 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// exp(x) for x <= 0 in 64 bits, to 3e-11 relative; below -700 it is 0.
-// 2^t = 2^n * 2^f with n the nearest whole number and f in [-1/2, 1/2]; 2^f by
-// its Taylor series in f ln 2 up to the 9th power (the rest is below
-// (ln 2 / 2)^10 / 10! = 7e-12).
+// exp(x) for x <= 0 in 64 bits, to 1e-10 relative; exp_neg(0) is 1, below -700
+// it is 0 or below 1e-304.  2^t = 2^n * 2^f with n the nearest whole number, f
+// in [-1/2, 1/2] and 2^f = 1 + f P(f), P the polynomial that meets
+// (2^f - 1) / f at the seven Chebyshev points.  Adding 1.5 * 2^52 rounds t to n
+// and leaves n in the sum's low word, from where it goes into the exponent.
 __device__ __forceinline__ double exp_neg(double x) {
-    const double t = fmax(x, -700.0) * 1.4426950408889634074;
-    const double n = __builtin_rint(t);
-    const double f = (t - n) * 0.69314718055994530942;
-    double p = 1.0 / 362880;
-    p = __builtin_fma(p, f, 1.0 / 40320);
-    p = __builtin_fma(p, f, 1.0 / 5040);
-    p = __builtin_fma(p, f, 1.0 / 720);
-    p = __builtin_fma(p, f, 1.0 / 120);
-    p = __builtin_fma(p, f, 1.0 / 24);
-    p = __builtin_fma(p, f, 1.0 / 6);
-    p = __builtin_fma(p, f, 0.5);
+    constexpr double kLog2e = 1.4426950408889634074, kRound = 6755399441055744.0;
+    x = fmax(x, -700.0);
+    const double r = __builtin_fma(x, kLog2e, kRound);
+    const double f = __builtin_fma(x, kLog2e, -(r - kRound));
+    double p = 1.5297323742797923e-05;
+    p = __builtin_fma(p, f, 0.00015461444700206743);
+    p = __builtin_fma(p, f, 0.001333350238623972);
+    p = __builtin_fma(p, f, 0.0096180566785199779);
+    p = __builtin_fma(p, f, 0.055504108839095574);
+    p = __builtin_fma(p, f, 0.24022650922288785);
+    p = __builtin_fma(p, f, 0.6931471805599454);
     p = __builtin_fma(p, f, 1.0);
-    p = __builtin_fma(p, f, 1.0);
-    return ldexp(p, (int)n);
+    return __hiloint2double(__double2hiint(p) + (__double2loint(r) << 20), __double2loint(p));
 }
 
 // What one wave finds in its part of a row of logits.
 struct Partials {
-    float* top;    // [parts] the part's largest logit; NaN: a NaN or +inf in it
-    double* sum;   // [parts] sum exp(logit - top)
-    float* value;  // [parts][W] its W largest logits, falling (-inf: none left)
-    int32_t* index;  // [parts][W] their tokens
+    double* sum;  // [parts] sum exp(logit - top)
+    float* top;   // [parts] the part's largest logit; NaN: a NaN or +inf in it
 };
 
 // The W best of a wave's values, key falling, then index rising: lane i < W
@@ -59,50 +57,50 @@ struct Partials {
 //
 // W groups of lanes each have a largest key, and the smallest of these W keys
 // bounds the W-th best from below: usually only a few more than W keys reach
-// it.  They are gathered in LDS (64 places a wave) and ranked by counting.
-// Where more than 64 reach it (long runs of equal keys), W rounds each look
-// for the best key behind the last one.
-template <int E, class Key>
-__device__ __forceinline__ void wave_top(const Key (&key)[E], const int32_t (&idx)[E], int W,
-                                         int group_lanes, int lane, Key* lds_key, int32_t* lds_idx,
-                                         Key* out_key, int32_t* out_idx) {
-    const Key none = -INFINITY;
-    Key t = none;
+// it.  They are gathered in LDS (64 places a wave), one a lane, and ranked by
+// counting.  Where more than 64 reach it (long runs of equal keys), W rounds
+// each look for the best key behind the last one.
+template <int E>
+__device__ __forceinline__ void wave_top(const double (&key)[E], const int32_t (&idx)[E], int W,
+                                         int group_lanes, int lane, double* lds_key,
+                                         int32_t* lds_idx, double* out_key, int32_t* out_idx) {
+    const double none = -INFINITY;
+    double t = none;
 #pragma unroll
     for (int e = 0; e < E; ++e) t = key[e] > t ? key[e] : t;
     for (int o = 1; o < group_lanes; o <<= 1) {
-        const Key x = __shfl_xor(t, o, 64);
+        const double x = __shfl_xor(t, o, 64);
         t = x > t ? x : t;
     }
     for (int o = group_lanes; o < 64; o <<= 1) {
-        const Key x = __shfl_xor(t, o, 64);
+        const double x = __shfl_xor(t, o, 64);
         t = x < t ? x : t;
     }
     int count = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         const uint64_t hit = __ballot(key[e] >= t && key[e] > none);
-        if (hit) {
-            const int at = count + __builtin_popcountll(hit & ((1ull << lane) - 1));
-            if (((hit >> lane) & 1) && at < 64) {
-                lds_key[at] = key[e];
-                lds_idx[at] = idx[e];
-            }
-            count += __builtin_popcountll(hit);
+        const int at = count + __builtin_popcountll(hit & ((1ull << lane) - 1));
+        if (((hit >> lane) & 1) && at < 64) {
+            lds_key[at] = key[e];
+            lds_idx[at] = idx[e];
         }
+        count += __builtin_popcountll(hit);
     }
+    wave_fence();
     if (count <= 64) {
-        wave_fence();
-        const Key k = lane < count ? lds_key[lane] : none;
+        const double k = lane < count ? lds_key[lane] : none;
         const int32_t i = lane < count ? lds_idx[lane] : 0x7FFFFFFF;
+        const int32_t hi = __double2hiint(k), lo = __double2loint(k);
         int rank = 0;
         for (int l = 0; l < count; ++l) {
-            const Key ok = lds_key[l];
-            const int32_t oi = lds_idx[l];
+            const double ok = __hiloint2double(__builtin_amdgcn_readlane(hi, l),
+                                               __builtin_amdgcn_readlane(lo, l));
+            const int32_t oi = __builtin_amdgcn_readlane(i, l);
             rank += (ok > k || (ok == k && oi < i)) ? 1 : 0;
         }
         wave_fence();
-        if (lane < count && rank < 64) {
+        if (lane < count) {
             lds_key[rank] = k;
             lds_idx[rank] = i;
         }
@@ -112,12 +110,12 @@ __device__ __forceinline__ void wave_top(const Key (&key)[E], const int32_t (&id
         wave_fence();
         return;
     }
-    Key last = INFINITY;
+    double last = INFINITY;
     int32_t last_i = -1;
     *out_key = none;
     *out_idx = 0;
     for (int r = 0; r < W; ++r) {
-        Key b = none;
+        double b = none;
         int32_t bi = 0x7FFFFFFF;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -128,7 +126,7 @@ __device__ __forceinline__ void wave_top(const Key (&key)[E], const int32_t (&id
             }
         }
         for (int o = 1; o < 64; o <<= 1) {
-            const Key xb = __shfl_xor(b, o, 64);
+            const double xb = __shfl_xor(b, o, 64);
             const int32_t xi = __shfl_xor(bi, o, 64);
             if (xb > b || (xb == b && xi < bi)) {
                 b = xb;
@@ -145,225 +143,373 @@ __device__ __forceinline__ void wave_top(const Key (&key)[E], const int32_t (&id
     }
 }
 
+// A row of logits in 16-byte pieces.  It may start at any element: pieces are
+// laid out from the 16-byte boundary before it, and a piece that reaches out
+// of the row is read by elements (-inf outside).
 template <class T>
-struct Logit;
-template <>
-struct Logit<float> {
-    static constexpr int VEC = 4;
-    __device__ static float get(const uint4& v, int e) {
-        return __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
+struct Row {
+    static constexpr int VEC = 16 / sizeof(T);
+    const T* src;
+    int before;  // elements between the boundary and the row
+
+    __device__ explicit Row(const T* row)
+        : src(row), before((int)(((uintptr_t)row & 15) / sizeof(T))) {}
+    // the column of piece i's first element
+    __device__ int64_t column(int64_t i) const { return i * VEC - before; }
+    __device__ bool whole(int64_t i, int V) const {
+        return column(i) >= 0 && column(i) + VEC <= V;
     }
-    __device__ static float one(const float* p) { return *p; }
-};
-template <>
-struct Logit<uint16_t> {
-    static constexpr int VEC = 8;
-    __device__ static float get(const uint4& v, int e) {
-        const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
-        return __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16);
+    // in two steps, so that several pieces can be on their way
+    __device__ uint4 fetch(int64_t i, int V) const {
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (whole(i, V)) raw = *reinterpret_cast<const uint4*>(src + column(i));
+        return raw;
     }
-    __device__ static float one(const uint16_t* p) { return bf16_to_f32(*p); }
+    __device__ void unpack(const uint4& raw, int64_t i, int V, float (&x)[VEC]) const {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            if constexpr (sizeof(T) == 4)
+                x[e] = __uint_as_float(w[e]);
+            else
+                x[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+        }
+        if (whole(i, V)) return;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int64_t c = column(i) + e;
+            x[e] = -INFINITY;
+            if (c >= 0 && c < V) {
+                if constexpr (sizeof(T) == 4)
+                    x[e] = src[c];
+                else
+                    x[e] = bf16_to_f32(src[c]);
+            }
+        }
+    }
 };
 
-// One wave a part: E logits a lane, 16-byte pieces of 64 lanes in a row.  A row
-// may start at any element: pieces are laid out from the 16-byte boundary
-// before it, and a piece that reaches out of the row is read by elements.
+// One wave a part: 64 lanes of E logits, E / VEC pieces of 64 lanes.  Each lane
+// sums against its own largest logit; the lanes meet at the end.
 template <class T, int E>
 __global__ void __launch_bounds__(64 * kWaves) beam_part_kernel(
     const T* __restrict__ logits, int64_t ld, const float* __restrict__ cum,
-    const uint8_t* __restrict__ finished, int W, int V, int parts, int group_lanes, Partials out,
+    const uint8_t* __restrict__ finished, int V, int parts, Partials out,
     uint32_t* __restrict__ err) {
-    constexpr int VEC = Logit<T>::VEC, NL = E / VEC;
-    __shared__ float lds_key[kWaves][64];
-    __shared__ int32_t lds_idx[kWaves][64];
+    constexpr int VEC = Row<T>::VEC, NL = E / VEC;
     const int64_t row = blockIdx.y;
     if (finished && finished[row]) return;
     const float c = cum[row];
     if (!(c > -INFINITY && c < INFINITY)) return;  // offers nothing
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int part = blockIdx.x * kWaves + wave;
-    const T* src = logits + row * ld;
-    const int before = (int)(((uintptr_t)src & 15) / sizeof(T));  // elements after the boundary
-    float v[E];
-    int32_t idx[E];
+    const Row<T> r(logits + row * ld);
+    const int64_t first = (int64_t)part * NL * 64 + lane;
+    uint4 raw[NL];
+    float v[NL][VEC];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) raw[i] = r.fetch(first + 64 * i, V);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) r.unpack(raw[i], first + 64 * i, V, v[i]);
+    float m = -INFINITY;
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-        const int64_t e0 = ((int64_t)part * NL + i) * (64 * VEC) + lane * VEC - before;
-        uint4 raw;
-        const bool whole = e0 >= 0 && e0 + VEC <= V;
-        if (whole) raw = *reinterpret_cast<const uint4*>(src + e0);
+    for (int i = 0; i < NL; ++i)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            float x = -INFINITY;
-            if (whole)
-                x = Logit<T>::get(raw, e);
-            else if (e0 + e >= 0 && e0 + e < V)
-                x = Logit<T>::one(src + e0 + e);
-            bad |= !(x < INFINITY);
-            v[i * VEC + e] = x;
-            idx[i * VEC + e] = (int32_t)(e0 + e);
+            bad |= !(v[i][e] < INFINITY);
+            m = fmaxf(m, v[i][e]);
         }
-    }
-    bad = __any(bad);
-    if (bad && lane == 0 && err) atomicOr(err, ENGRAM_ERRBIT_LOGIT);
-    float m = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < E; ++e) m = fmaxf(m, v[e]);
-    for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
     double s = 0.0;
-    if (m > -INFINITY && !bad) {
+    if (m > -INFINITY) {
+        const double md = m;
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            s += v[e] > -INFINITY ? exp_neg((double)v[e] - (double)m) : 0.0;
+        for (int i = 0; i < NL; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s += exp_neg((double)v[i][e] - md);
     }
+    float top = m;
+    for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    if (m > -INFINITY) s *= exp_neg((double)m - (double)top);
     for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
-    const int64_t at = row * parts + part;
+    bad = __any(bad);
     if (lane == 0) {
-        out.top[at] = bad ? __uint_as_float(0x7FC00000u) : m;
-        out.sum[at] = s;
-    }
-    if (bad) return;
-    float k;
-    int32_t i;
-    wave_top<E, float>(v, idx, W, group_lanes, lane, lds_key[wave], lds_idx[wave], &k, &i);
-    if (lane < W) {
-        out.value[at * W + lane] = k;
-        out.index[at * W + lane] = i;
+        out.top[row * parts + part] = bad ? __uint_as_float(0x7FC00000u) : top;
+        out.sum[row * parts + part] = s;
+        if (bad && err) atomicOr(err, ENGRAM_ERRBIT_LOGIT);
     }
 }
 
-// One workgroup a sequence: each beam's log sum, then the W best of all
-// parts' candidates.
+// One workgroup of 16 waves a sequence:
+//  1. a wave a beam: its log sum, and the largest scores of at least W groups
+//     of its parts;
+//  2. the W-th largest of all groups' scores: at least W parts reach it, so
+//     what the selection takes reaches it too (and little else does);
+//  3. the parts that reach it, listed; where a long run of equal scores makes
+//     that more than the list holds, exactly the W best parts instead (ties to
+//     the lowest), in which the selection lies as well;
+//  4. these parts' logits once more: what reaches the bound is gathered and
+//     ranked by counting.
 constexpr int kMaxBeams = 32;
-constexpr int kJoin = 16;  // candidates a lane takes at a time
+constexpr int kJoinWaves = 16;
+constexpr int kParts = 64;  // listed parts
+constexpr int kList = 512;  // gathered candidates
 
-__global__ void __launch_bounds__(64 * kWaves) beam_join_kernel(
-    const float* cum, const uint8_t* finished, int W, int V, int parts, int group_lanes,
-    const Partials in, int32_t eos_id, int32_t pad_id, int32_t* __restrict__ tokens,
-    int32_t* __restrict__ parents, float* new_cum, uint8_t* new_finished,
-    uint32_t* __restrict__ err) {
+template <class T, int E>
+__global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(
+    const T* __restrict__ logits, int64_t ld, const float* cum, const uint8_t* finished, int W,
+    int V, int parts, int group_lanes, const Partials in, int32_t eos_id, int32_t pad_id,
+    int32_t* __restrict__ tokens, int32_t* __restrict__ parents, float* new_cum,
+    uint8_t* new_finished, uint32_t* __restrict__ err) {
+    constexpr int VEC = Row<T>::VEC, NL = E / VEC, NT = 64 * kJoinWaves;
     // score = own + ((logit - top) - low): the difference first, which keeps it
     // whole also where logits are masked by the type's lowest value
     __shared__ double low[kMaxBeams];  // log sum exp(logit - top); NaN: offers nothing
-    __shared__ float top[kMaxBeams];
-    __shared__ float own[kMaxBeams];
+    __shared__ float top[kMaxBeams], own[kMaxBeams];
     __shared__ uint8_t done[kMaxBeams];
-    __shared__ double lds_key[kWaves][64];
-    __shared__ int32_t lds_idx[kWaves][64];
-    __shared__ double win_key[kWaves][kMaxBeams];
-    __shared__ int32_t win_idx[kWaves][kMaxBeams];
+    __shared__ double group_key[kJoinWaves * kMaxBeams], list_key[kList];
+    __shared__ double win_key[kJoinWaves];
+    __shared__ int32_t list_idx[kList], win_idx[kJoinWaves];
+    __shared__ int32_t listed[kParts];  // parts as beam * parts + part
+    __shared__ double reach;
+    __shared__ int part_count, count;
     const int64_t b = blockIdx.x;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const double none = -INFINITY;
-    for (int w = wave; w < W; w += kWaves) {
-        const int64_t row = b * W + w;
-        const float c = cum[row];
-        const bool fin = finished && finished[row];
-        double lo = __longlong_as_double(0x7FF8000000000000ll);
-        float m = -INFINITY;
+    const float* tops = in.top + b * W * parts;
+    const double* sums = in.sum + b * W * parts;
+    if (tid == 0) count = part_count = 0;
+    auto score_of = [](float c, float m, double lo, float x) {
+        return (double)c + (((double)x - (double)m) - lo);
+    };
+    auto score = [&](int w, float x) { return score_of(own[w], top[w], low[w], x); };
+
+    double group = none;  // the largest score of this lane's group of parts
+    for (int w = wave; w < W; w += kJoinWaves) {
+        const float c = cum[b * W + w];
+        const bool fin = finished && finished[b * W + w];
         const bool live = c > -INFINITY && c < INFINITY;
-        if (!live && !(c == -INFINITY) && lane == 0 && err) atomicOr(err, ENGRAM_ERRBIT_LOGIT);
+        double lo = __longlong_as_double(0x7FF8000000000000ll);
+        float all = -INFINITY;
         if (live && !fin) {
+            double s = 0.0;
+            float m = -INFINITY;
             bool bad = false;
-            for (int p = lane; p < parts; p += 64) {
-                const float t = in.top[row * parts + p];
-                bad |= t != t;
-                m = fmaxf(m, t);
-            }
-            for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x, 64));
-            if (!__any(bad) && m > -INFINITY) {
-                double s = 0.0;
-                for (int p = lane; p < parts; p += 64) {
-                    const float t = in.top[row * parts + p];
-                    if (t > -INFINITY) s += in.sum[row * parts + p] * exp_neg((double)t - (double)m);
+            for (int p0 = lane; p0 < parts; p0 += 64 * 4) {
+                float t[4];
+                double x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int p = p0 + 64 * i;
+                    t[i] = p < parts ? tops[w * parts + p] : -INFINITY;
+                    x[i] = p < parts ? sums[w * parts + p] : 0.0;
                 }
-                for (int x = 1; x < 64; x <<= 1) s += __shfl_xor(s, x, 64);
+                float nm = m;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    bad |= t[i] != t[i];
+                    nm = fmaxf(nm, t[i]);
+                }
+                if (m > -INFINITY) s *= exp_neg((double)m - (double)nm);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (t[i] > -INFINITY) s += x[i] * exp_neg((double)t[i] - (double)nm);
+                m = nm;
+            }
+            all = m;
+            for (int o = 1; o < 64; o <<= 1) all = fmaxf(all, __shfl_xor(all, o, 64));
+            if (m > -INFINITY) s *= exp_neg((double)m - (double)all);
+            for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
+            if (!__any(bad) && all > -INFINITY) {
                 lo = log(s);
+                if (m > -INFINITY) group = fmax(group, score_of(c, all, lo, m));
             }
         }
         if (lane == 0) {
             low[w] = lo;
-            top[w] = m;
+            top[w] = all;
             own[w] = c;
             done[w] = fin;
+            if (!live && c != -INFINITY && err) atomicOr(err, ENGRAM_ERRBIT_LOGIT);
         }
     }
+    for (int o = 1; o < group_lanes; o <<= 1) group = fmax(group, __shfl_xor(group, o, 64));
+    const int waves = W < kJoinWaves ? W : kJoinWaves;
+    const int groups = waves * (64 / group_lanes);
+    if (lane % group_lanes == 0 && wave < waves)
+        group_key[wave * (64 / group_lanes) + lane / group_lanes] = group;
     __syncthreads();
-
-    // each wave keeps its W best so far in its lanes and takes kJoin more
-    // candidates a lane with them
-    double best = none;
-    int32_t best_i = 0;
-    const uint32_t per_beam = (uint32_t)parts * W, total = per_beam * W;  // [beam][part][W]
-    const float* values = in.value + b * total;
-    const int32_t* indices = in.index + b * total;
-    for (uint32_t c0 = wave * 64 * kJoin; c0 < total; c0 += kWaves * 64 * kJoin) {
-        double key[kJoin + 1];
-        int32_t idx[kJoin + 1];
-#pragma unroll
-        for (int e = 0; e < kJoin; ++e) {
-            const uint32_t i = c0 + e * 64 + lane;
-            key[e] = none;
-            idx[e] = 0x7FFFFFFF - e * 64 - lane;
-            if (i < total) {
-                const int w = (int)(i / per_beam);
-                const double lo = low[w];
-                if (lo == lo) {
-                    const float x = values[i];
-                    if (x > -INFINITY) {
-                        key[e] = (double)own[w] + (((double)x - (double)top[w]) - lo);
-                        idx[e] = w * V + indices[i];
-                    }
-                }
+    if (tid < groups) {
+        const double k = group_key[tid];
+        int rank = 0;
+        for (int l = 0; l < groups; ++l) {
+            const double x = group_key[l];
+            rank += (x > k || (x == k && l < tid)) ? 1 : 0;
+        }
+        if (rank == W - 1) reach = k;  // -inf: fewer than W parts
+    }
+    __syncthreads();
+    const double t = reach;
+    for (int w = wave; w < W; w += kJoinWaves) {
+        if (low[w] != low[w]) continue;
+        for (int p = lane; p < parts; p += 64) {
+            const float x = tops[w * parts + p];
+            if (x > -INFINITY && score(w, x) >= t) {
+                const int at = atomicAdd(&part_count, 1);
+                if (at < kParts) listed[at] = w * parts + p;
             }
         }
-        key[kJoin] = best;
-        idx[kJoin] = best > none ? best_i : 0x7FFFFFFF - kJoin * 64 - lane;
-        if (lane >= W) key[kJoin] = none;
-        wave_top<kJoin + 1, double>(key, idx, W, group_lanes, lane, lds_key[wave], lds_idx[wave],
-                                    &best, &best_i);
-    }
-    if (lane < W) {
-        win_key[wave][lane] = best;
-        win_idx[wave][lane] = best_i;
     }
     __syncthreads();
-    if (wave != 0) return;
-    // the waves' winners and the finished beams' one candidate each
-    double key[3];
-    int32_t idx[3];
+    int n_listed = part_count;
+    if (n_listed > kParts) {
+        __syncthreads();  // everyone has seen the count
+        if (wave == 0) {
+            // the wave keeps its best so far in its lanes and takes four more a
+            // lane with them
+            constexpr int kTake = 4;
+            double best = none;
+            int32_t best_i = 0;
+            for (int c0 = 0; c0 < W * parts; c0 += 64 * kTake) {
+                double key[kTake + 1];
+                int32_t idx[kTake + 1];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int i = e * 64 + lane;  // [wave][W]
-        key[e] = none;
-        idx[e] = 0;
-        if (i < kWaves * W) {
-            key[e] = win_key[i / W][i % W];
-            idx[e] = win_idx[i / W][i % W];
+                for (int e = 0; e < kTake; ++e) {
+                    idx[e] = c0 + e * 64 + lane;
+                    key[e] = none;
+                    if (idx[e] < W * parts) {
+                        const float x = tops[idx[e]];
+                        const int w = idx[e] / parts;
+                        if (low[w] == low[w] && x > -INFINITY) key[e] = score(w, x);
+                    }
+                }
+                key[kTake] = lane < W ? best : none;
+                idx[kTake] = best_i;
+                wave_top<kTake + 1>(key, idx, W, group_lanes, lane, list_key, list_idx, &best,
+                                    &best_i);
+            }
+            if (lane < W) listed[lane] = best_i;  // (more than W parts reach the bound)
         }
+        n_listed = W;
+        __syncthreads();
     }
-    key[2] = none;
-    idx[2] = 0;
-    if (lane < W && done[lane] && own[lane] > -INFINITY && own[lane] < INFINITY) {
-        key[2] = own[lane];
-        idx[2] = lane * V + pad_id;
-    }
-    wave_top<3, double>(key, idx, W, group_lanes, lane, lds_key[0], lds_idx[0], &best, &best_i);
-    if (lane < W) {
-        const int64_t row = b * W + lane;
-        const bool some = best > none;
-        const int parent = some ? best_i / V : lane;
-        const int token = some ? best_i % V : pad_id;
+
+    // the listed parts' logits that may reach the bound: f(score, beam * V + token)
+    auto scan = [&](auto f) {
+        constexpr int AT = 4;  // pieces on their way
+        for (int i0 = 0; i0 < n_listed * NL * 64; i0 += NT * AT) {
+            uint4 raw[AT];
+            int w[AT];
+            int64_t piece[AT];
+#pragma unroll
+            for (int a = 0; a < AT; ++a) {
+                const int i = i0 + a * NT + tid, q = i / (NL * 64);
+                const int at = q < n_listed ? listed[q] : -1;
+                w[a] = at < 0 ? -1 : at / parts;
+                piece[a] = (int64_t)(at - w[a] * parts) * (NL * 64) + i % (NL * 64);
+                if (at >= 0) raw[a] = Row<T>(logits + (b * W + w[a]) * ld).fetch(piece[a], V);
+            }
+#pragma unroll
+            for (int a = 0; a < AT; ++a) {
+                if (w[a] < 0) continue;
+                const Row<T> r(logits + (b * W + w[a]) * ld);
+                float x[VEC];
+                r.unpack(raw[a], piece[a], V, x);
+                const int base = w[a] * V + (int)r.column(piece[a]);
+                const float c = own[w[a]], m = top[w[a]];
+                const double lo = low[w[a]];
+                float most = x[0];
+#pragma unroll
+                for (int e = 1; e < VEC; ++e) most = fmaxf(most, x[e]);
+                if (!(most > -INFINITY) || score_of(c, m, lo, most) < t) continue;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (x[e] > -INFINITY) f(score_of(c, m, lo, x[e]), base + e);
+            }
+        }
+        if (tid < W && done[tid] && own[tid] > -INFINITY && own[tid] < INFINITY)
+            f((double)own[tid], tid * V + pad_id);  // a finished beam's one candidate
+    };
+    auto emit = [&](int slot, double key, int32_t i) {
+        const int parent = i / V, token = i - parent * V;
+        const int64_t row = b * W + slot;
         tokens[row] = token;
         parents[row] = parent;
-        new_cum[row] = (float)best;
-        if (new_finished) new_finished[row] = some && (done[parent] || token == eos_id);
+        new_cum[row] = (float)key;
+        if (new_finished) new_finished[row] = done[parent] || token == eos_id;
+    };
+    scan([&](double key, int32_t i) {
+        if (key >= t) {
+            const int at = atomicAdd(&count, 1);
+            if (at < kList) {
+                list_key[at] = key;
+                list_idx[at] = i;
+            }
+        }
+    });
+    __syncthreads();
+    int found = count;
+    if (found <= kList) {
+        // (the list's order is not the same on every run; the ranks are)
+        for (int j = tid; j < found; j += NT) {
+            const double k = list_key[j];
+            const int32_t i = list_idx[j];
+            int rank = 0;
+            for (int l = 0; l < found; ++l)
+                rank += (list_key[l] > k || (list_key[l] == k && list_idx[l] < i)) ? 1 : 0;
+            if (rank < W) emit(rank, k, i);
+        }
+    } else {
+        // long runs of equal scores: W rounds, each for the best behind the last
+        double last = INFINITY;
+        int32_t last_i = -1;
+        found = W;
+        for (int r = 0; r < W; ++r) {
+            double k = none;
+            int32_t ki = 0x7FFFFFFF;
+            scan([&](double key, int32_t i) {
+                if ((key < last || (key == last && i > last_i)) && (key > k || (key == k && i < ki))) {
+                    k = key;
+                    ki = i;
+                }
+            });
+            for (int o = 1; o < 64; o <<= 1) {
+                const double xk = __shfl_xor(k, o, 64);
+                const int32_t xi = __shfl_xor(ki, o, 64);
+                if (xk > k || (xk == k && xi < ki)) {
+                    k = xk;
+                    ki = xi;
+                }
+            }
+            __syncthreads();  // the last round's winners are read
+            if (lane == 0) {
+                win_key[wave] = k;
+                win_idx[wave] = ki;
+            }
+            __syncthreads();
+            k = none;
+            ki = 0x7FFFFFFF;
+            for (int x = 0; x < kJoinWaves; ++x)
+                if (win_key[x] > k || (win_key[x] == k && win_idx[x] < ki)) {
+                    k = win_key[x];
+                    ki = win_idx[x];
+                }
+            if (tid == 0) emit(r, k, ki);
+            last = k;
+            last_i = ki;
+        }
+    }
+    if (tid >= found && tid < W) {  // fewer than W are offered
+        const int64_t row = b * W + tid;
+        tokens[row] = pad_id;
+        parents[row] = tid;
+        new_cum[row] = -INFINITY;
+        if (new_finished) new_finished[row] = 0;
     }
 }
 
 // Elements a lane holds (a part is 64 of these), by the rows there are: many
-// rows fill the machine with long parts (fewer candidates to join), few rows
+// rows fill the machine with long parts (fewer partial sums to join), few rows
 // are cut short so that one row spreads over many compute units.
 int elements_of(int64_t rows, int V) {
     return rows * ((V + 8191) / 8192) >= 1024 ? 32 : 8;
@@ -384,25 +530,19 @@ int group_lanes_of(int W) {
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-Partials carve(int64_t rows, int W, int parts, void* scratch) {
-    Partials p;
-    char* at = (char*)scratch;
-    const size_t n = (size_t)rows * parts;
-    p.sum = (double*)at;
-    at += up256(n * sizeof(double));
-    p.top = (float*)at;
-    at += up256(n * sizeof(float));
-    p.value = (float*)at;
-    at += up256(n * W * sizeof(float));
-    p.index = (int32_t*)at;
-    return p;
-}
-
 template <class T, int E>
-void run_part(const T* logits, int64_t ld, const float* cum, const uint8_t* finished, int64_t rows,
-              int W, int V, int parts, const Partials& p, uint32_t* err, hipStream_t s) {
-    beam_part_kernel<T, E><<<dim3(parts / kWaves, (uint32_t)rows), dim3(64 * kWaves), 0, s>>>(
-        logits, ld, cum, finished, W, V, parts, group_lanes_of(W), p, err);
+hipError_t run_select(const T* logits, int64_t ld, const float* cum, const uint8_t* finished,
+                      int64_t B, int W, int V, int parts, const Partials& p, int32_t eos_id,
+                      int32_t pad_id, int32_t* tokens, int32_t* parents, float* new_cum,
+                      uint8_t* new_finished, uint32_t* err, hipStream_t s) {
+    beam_part_kernel<T, E><<<dim3(parts / kWaves, (uint32_t)(B * W)), dim3(64 * kWaves), 0, s>>>(
+        logits, ld, cum, finished, V, parts, p, err);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    beam_join_kernel<T, E><<<dim3((uint32_t)B), dim3(64 * kJoinWaves), 0, s>>>(
+        logits, ld, cum, finished, W, V, parts, group_lanes_of(W), p, eos_id, pad_id, tokens,
+        parents, new_cum, new_finished, err);
+    return hipGetLastError();
 }
 
 // ---------------------------------------------------------------- reordering
@@ -500,7 +640,7 @@ hipError_t run_reorder(ReorderArgs& a, const int32_t* parents, int64_t B, int W,
 
 size_t beam_scratch_bytes(int64_t rows, int W, int V) {
     const size_t n = (size_t)rows * parts_of(rows, V);
-    return up256(n * sizeof(double)) + up256(n * sizeof(float)) + 2 * up256(n * W * sizeof(float));
+    return up256(n * sizeof(double)) + up256(n * sizeof(float));
 }
 
 hipError_t launch_beam_select(const void* logits, bool f32, int64_t ld, const float* cum,
@@ -511,20 +651,15 @@ hipError_t launch_beam_select(const void* logits, bool f32, int64_t ld, const fl
     const int64_t rows = B * W;
     const int parts = parts_of(rows, V);
     const bool wide = elements_of(rows, V) == 32;
-    const Partials p = carve(rows, W, parts, scratch);
-    if (f32) {
-        auto f = wide ? run_part<float, 32> : run_part<float, 8>;
-        f((const float*)logits, ld, cum, finished, rows, W, V, parts, p, err, s);
-    } else {
-        auto f = wide ? run_part<uint16_t, 32> : run_part<uint16_t, 8>;
-        f((const uint16_t*)logits, ld, cum, finished, rows, W, V, parts, p, err, s);
-    }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    beam_join_kernel<<<dim3((uint32_t)B), dim3(64 * kWaves), 0, s>>>(
-        cum, finished, W, V, parts, group_lanes_of(W), p, eos_id, pad_id, tokens, parents, new_cum,
-        new_finished, err);
-    return hipGetLastError();
+    Partials p;
+    p.sum = (double*)scratch;
+    p.top = (float*)((char*)scratch + up256((size_t)rows * parts * sizeof(double)));
+    auto go = [&](auto run, auto* x) {
+        return run(x, ld, cum, finished, B, W, V, parts, p, eos_id, pad_id, tokens, parents,
+                   new_cum, new_finished, err, s);
+    };
+    if (f32) return go(wide ? run_select<float, 32> : run_select<float, 8>, (const float*)logits);
+    return go(wide ? run_select<uint16_t, 32> : run_select<uint16_t, 8>, (const uint16_t*)logits);
 }
 
 hipError_t launch_beam_reorder(void* const* states, const int64_t* row_bytes, int n,

@@ -68,7 +68,9 @@ wkv_kernel(const uint16_t* __restrict__ A, const uint16_t* __restrict__ W, int64
     for (int i = 0; i < A_LD; ++i) {
         const int q = tid + i * NT, row = q / CH, ch = q % CH;
         a_ok[i] = (m0 + row) < M;
-        a_src[i] = A + (a_ok[i] ? (m0 + row) : 0) * (int64_t)K + ch * 8;
+        int64_t src = a_ok[i] ? m0 + row : 0;
+        if constexpr (D::on) src = ad.row(src);
+        a_src[i] = A + src * (int64_t)K + ch * 8;
         a_dst[i] = row * CH + swz(row, ch);
         a_ch[i] = ch * 8;
     }
@@ -162,7 +164,9 @@ wkv_kernel(const uint16_t* __restrict__ A, const uint16_t* __restrict__ W, int64
                 if (n >= N) continue;
                 const uint32_t lo = pack_bf16(acc[j][i][4 * g4 + 0], acc[j][i][4 * g4 + 1]);
                 const uint32_t hi = pack_bf16(acc[j][i][4 * g4 + 2], acc[j][i][4 * g4 + 3]);
-                *reinterpret_cast<uint2*>(C + m * N + n) = make_uint2(lo, hi);
+                int64_t to = m;
+                if constexpr (D::on) to = ad.row(m);
+                *reinterpret_cast<uint2*>(C + to * N + n) = make_uint2(lo, hi);
             }
         }
     }
@@ -224,7 +228,18 @@ __device__ __forceinline__ void wkv_tile(const uint16_t* __restrict__ A,
 
     const int64_t rows_a = min((int64_t)BM, M - m0);
     const int rows_w = min(BN, N - n0);
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(A + m0 * K, (uint32_t)(rows_a * K * 2));
+    // with adapters the tile's rows may be any positions (M * K * 2 < 2^31)
+    const __amdgpu_buffer_rsrc_t ra = D::on ? make_rsrc(A, (uint32_t)(M * K * 2))
+                                            : make_rsrc(A + m0 * K, (uint32_t)(rows_a * K * 2));
+    int ids[BT / 64], pos[BT / 64];  // of rows m0 + 64 k + lane
+    if constexpr (D::on) {
+#pragma unroll
+        for (int k = 0; k < BT / 64; ++k) {
+            const int64_t p = m0 + 64 * k + lane;
+            pos[k] = (int)ad.row(p < M ? p : M - 1);
+            ids[k] = p < M ? ad.id_of(pos[k]) : -1;
+        }
+    }
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(W + (int64_t)n0 * K, (uint32_t)(rows_w * K * 2));
 
     // load slots: instruction i of this wave fills LDS segment
@@ -235,13 +250,23 @@ __device__ __forceinline__ void wkv_tile(const uint16_t* __restrict__ A,
         const int row = (NW * i + wave) * 8 + (lane >> 3);
         voff[i] = (uint32_t)(row * K * 2 + slot128(row, lane & 7) * 16);
     }
+    uint32_t aoff[NLD];
+#pragma unroll
+    for (int i = 0; i < NLD; ++i) {
+        aoff[i] = voff[i];
+        if constexpr (D::on) {
+            const int row = (NW * i + wave) * 8 + (lane >> 3);
+            const int64_t p = m0 + row < M ? m0 + row : M - 1;  // (rows past M are not stored)
+            aoff[i] = (uint32_t)ad.row(p) * (uint32_t)(K * 2) + (uint32_t)(slot128(row, lane & 7) * 16);
+        }
+    }
     auto issue_loads = [&](int kt, int stage) {
         uint8_t* st = smem + stage * STAGE;
         const int soff = kt * 128;
 #pragma unroll
         for (int i = 0; i < NLD; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                ra, (lds_void*)(st + (NW * i + wave) * 1024), 16, voff[i], soff, 0, 0);
+                ra, (lds_void*)(st + (NW * i + wave) * 1024), 16, aoff[i], soff, 0, 0);
 #pragma unroll
         for (int i = 0; i < NLD; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -358,7 +383,8 @@ __device__ __forceinline__ void wkv_tile(const uint16_t* __restrict__ A,
     for (int kt = 0; kt + 1 < nk; ++kt) k_tile(kt, T{});
     k_tile(nk - 1, F{});
     __syncthreads();  // every wave is done with the operand stages
-    if constexpr (D::on) ad.template add<TI, TJ>(acc, m0 + wm * WM, M, n0 + wn * WN, N, lane);
+    if constexpr (D::on)
+        add_tile<BT, NW, TI, TJ>(ad, acc, ids, pos, M, n0, N, wm, wn, wave, lane, smem);
 
     // ---- epilogue through LDS.  D[n][m]: lane holds m = lane%32 (+32 i) and
     // n = 32 j + 8 (v/4) + 4 (lane/32) + v%4.  Each wave writes its WM x WN
@@ -391,7 +417,9 @@ __device__ __forceinline__ void wkv_tile(const uint16_t* __restrict__ A,
             *reinterpret_cast<const uint4*>(ep + r * RB + ((csub ^ (r & (CHW - 1))) << 4));
         const int64_t m = m0 + wm * WM + r;
         const int n = n0 + wn * WN + csub * 8;
-        if (m < M && n < N) *reinterpret_cast<uint4*>(C + m * ldc + n) = v;
+        int64_t to = m;
+        if constexpr (D::on) to = m < M ? ad.row(m) : 0;
+        if (m < M && n < N) *reinterpret_cast<uint4*>(C + to * ldc + n) = v;
     }
 }
 
@@ -478,6 +506,9 @@ template <class D>
 hipError_t project(const uint16_t* a, const uint16_t* w, int64_t M, int N, int K, uint16_t* kv,
                    const D& ad, hipStream_t s) {
     if (M == 0) return hipSuccess;
+    if constexpr (D::on)
+        if (M < 1024 && K % BK == 0 && (int64_t)K * 2 * 256 < (1ll << 31))
+            return run_fast<128>(a, w, M, N, K, kv, N, ad, s);
     if (M >= 1024 && K % BK == 0 && (int64_t)K * 2 * 256 < (1ll << 31))
         return run_main(a, w, M, N, K, kv, ad, s);
     if (M >= 1024) return run<256, 256, 128, 64>(a, w, M, N, K, kv, ad, s);

@@ -300,8 +300,8 @@ typedef struct engram_adapters {
 /* Stage 3 with each position's own adapter:
  *   kv[m] = bf16( w a[m] + scale[j] * up[j] (down[j] a[m]) ),  j = adapter_ids[m],
  * and the projection alone for j = -1; sums in fp32 (down's result enters the
- * second product as fp32 or as a bf16 pair that holds 16 of its bits), one
- * rounding to bf16.  A position's output depends on its own adapter alone: a
+ * second product as a pair of bf16 values, which hold it to 2^-16), one rounding
+ * to bf16.  A position's output depends on its own adapter alone: a
  * NaN or an infinity in another one does not reach it.
  *   a, w, kv as in engram_wkv; adapter_ids int32 [M], in any order;
  *   scratch  device memory of engram_wkv_adapters_scratch_size bytes,
