@@ -30,8 +30,10 @@ struct AddAdapters {
     const uint16_t* up;   // [n][n_out][rank], at this launch's first column
     const uint16_t* u;    // [M][rp / 8][hi, lo][8]
     const int32_t* ids;   // position m of this launch takes ids[(first + m) / seg]
-    const int32_t* perm;  // [M]: tile row -> position, positions of one adapter
-                          // together (null: in order)
+    // [M up to a multiple of 256] (position, adapter or -1) of each tile row,
+    // positions of one adapter together; rows behind the last one hold
+    // (M - 1, -1).  Null: positions in order.
+    const int2* tile;
     int64_t first;
     int n, rank, rp, seg;
     int64_t up_stride;  // n_out * rank
@@ -40,27 +42,29 @@ struct AddAdapters {
         const int j = ids[seg == 1 ? first + m : (first + m) / seg];
         return j >= 0 && j < n ? j : -1;
     }
-    // position of tile row p < M
-    __device__ __forceinline__ int64_t row(int64_t p) const { return perm ? perm[p] : p; }
-
+    // whether position m's id is one that is neither an adapter nor -1
+    __device__ __forceinline__ bool bad(int64_t m) const {
+        const int j = ids[seg == 1 ? first + m : (first + m) / seg];
+        return j < -1 || j >= n;
+    }
     // u's 8 ranks from r on, as hi or lo
     __device__ __forceinline__ const uint16_t* pair(int64_t m, int r, int lo) const {
         return u + (m * rp + r) * 2 + lo * 8;
     }
 
-    // For the kernels without a free LDS stage: straight from memory.
-    // acc[jt][it]: output columns n0 + 32 jt .. (of N) and rows
-    // m0 + 32 it .. (of M); lane: row m0 + 32 it + lane % 32, columns
+    // For a kernel without free LDS: straight from memory.
+    // acc[jt][it]: output columns n0 + 32 jt .. (of N) and tile rows
+    // m0 + 32 it ..; lane: row m0 + 32 it + lane % 32, columns
     // 8 (v / 4) + 4 (lane / 32) + v % 4
     template <int TI, int TJ>
-    __device__ __forceinline__ void add(f32x16 (&acc)[TJ][TI], int64_t m0, int64_t M, int n0, int N,
+    __device__ __forceinline__ void add(f32x16 (&acc)[TJ][TI], int64_t m0, int n0, int N,
                                         int lane) const {
         const int lrow = lane & 31, lhalf = lane >> 5;
 #pragma unroll
         for (int i = 0; i < TI; ++i) {
-            const int64_t p = m0 + i * 32 + lrow;
-            const int64_t m = row(p < M ? p : M - 1);
-            const int mine = p < M ? id_of(m) : -1;
+            const int2 own = tile[m0 + i * 32 + lrow];
+            const int64_t m = own.x;
+            const int mine = own.y;
             uint64_t todo = __ballot(mine >= 0);
             while (todo) {
                 const int j = __builtin_amdgcn_readlane(mine, __builtin_ctzll(todo));
@@ -102,15 +106,13 @@ __device__ __forceinline__ int slot_up(int row, int c) { return c ^ ((row >> 2) 
 // pairs and the adapter's up rows arrive by DMA in groups of 16 ranks (whole
 // 1 KiB pieces; loaded straight into the fragment layout, every wave fetches 32
 // lines a load), then each wave multiplies as in the projection's own k-steps.
-//   ids[k]: the adapter of row p0 + 64 k + lane (-1: none, or past M)
-//   pos[k]: its position
+//   own[k]: position and adapter of row p0 + 64 k + lane
 // NW waves, the calling one at rows wm * 32 TI, columns wn * 32 TJ; smem
 // (4 groups of BT * 96 bytes) is free, before and after.
 template <int BT, int NW, int TI, int TJ>
 __device__ __forceinline__ void add_tile(const AddAdapters& ad, f32x16 (&acc)[TJ][TI],
-                                         const int (&ids)[BT / 64], const int (&pos)[BT / 64],
-                                         int64_t M, int n0, int N, int wm, int wn, int wave,
-                                         int lane, uint8_t* smem) {
+                                         const int2 (&own)[BT / 64], int64_t M, int n0, int N,
+                                         int wm, int wn, int wave, int lane, uint8_t* smem) {
     constexpr int GROUP = BT * 96, UP = BT * 64;  // bytes of a group; its up rows start at UP
     constexpr int LU = BT / 16, LB = BT / 32;     // DMA instructions of a group
     static_assert(LU % NW == 0 && LB % NW == 0, "DMA shares");
@@ -118,8 +120,8 @@ __device__ __forceinline__ void add_tile(const AddAdapters& ad, f32x16 (&acc)[TJ
     const __amdgpu_buffer_rsrc_t ru = make_rsrc(ad.u, (uint32_t)(M * ad.rp * 4));
     bool any = false;
 #pragma unroll
-    for (int k = 0; k < BT / 64; ++k) any |= __ballot(ids[k] >= 0) != 0;
-    if (!any) return;  // (every wave holds the same ids)
+    for (int k = 0; k < BT / 64; ++k) any |= __ballot(own[k].y >= 0) != 0;
+    if (!any) return;  // (every wave holds the same rows)
     for (int r0 = 0; r0 < ad.rp; r0 += 64) {
         const int groups = min(4, (ad.rp - r0) / 16);
 #pragma unroll
@@ -130,7 +132,7 @@ __device__ __forceinline__ void add_tile(const AddAdapters& ad, f32x16 (&acc)[TJ
             int m = 0;
 #pragma unroll
             for (int k = 0; k < BT / 64; ++k) {
-                const int x = __shfl(pos[k], row & 63, 64);
+                const int x = __shfl(own[k].x, row & 63, 64);
                 m = (row >> 6) == k ? x : m;
             }
             const uint32_t off = (uint32_t)m * (uint32_t)(ad.rp * 4) + (uint32_t)(r0 * 4 + c * 16);
@@ -140,17 +142,17 @@ __device__ __forceinline__ void add_tile(const AddAdapters& ad, f32x16 (&acc)[TJ
         }
         uint64_t todo[BT / 64];
 #pragma unroll
-        for (int k = 0; k < BT / 64; ++k) todo[k] = __ballot(ids[k] >= 0);
+        for (int k = 0; k < BT / 64; ++k) todo[k] = __ballot(own[k].y >= 0);
         for (;;) {
             int j = -1;
 #pragma unroll
             for (int k = BT / 64 - 1; k >= 0; --k)
-                if (todo[k]) j = __builtin_amdgcn_readlane(ids[k], __builtin_ctzll(todo[k]));
+                if (todo[k]) j = __builtin_amdgcn_readlane(own[k].y, __builtin_ctzll(todo[k]));
             if (j < 0) break;
             uint64_t has[BT / 64];
 #pragma unroll
             for (int k = 0; k < BT / 64; ++k) {
-                has[k] = __ballot(ids[k] == j);
+                has[k] = __ballot(own[k].y == j);
                 todo[k] &= ~has[k];
             }
             const __amdgpu_buffer_rsrc_t rb =

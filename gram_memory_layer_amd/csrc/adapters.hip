@@ -8,6 +8,7 @@
 namespace engram {
 namespace {
 
+typedef __attribute__((address_space(1))) const void global_void;
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // u[m][r] = scale[j] * sum_k down[j][r][k] * a[m][k] for the positions m of
@@ -21,69 +22,83 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 // v_mfma_f32_16x16x32_bf16 takes down as A (its row r0 + lane % 16) and the
 // positions as B (lane % 16), 8 consecutive k a lane; both come straight from
 // memory in that order.
-//
-// With perm, one workgroup more writes the order in which the projection's
-// tiles take the positions: those of one adapter together (a counting sort by
-// id mod 1023; within a bucket in any order, on which no output depends), so
-// that a tile meets few adapters however the requests are mixed.
-constexpr int kDownWaves = 8, kBuckets = 1024;
+constexpr int kDownWaves = 8;
 
-__device__ __forceinline__ void order_positions(const AddAdapters& ad, int M, int32_t* perm,
-                                                int* hist) {
-    const int tid = threadIdx.x, nt = blockDim.x;
-    auto bucket = [&](int m) {
-        const int j = ad.id_of(m);
-        return j < 0 ? 0 : 1 + j % (kBuckets - 1);
+// The order in which the projection's tiles (and the first product) take the
+// positions: those of one adapter together, so that a tile meets few adapters
+// however the requests are mixed.  A counting sort by id mod 1023, positions
+// without an adapter first; within a bucket in any order, on which no output
+// depends.  One workgroup.  A wave whose 64 positions are of one bucket (a
+// prompt) counts them at once: 64 additions to one LDS word go one by one.
+constexpr int kBuckets = 1024;
+__global__ void __launch_bounds__(kBuckets) adapter_order_kernel(const AddAdapters ad, int M,
+                                                                 int2* __restrict__ tile,
+                                                                 uint32_t* __restrict__ err) {
+    __shared__ int hist[kBuckets];
+    __shared__ int wave_sum[kBuckets / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    auto adapter = [&](int m) { return m < M ? ad.id_of(m) : -2; };  // -2: no position
+    // the place of a lane's position in its bucket, counted on from hist
+    auto count = [&](int j) {
+        const int bucket = j < 0 ? j + 1 : 1 + j % (kBuckets - 1);
+        const int first = __builtin_amdgcn_readfirstlane(bucket);
+        if (__all(bucket == first)) {
+            int at = 0;
+            if (first >= 0 && lane == 0) at = atomicAdd(&hist[first], 64);
+            return __builtin_amdgcn_readfirstlane(at) + lane;
+        }
+        return bucket >= 0 ? atomicAdd(&hist[bucket], 1) : 0;
     };
-    for (int i = tid; i < kBuckets; i += nt) hist[i] = 0;
+    const int end = (M + 63) / 64 * 64;  // (whole waves count)
+    bool bad = false;
+    hist[tid] = 0;
     __syncthreads();
-    for (int m = tid; m < M; m += nt) atomicAdd(&hist[bucket(m)], 1);
-    __syncthreads();
-    // exclusive sums: two buckets a thread (512 threads), doubling steps
-    const int a = hist[2 * tid], b = hist[2 * tid + 1];
-    int sum = a + b;
-    __syncthreads();
-    hist[tid] = sum;
-    __syncthreads();
-    for (int o = 1; o < kBuckets / 2; o <<= 1) {
-        const int x = tid >= o ? hist[tid - o] : 0;
-        __syncthreads();
-        hist[tid] = sum = sum + x;
-        __syncthreads();
+    for (int m = tid; m < end; m += kBuckets) {
+        const int j = adapter(m);
+        bad |= j == -1 && ad.bad(m);
+        count(j);
     }
+    if (bad && err) atomicOr(err, ENGRAM_ERRBIT_ADAPTER);
     __syncthreads();
-    hist[2 * tid] = sum - a - b;
-    hist[2 * tid + 1] = sum - b;
+    // exclusive sums over the buckets
+    const int own = hist[tid];
+    int sum = own;
+    for (int o = 1; o < 64; o <<= 1) {
+        const int x = __shfl_up(sum, o, 64);
+        if (lane >= o) sum += x;
+    }
+    if (lane == 63) wave_sum[wave] = sum;
     __syncthreads();
-    for (int m = tid; m < M; m += nt) perm[atomicAdd(&hist[bucket(m)], 1)] = m;
+    int before = 0;
+    for (int w = 0; w < wave; ++w) before += wave_sum[w];
+    hist[tid] = before + sum - own;
+    __syncthreads();
+    for (int m = tid; m < end; m += kBuckets) {
+        const int j = adapter(m), at = count(j);
+        if (m < M) tile[at] = make_int2(m, j);
+    }
+    for (int p = M + tid; p < (M + 255) / 256 * 256; p += kBuckets) tile[p] = make_int2(M - 1, -1);
 }
 
 template <int RT>  // rank tiles of 16
 __global__ void __launch_bounds__(64 * kDownWaves) adapter_down_kernel(
     const uint16_t* __restrict__ a, const uint16_t* __restrict__ down,
     const float* __restrict__ scale, const AddAdapters ad, int M, int K,
-    uint16_t* __restrict__ u, int32_t* __restrict__ perm, uint32_t* __restrict__ err) {
-    static_assert(2 * 64 * kDownWaves == kBuckets, "two buckets a thread");
-    __shared__ union {
-        float part[kDownWaves][RT * 16][17];
-        int hist[kBuckets];
-    } sh;
+    uint16_t* __restrict__ u, uint32_t* __restrict__ err) {
+    __shared__ float part[kDownWaves][RT * 16][17];
     const int m0 = blockIdx.x * 16;
-    if (m0 >= M) {
-        if (blockIdx.y == 0) order_positions(ad, M, perm, sh.hist);
-        return;
-    }
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, quad = lane >> 4;
     const int rank = ad.rank, rp = ad.rp;
-    const int m = min(m0 + col, M - 1);
-    int mine = -1;
-    if (m0 + col < M) {
+    int m = min(m0 + col, M - 1), mine = -1;
+    if (ad.tile) {
+        const int2 own = ad.tile[m0 + col];
+        m = own.x;
+        mine = own.y;
+    } else if (m0 + col < M) {
         mine = ad.id_of(m);
-        const int64_t at = ad.first + m;
-        if (mine < 0 && err && blockIdx.y == 0 && tid < 16 &&
-            ad.ids[ad.seg == 1 ? at : at / ad.seg] != -1)
+        if (mine < 0 && err && blockIdx.y == 0 && tid < 16 && ad.bad(m))
             atomicOr(err, ENGRAM_ERRBIT_ADAPTER);
     }
     const int steps = K / 32, per = (steps + kDownWaves - 1) / kDownWaves;
@@ -117,14 +132,14 @@ __global__ void __launch_bounds__(64 * kDownWaves) adapter_down_kernel(
 #pragma unroll
         for (int t = 0; t < RT; ++t)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) sh.part[wave][16 * t + 4 * quad + v][col] = acc[t][v];
+            for (int v = 0; v < 4; ++v) part[wave][16 * t + 4 * quad + v][col] = acc[t][v];
         __syncthreads();
         const float sc = scale ? scale[j] : 1.0f;
         // (mine is the same in every wave and quad: lane % 16 names the position)
         for (int r = tid >> 4; r < rp; r += 4 * kDownWaves) {
             float sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kDownWaves; ++w) sum += sh.part[w][r][col];
+            for (int w = 0; w < kDownWaves; ++w) sum += part[w][r][col];
             const float f = r < rank ? sc * sum : 0.0f;
             const __bf16 hi = (__bf16)f;
             // (an infinite value has no rest)
@@ -141,18 +156,19 @@ __global__ void __launch_bounds__(64 * kDownWaves) adapter_down_kernel(
 
 template <int RT>
 hipError_t run_down(const uint16_t* a, const Adapters& ad, const AddAdapters& add, int M, int K,
-                    uint16_t* u, int32_t* perm, uint32_t* err, hipStream_t s) {
-    const int tiles = (M + 15) / 16 + (perm ? 1 : 0);
-    int ny = ad.n < 16 ? ad.n : 16;
+                    uint16_t* u, uint32_t* err, hipStream_t s) {
+    // positions in order of their adapters meet one or two in 16; others up to 16
+    int ny = add.tile ? 2 : 16;
+    if (ny > ad.n) ny = ad.n;
     if (ny > M) ny = M;
-    adapter_down_kernel<RT><<<dim3(tiles, ny), dim3(64 * kDownWaves), 0, s>>>(
-        a, ad.down, ad.scale, add, M, K, u, perm, err);
+    adapter_down_kernel<RT><<<dim3((M + 15) / 16, ny), dim3(64 * kDownWaves), 0, s>>>(
+        a, ad.down, ad.scale, add, M, K, u, err);
     return hipGetLastError();
 }
 
-// The projection with adapters for a decode batch (M <= 16 MT positions, K a
-// multiple of 64): W is read once and bounds it.  A workgroup takes 64 columns
-// and all positions; its four waves (16 columns each) share the positions' tile
+// The projection with adapters for a decode batch (16 MT positions a workgroup, K
+// a multiple of 64): W is read once and bounds it.  A workgroup takes 64 columns
+// and, up to 64, all positions; its four waves (16 columns each) share the positions' tile
 // in LDS.  Both operands' k-tiles of 64 arrive by DMA in a ring of NS stages,
 // NS - 1 of them on their way, with one barrier a k-tile.  (With the fragments
 // straight from memory, each wave of 32 columns fetching its own quarter of
@@ -169,14 +185,20 @@ template <int MT, int NS>
 __device__ __forceinline__ void adapter_rows(const uint16_t* __restrict__ a,
                                              const uint16_t* __restrict__ w, const AddAdapters& ad,
                                              int M, int N, int K, uint16_t* __restrict__ kv,
+                                             int tiles_m, int tiles_n, int per_xcd,
                                              uint8_t* smem) {
     constexpr int ROWS = 16 * MT, STAGE = (ROWS + 64) * 128;
     constexpr int NA = MT == 4 ? 2 : 1, NLOAD = NA + 2;  // DMA of a wave and k-tile
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, quad = lane >> 4;
-    const int n0 = blockIdx.x * 64;
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a, (uint32_t)(M * K * 2));
+    int mt, nt;
+    if (!tile_of<2>(blockIdx.x, per_xcd, tiles_m, tiles_n, &mt, &nt)) return;
+    const int n0 = nt * 64, m0 = mt * ROWS;
+    const int rows = min(ROWS, M - m0);
+    a += (int64_t)m0 * K;
+    kv += (int64_t)m0 * N;
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a, (uint32_t)(rows * K * 2));
     const __amdgpu_buffer_rsrc_t rw =
         make_rsrc(w + (int64_t)n0 * K, (uint32_t)(min(64, N - n0) * K * 2));
     // instruction i of a wave fills 8 rows of 128 bytes (rows past M or N read
@@ -246,46 +268,69 @@ __device__ __forceinline__ void adapter_rows(const uint16_t* __restrict__ a,
 
     // D[n][m]: lane holds m = 16 t + lane % 16, n = 16 wave + 4 (lane / 16) + v.
     // The second product takes 16 ranks in one v_mfma_f32_16x16x32_bf16: quads 0
-    // and 1 hold u's hi, quads 2 and 3 its lo, and up's ranks twice.
-    const int mine = lane < M ? ad.id_of(lane) : -1;  // of position `lane`
-    const int n = n0 + 16 * wave + col;
+    // and 1 hold u's hi, quads 2 and 3 its lo, and up's ranks twice.  The up rows
+    // of a wave's 16 columns (512 bytes an adapter) come by DMA into its own
+    // quarter of the ring, as many adapters at once as fit (with loads into
+    // registers, eight on their way, 32 adapters of rank 16 cost 15 us at
+    // 64 positions instead of UPCOST).
+    constexpr int PIECES = NS * STAGE / 4 / 1024;  // two adapters each
+    uint8_t* ups = smem + wave * (PIECES * 1024);
+    const int mine = lane < rows ? ad.id_of(m0 + lane) : -1;  // of position m0 + lane
+    const int n = min(n0 + 16 * wave + ((lane & 31) >> 1), N - 1);
+    __syncthreads();  // the ring is read
     for (int r0 = 0; r0 < ad.rp; r0 += 16) {
-        const int r = r0 + 8 * (quad & 1);
         bf16x8 fu[MT];
 #pragma unroll
         for (int t = 0; t < MT; ++t)
             fu[t] = *reinterpret_cast<const bf16x8*>(
-                ad.pair(min(16 * t + col, M - 1), r, quad >> 1));
+                ad.pair(m0 + min(16 * t + col, rows - 1), r0 + 8 * (quad & 1), quad >> 1));
+        // (up's ranks stop at 8 in the last 16 of some: the rest is zeroed below)
+        const int r = r0 + 8 * (lane & 1) < ad.rank ? r0 + 8 * (lane & 1) : r0;
+        const bool past = r0 + 8 * (quad & 1) >= ad.rank;
+        const uint16_t* from = ad.up + (int64_t)n * ad.rank + r;
         uint64_t todo = __ballot(mine >= 0);
         while (todo) {
-            constexpr int AT = 8;  // adapters on their way
-            bf16x8 b[AT];
-            uint64_t has[AT];
+            uint64_t next = todo;
+            for (int y = 0; y < PIECES && next; ++y) {
+                const int j0 = __builtin_amdgcn_readlane(mine, __builtin_ctzll(next));
+                next &= ~__ballot(mine == j0);
+                const int j1 = next ? __builtin_amdgcn_readlane(mine, __builtin_ctzll(next)) : j0;
+                next &= ~__ballot(mine == j1);
+                const uint16_t* src = from + (lane < 32 ? j0 : j1) * ad.up_stride;
+                __builtin_amdgcn_global_load_lds((global_void*)src, (lds_void*)(ups + y * 1024), 16,
+                                                 0, 0);
+            }
+            __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+            asm volatile("" ::: "memory");
+            for (int y = 0; todo != next; y += 4) {
+                bf16x8 b[4];
 #pragma unroll
-            for (int x = 0; x < AT; ++x) {
-                b[x] = bf16x8{};
-                has[x] = 0;
-                if (todo) {
+                for (int x = 0; x < 4; ++x) {
+                    const int at = min(y + x, 2 * PIECES - 1);
+                    b[x] = *reinterpret_cast<const bf16x8*>(ups + at * 512 + col * 32 +
+                                                            (quad & 1) * 16);
+                    if (past) b[x] = bf16x8{};
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if (todo == next) break;
                     const int j = __builtin_amdgcn_readlane(mine, __builtin_ctzll(todo));
-                    has[x] = __ballot(mine == j);
-                    todo &= ~has[x];
-                    if (n < N && r < ad.rank)
-                        b[x] = *reinterpret_cast<const bf16x8*>(ad.up + j * ad.up_stride +
-                                                                (int64_t)n * ad.rank + r);
+                    const uint64_t has = __ballot(mine == j);
+                    todo &= ~has;
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        const uint32_t mask = (uint32_t)(has >> (16 * t)) & 0xFFFFu;
+                        if (mask == 0) continue;
+                        const f32x4 d =
+                            __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[x], fu[t], acc[t], 0, 0, 0);
+                        const bool hit = (mask >> col) & 1;
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) acc[t][v] = hit ? d[v] : acc[t][v];
+                    }
                 }
             }
-#pragma unroll
-            for (int x = 0; x < AT; ++x)
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    const uint32_t mask = (uint32_t)(has[x] >> (16 * t)) & 0xFFFFu;
-                    if (mask == 0) continue;
-                    const f32x4 d =
-                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[x], fu[t], acc[t], 0, 0, 0);
-                    const bool hit = (mask >> col) & 1;
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[t][v] = hit ? d[v] : acc[t][v];
-                }
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this quarter is read
+            asm volatile("" ::: "memory");
         }
     }
 
@@ -301,7 +346,7 @@ __device__ __forceinline__ void adapter_rows(const uint16_t* __restrict__ a,
 #pragma unroll
     for (int i = 0; i < (ROWS * 8 + 255) / 256; ++i) {
         const int at = i * 256 + tid, row = at >> 3, c = at & 7;
-        if (row < M && row < ROWS && n0 + 8 * c < N)
+        if (row < rows && n0 + 8 * c < N)
             *reinterpret_cast<uint4*>(kv + (int64_t)row * N + n0 + 8 * c) =
                 *reinterpret_cast<const uint4*>(smem + row * 128 + ((c ^ (row & 7)) << 4));
     }
@@ -311,21 +356,25 @@ template <int MT, int NS>
 __global__ void __launch_bounds__(256) adapter_rows_kernel(const uint16_t* __restrict__ a,
                                                            const uint16_t* __restrict__ w,
                                                            const AddAdapters ad, int M, int N, int K,
-                                                           uint16_t* __restrict__ kv) {
+                                                           uint16_t* __restrict__ kv, int tiles_m,
+                                                           int tiles_n, int per_xcd) {
     __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * (16 * MT + 64) * 128];
-    adapter_rows<MT, NS>(a, w, ad, M, N, K, kv, smem);
+    adapter_rows<MT, NS>(a, w, ad, M, N, K, kv, tiles_m, tiles_n, per_xcd, smem);
 }
 
 template <int MT, int NS>
 hipError_t run_rows(const uint16_t* a, const uint16_t* w, const AddAdapters& ad, int M, int N,
                     int K, uint16_t* kv, hipStream_t s) {
-    adapter_rows_kernel<MT, NS><<<dim3((N + 63) / 64), dim3(256), 0, s>>>(a, w, ad, M, N, K, kv);
+    const int tiles_m = (M + 16 * MT - 1) / (16 * MT), tiles_n = (N + 63) / 64;
+    const int per_xcd = (tiles_m * tiles_n + N_XCD - 1) / N_XCD;
+    adapter_rows_kernel<MT, NS><<<dim3(per_xcd * N_XCD), dim3(256), 0, s>>>(
+        a, w, ad, M, N, K, kv, tiles_m, tiles_n, per_xcd);
     return hipGetLastError();
 }
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-constexpr int64_t kRowsMax = 64;  // positions of the decode kernel
+constexpr int64_t kRowsMax = 128;  // positions of the decode kernel
 
 // Positions of one launch: the tiles address the positions and the pairs with
 // 32 bits.
@@ -338,7 +387,7 @@ int64_t launch_positions(int K) {
 
 size_t adapters_scratch_bytes(int rank, int64_t M) {
     return up256((size_t)M * ((rank + 15) / 16 * 16) * 2 * sizeof(uint16_t)) +
-           up256((size_t)M * sizeof(int32_t));
+           (size_t)((M + 255) / 256 * 256) * sizeof(int2);
 }
 
 hipError_t launch_wkv_adapters(const uint16_t* a, const uint16_t* w, const Adapters& ad,
@@ -346,18 +395,23 @@ hipError_t launch_wkv_adapters(const uint16_t* a, const uint16_t* w, const Adapt
                                void* scratch, uint32_t* err, hipStream_t s) {
     const int rt = (ad.rank + 15) / 16, rp = 16 * rt;
     uint16_t* u = (uint16_t*)scratch;
-    int32_t* perm = (int32_t*)((char*)scratch + up256((size_t)M * rp * 2 * sizeof(uint16_t)));
+    int2* tile = (int2*)((char*)scratch + up256((size_t)M * rp * 2 * sizeof(uint16_t)));
     const int64_t most = launch_positions(K);
     for (int64_t m0 = 0; m0 < M; m0 += most) {
         const int m = (int)(M - m0 < most ? M - m0 : most);
         const uint16_t* am = a + m0 * K;
         uint16_t *um = u + m0 * rp * 2, *kvm = kv + m0 * N;
         const bool rows = m <= kRowsMax && K % 64 == 0 && (int64_t)K * 2 * 64 < (1ll << 31);
-        int32_t* order = rows ? nullptr : perm + m0;
+        int2* order = rows ? nullptr : tile + m0;
         const AddAdapters add{ad.up, um, ids, order, m0, ad.n, ad.rank, rp, seg,
                               (int64_t)N * ad.rank};
         auto down = rt <= 1 ? run_down<1> : rt <= 2 ? run_down<2> : rt <= 4 ? run_down<4> : run_down<8>;
-        hipError_t e = down(am, ad, add, m, K, um, order, err, s);
+        hipError_t e = hipSuccess;
+        if (order) {
+            adapter_order_kernel<<<dim3(1), dim3(kBuckets), 0, s>>>(add, m, order, err);
+            e = hipGetLastError();
+        }
+        if (e == hipSuccess) e = down(am, ad, add, m, K, um, err, s);
         if (e != hipSuccess) return e;
         if (!rows)
             e = launch_wkv_added(am, w, m, N, K, add, kvm, s);

@@ -69,7 +69,7 @@ wkv_kernel(const uint16_t* __restrict__ A, const uint16_t* __restrict__ W, int64
         const int q = tid + i * NT, row = q / CH, ch = q % CH;
         a_ok[i] = (m0 + row) < M;
         int64_t src = a_ok[i] ? m0 + row : 0;
-        if constexpr (D::on) src = ad.row(src);
+        if constexpr (D::on) src = ad.tile[m0 + row].x;
         a_src[i] = A + src * (int64_t)K + ch * 8;
         a_dst[i] = row * CH + swz(row, ch);
         a_ch[i] = ch * 8;
@@ -149,7 +149,7 @@ wkv_kernel(const uint16_t* __restrict__ A, const uint16_t* __restrict__ W, int64
         __syncthreads();
     }
 
-    if constexpr (D::on) ad.template add<TM, TN>(acc, m0 + wm * WM, M, n0 + wn * WN, N, lane);
+    if constexpr (D::on) ad.template add<TM, TN>(acc, m0 + wm * WM, n0 + wn * WN, N, lane);
 
     // ---- epilogue: D[n][m]; lane holds m = lane%32, n = 8*(v/4) + 4*(lane/32) + v%4
 #pragma unroll
@@ -165,7 +165,7 @@ wkv_kernel(const uint16_t* __restrict__ A, const uint16_t* __restrict__ W, int64
                 const uint32_t lo = pack_bf16(acc[j][i][4 * g4 + 0], acc[j][i][4 * g4 + 1]);
                 const uint32_t hi = pack_bf16(acc[j][i][4 * g4 + 2], acc[j][i][4 * g4 + 3]);
                 int64_t to = m;
-                if constexpr (D::on) to = ad.row(m);
+                if constexpr (D::on) to = ad.tile[m].x;
                 *reinterpret_cast<uint2*>(C + to * N + n) = make_uint2(lo, hi);
             }
         }
@@ -231,15 +231,10 @@ __device__ __forceinline__ void wkv_tile(const uint16_t* __restrict__ A,
     // with adapters the tile's rows may be any positions (M * K * 2 < 2^31)
     const __amdgpu_buffer_rsrc_t ra = D::on ? make_rsrc(A, (uint32_t)(M * K * 2))
                                             : make_rsrc(A + m0 * K, (uint32_t)(rows_a * K * 2));
-    int ids[BT / 64], pos[BT / 64];  // of rows m0 + 64 k + lane
-    if constexpr (D::on) {
+    int2 own[BT / 64];  // position and adapter of rows m0 + 64 k + lane
+    if constexpr (D::on)
 #pragma unroll
-        for (int k = 0; k < BT / 64; ++k) {
-            const int64_t p = m0 + 64 * k + lane;
-            pos[k] = (int)ad.row(p < M ? p : M - 1);
-            ids[k] = p < M ? ad.id_of(pos[k]) : -1;
-        }
-    }
+        for (int k = 0; k < BT / 64; ++k) own[k] = ad.tile[m0 + 64 * k + lane];
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(W + (int64_t)n0 * K, (uint32_t)(rows_w * K * 2));
 
     // load slots: instruction i of this wave fills LDS segment
@@ -256,8 +251,8 @@ __device__ __forceinline__ void wkv_tile(const uint16_t* __restrict__ A,
         aoff[i] = voff[i];
         if constexpr (D::on) {
             const int row = (NW * i + wave) * 8 + (lane >> 3);
-            const int64_t p = m0 + row < M ? m0 + row : M - 1;  // (rows past M are not stored)
-            aoff[i] = (uint32_t)ad.row(p) * (uint32_t)(K * 2) + (uint32_t)(slot128(row, lane & 7) * 16);
+            aoff[i] = (uint32_t)ad.tile[m0 + row].x * (uint32_t)(K * 2) +
+                      (uint32_t)(slot128(row, lane & 7) * 16);
         }
     }
     auto issue_loads = [&](int kt, int stage) {
@@ -384,7 +379,7 @@ __device__ __forceinline__ void wkv_tile(const uint16_t* __restrict__ A,
     k_tile(nk - 1, F{});
     __syncthreads();  // every wave is done with the operand stages
     if constexpr (D::on)
-        add_tile<BT, NW, TI, TJ>(ad, acc, ids, pos, M, n0, N, wm, wn, wave, lane, smem);
+        add_tile<BT, NW, TI, TJ>(ad, acc, own, M, n0, N, wm, wn, wave, lane, smem);
 
     // ---- epilogue through LDS.  D[n][m]: lane holds m = lane%32 (+32 i) and
     // n = 32 j + 8 (v/4) + 4 (lane/32) + v%4.  Each wave writes its WM x WN
@@ -418,7 +413,7 @@ __device__ __forceinline__ void wkv_tile(const uint16_t* __restrict__ A,
         const int64_t m = m0 + wm * WM + r;
         const int n = n0 + wn * WN + csub * 8;
         int64_t to = m;
-        if constexpr (D::on) to = m < M ? ad.row(m) : 0;
+        if constexpr (D::on) to = ad.tile[m].x;
         if (m < M && n < N) *reinterpret_cast<uint4*>(C + to * ldc + n) = v;
     }
 }

@@ -24,9 +24,9 @@ def test_adapters_host_checks():
     lib, g = ge.load(), geom()
     ok = c_adapters()
     size = lambda ad, M: lib.engram_wkv_adapters_scratch_size(C.byref(g), C.byref(ad), M)  # noqa: E731
-    # ranks in whole 16s, a pair of bf16 each, then the positions' order; both in whole 256 bytes
-    assert size(ok, 64) == 64 * 16 * 4 + 256
-    assert size(c_adapters(rank=24), 300) == 300 * 32 * 4 + 1280
+    # ranks in whole 16s, a pair of bf16 each, then 8 bytes for each of the tiles' rows (whole 256s)
+    assert size(ok, 64) == 64 * 16 * 4 + 256 * 8
+    assert size(c_adapters(rank=24), 300) == 300 * 32 * 4 + 512 * 8
     assert size(ok, 0) == 0 and size(ok, -1) == 0
 
     def call(ad=ok, a=FAKE, w=FAKE, ids=FAKE, M=8, kv=FAKE, scratch=FAKE, nbytes=1 << 30):
@@ -54,7 +54,7 @@ def test_forward_adapted_host_checks():
     lib, g, ok = ge.load(), geom(), c_adapters()
     ht = ge.HashTables(FAKE, FAKE, FAKE, FAKE)
     need = lib.engram_forward_adapted_workspace_size(C.byref(g), C.byref(ok), 8)
-    assert need == ge.engram_forward_workspace_size(g, 8) + 8 * 16 * 4 + 256
+    assert need == ge.engram_forward_workspace_size(g, 8) + 8 * 16 * 4 + 256 * 8
     assert lib.engram_forward_adapted_workspace_size(C.byref(g), C.byref(c_adapters(n=0)), 8) == 0
 
     def call(ad=ok, ids=FAKE, aid=FAKE, B=2, T=4, ws=FAKE, nbytes=need):
