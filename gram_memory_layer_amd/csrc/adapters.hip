@@ -3,12 +3,13 @@
 // the shared part).  Two kernels: the first product, u = scale * down . a, in
 // fp32 (here), then the projection with the second product, up . u, added to
 // its accumulators (adapters.h, wkv.hip).
+#include <type_traits>
+
 #include "adapters.h"
 
 namespace engram {
 namespace {
 
-typedef __attribute__((address_space(1))) const void global_void;
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // u[m][r] = scale[j] * sum_k down[j][r][k] * a[m][k] for the positions m of
@@ -118,14 +119,24 @@ __global__ void __launch_bounds__(64 * kDownWaves) adapter_down_kernel(
             acc[t] = f32x4{0, 0, 0, 0};
             dr[t] = dj + (int64_t)min(16 * t + col, rank - 1) * K;
         }
-#pragma unroll 3
-        for (int s = s0; s < s1; ++s) {
-            const bf16x8 fa = *reinterpret_cast<const bf16x8*>(am + 32 * s);
+        // AT k-steps on their way (behind the last: that one again, unused)
+        constexpr int AT = RT <= 4 ? 6 : 3;
+        for (int s = s0; s < s1; s += AT) {
+            bf16x8 fa[AT], fd[AT][RT];
 #pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                const bf16x8 fd = *reinterpret_cast<const bf16x8*>(dr[t] + 32 * s);
-                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fd, fa, acc[t], 0, 0, 0);
+            for (int x = 0; x < AT; ++x) {
+                const int k = 32 * min(s + x, s1 - 1);
+                fa[x] = *reinterpret_cast<const bf16x8*>(am + k);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) fd[x][t] = *reinterpret_cast<const bf16x8*>(dr[t] + k);
             }
+#pragma unroll
+            for (int x = 0; x < AT; ++x)
+                if (s + x < s1)
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fd[x][t], fa[x], acc[t], 0,
+                                                                         0, 0);
         }
         // D[r][m]: lane holds m = lane % 16, r = 4 (lane / 16) + v
         __syncthreads();  // the last adapter's sums are read
@@ -174,6 +185,12 @@ hipError_t run_down(const uint16_t* a, const Adapters& ad, const AddAdapters& ad
 // straight from memory, each wave of 32 columns fetching its own quarter of
 // K, the positions' loads - 16 rows a load, twice W's bytes - bound it: 44 us
 // at 64 positions of 1536 -> 25600 against 19 for the ring.)
+// LDS of a workgroup: the ring, or the up rows (up to 80 KiB less the sums, so
+// that two workgroups fit a compute unit) and the sums behind them
+constexpr int kSumsRow = 68;  // floats of a position's 64 columns
+constexpr int rows_sums(int mt) { return 16 * mt * kSumsRow * 4; }
+constexpr int rows_ups(int mt) { return 81920 - rows_sums(mt); }
+
 template <int LATER>
 __device__ __forceinline__ void arrived() {
     static_assert(LATER >= 0 && LATER < 64, "vmcnt range");
@@ -189,6 +206,8 @@ __device__ __forceinline__ void adapter_rows(const uint16_t* __restrict__ a,
                                              uint8_t* smem) {
     constexpr int ROWS = 16 * MT, STAGE = (ROWS + 64) * 128;
     constexpr int NA = MT == 4 ? 2 : 1, NLOAD = NA + 2;  // DMA of a wave and k-tile
+    constexpr int RING = NS * STAGE, UPS = rows_ups(MT), SROW = kSumsRow;
+    static_assert(rows_sums(MT) <= RING, "the sums fit the ring");
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, quad = lane >> 4;
@@ -207,16 +226,16 @@ __device__ __forceinline__ void adapter_rows(const uint16_t* __restrict__ a,
     int as[NA], ws[2];
     const int r8 = lane >> 3;
 #pragma unroll
-    for (int i = 0; i < NA; ++i) {
-        const int seg = MT == 1 ? wave & 1 : NA * wave + i, row = seg * 8 + r8;
-        ao[i] = (uint32_t)(row * K * 2 + slot128(row, lane & 7) * 16);
-        as[i] = seg * 1024;
-    }
-#pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int seg = 2 * wave + i, row = seg * 8 + r8;
         wo[i] = (uint32_t)(row * K * 2 + slot128(row, lane & 7) * 16);
         ws[i] = ROWS * 128 + seg * 1024;
+    }
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+        const int seg = MT == 1 ? wave & 1 : NA * wave + i, row = seg * 8 + r8;
+        ao[i] = (uint32_t)(row * K * 2 + slot128(row, lane & 7) * 16);
+        as[i] = seg * 1024;
     }
     auto issue = [&](int kt, int stage) {
         uint8_t* st = smem + stage * STAGE;
@@ -229,10 +248,64 @@ __device__ __forceinline__ void adapter_rows(const uint16_t* __restrict__ a,
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + as[i]), 16, ao[i],
                                                      kt * 128, 0, 0);
     };
+    // This lane's position: its pairs (the first 64 ranks) are on their way
+    // before the ring starts.
+    const int lm = lane & (ROWS - 1);
+    bf16x8 hi[8], lo[8];
+    auto load_pairs = [&](int r0) {
+        const uint16_t* from = ad.pair(m0 + min(lm, rows - 1), r0, 0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (r0 + 8 * k < ad.rank) {
+                hi[k] = *reinterpret_cast<const bf16x8*>(from + 16 * k);
+                lo[k] = *reinterpret_cast<const bf16x8*>(from + 16 * k + 8);
+            }
+    };
+    const int own = lm < rows ? ad.id_of(m0 + lm) : -1;
+    load_pairs(0);
     const int nk = K / 64;
 #pragma unroll
     for (int p = 0; p < NS - 1; ++p)
         if (p < nk) issue(p, p);
+
+    // The adapters of this workgroup's positions, each once: lane x holds the
+    // x-th in `list`, and a lane's position (lane mod the positions) has its
+    // adapter as the `which`-th.
+    int list = 0, which = -1, distinct = 0;
+    {
+        uint64_t todo = __ballot(own >= 0);
+        while (todo) {
+            const int j = __builtin_amdgcn_readlane(own, __builtin_ctzll(todo));
+            const bool same = own == j;
+            todo &= ~__ballot(same);
+            which = same ? distinct : which;
+            list = lane == distinct ? j : list;
+            ++distinct;
+        }
+    }
+    // The distinct adapters' up rows of columns n0 + c0 .. and ranks r0 .. (8
+    // `chunks` of them) to `to`, one after the other with 16 bytes between two;
+    // a wave takes every fourth adapter.  (Columns past N read as zeros.)
+    auto load_ups = [&](uint8_t* to, int r0, int chunks, int c0, int nc) {
+        const int pieces = nc * chunks, slab = pieces * 16 + 16;
+        const int inv = 65536 / chunks + 1;  // L / chunks = L * inv >> 16 for L < 512
+        const uint32_t bytes = (uint32_t)(min(nc, N - n0 - c0) * ad.rank * 2);
+        const uint16_t* from = ad.up + (int64_t)(n0 + c0) * ad.rank + r0;
+        for (int i = 0; i < pieces; i += 64) {
+            const int L = i + lane, row = L * inv >> 16, c = L - row * chunks;
+            const uint32_t off = L < pieces ? (uint32_t)(row * ad.rank + c * 8) * 2u : 0xF0000000u;
+            if (L < pieces)
+                for (int x = wave; x < distinct; x += 4) {
+                    const int j = __builtin_amdgcn_readlane(list, x);
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                        make_rsrc(from + j * ad.up_stride, bytes - (uint32_t)(r0 * 2)),
+                        (lds_void*)(to + x * slab + i * 16), 16, off, 0, 0, 0);
+                }
+        }
+    };
+    // few adapters fit the LDS behind the ring: their rows come beside it
+    const bool early = ad.rank <= 64 && distinct * (128 * ad.rank + 16) <= 81920 - RING;
+    if (early) load_ups(smem + RING, 0, ad.rank / 8, 0, 64);
 
     f32x4 acc[MT];
 #pragma unroll
@@ -266,72 +339,75 @@ __device__ __forceinline__ void adapter_rows(const uint16_t* __restrict__ a,
         stage = stage + 1 == NS ? 0 : stage + 1;
     }
 
-    // D[n][m]: lane holds m = 16 t + lane % 16, n = 16 wave + 4 (lane / 16) + v.
-    // The second product takes 16 ranks in one v_mfma_f32_16x16x32_bf16: quads 0
-    // and 1 hold u's hi, quads 2 and 3 its lo, and up's ranks twice.  The up rows
-    // of a wave's 16 columns (512 bytes an adapter) come by DMA into its own
-    // quarter of the ring, as many adapters at once as fit (with loads into
-    // registers, eight on their way, 32 adapters of rank 16 cost 15 us at
-    // 64 positions instead of UPCOST).
-    constexpr int PIECES = NS * STAGE / 4 / 1024;  // two adapters each
-    uint8_t* ups = smem + wave * (PIECES * 1024);
-    const int mine = lane < rows ? ad.id_of(m0 + lane) : -1;  // of position m0 + lane
-    const int n = min(n0 + 16 * wave + ((lane & 31) >> 1), N - 1);
-    __syncthreads();  // the ring is read
-    for (int r0 = 0; r0 < ad.rp; r0 += 16) {
-        bf16x8 fu[MT];
+    // The second product on the vector units: with an adapter for each position
+    // the matrix cores have nothing to share, and going through the adapters one
+    // by one costs 0.4 us each in scalar work (32 adapters of rank 16 at 64
+    // positions: 17 us).  Here a lane takes one position and a few columns,
+    // whatever the other positions have: its pairs are in registers, its
+    // adapter's up rows come from LDS, and v_dot2_f32_bf16 adds two products in
+    // fp32.  The up rows of all distinct adapters arrive by DMA in the ring's
+    // memory, as many of the 64 columns a round as fit (the four waves split
+    // them); 16 bytes between two adapters spread equal rows over the banks.
+    if (distinct) {
+        // [position][SROW]
+        float* sums = reinterpret_cast<float*>(smem + (early ? 0 : UPS));
+        for (int r0 = 0; r0 < ad.rank; r0 += 64) {
+            const int ranks = min(64, ad.rank - r0), chunks = ranks / 8;
+            if (r0) load_pairs(r0);
+            int nc = 64;
+            while (distinct * (nc * chunks * 16 + 16) > UPS) nc >>= 1;
+            const int slab = nc * chunks * 16 + 16;
+            const int per = nc * MT / 16;  // columns a lane
+            const int first = (wave * (4 / MT) + lane / ROWS) * per;
+            for (int c0 = 0; c0 < 64 && n0 + c0 < N; c0 += nc) {
+                __syncthreads();  // the memory is free: the ring, or the round before, is read
+                if (!early) {
+                    load_ups(smem, r0, chunks, c0, nc);
+                    arrived<0>();
+                }
+                const uint8_t* up = smem + (early ? RING : 0) + max(which, 0) * slab +
+                                    first * (chunks * 16);
+                float* to = sums + lm * SROW + c0 + first;
+                auto columns = [&](auto count) {
+                    constexpr int P = decltype(count)::value;
+                    float o[P];
+#pragma unroll
+                    for (int i = 0; i < P; ++i) o[i] = r0 ? to[i] : 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (k >= chunks) break;
+#pragma unroll
+                        for (int i = 0; i < P; ++i) {
+                            const bf16x8 b = *reinterpret_cast<const bf16x8*>(
+                                up + (i * chunks + k) * 16);
+#pragma unroll
+                            for (int e = 0; e < 8; e += 2) {
+                                const bf16x2 bb = {b[e], b[e + 1]};
+                                o[i] = __builtin_amdgcn_fdot2_f32_bf16(
+                                    bb, bf16x2{hi[k][e], hi[k][e + 1]}, o[i], false);
+                                o[i] = __builtin_amdgcn_fdot2_f32_bf16(
+                                    bb, bf16x2{lo[k][e], lo[k][e + 1]}, o[i], false);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < P; ++i) to[i] = which >= 0 ? o[i] : 0.0f;
+                };
+                if constexpr (MT == 4)
+                    if (per == 16) columns(std::integral_constant<int, 16>{});
+                if constexpr (MT >= 2)
+                    if (per == 8) columns(std::integral_constant<int, 8>{});
+                if (per == 4) columns(std::integral_constant<int, 4>{});
+                if (per == 2) columns(std::integral_constant<int, 2>{});
+                if (per == 1) columns(std::integral_constant<int, 1>{});
+            }
+        }
+        __syncthreads();
+        // D[n][m]: lane holds m = 16 t + lane % 16, n = 16 wave + 4 (lane / 16) + v
 #pragma unroll
         for (int t = 0; t < MT; ++t)
-            fu[t] = *reinterpret_cast<const bf16x8*>(
-                ad.pair(m0 + min(16 * t + col, rows - 1), r0 + 8 * (quad & 1), quad >> 1));
-        // (up's ranks stop at 8 in the last 16 of some: the rest is zeroed below)
-        const int r = r0 + 8 * (lane & 1) < ad.rank ? r0 + 8 * (lane & 1) : r0;
-        const bool past = r0 + 8 * (quad & 1) >= ad.rank;
-        const uint16_t* from = ad.up + (int64_t)n * ad.rank + r;
-        uint64_t todo = __ballot(mine >= 0);
-        while (todo) {
-            uint64_t next = todo;
-            for (int y = 0; y < PIECES && next; ++y) {
-                const int j0 = __builtin_amdgcn_readlane(mine, __builtin_ctzll(next));
-                next &= ~__ballot(mine == j0);
-                const int j1 = next ? __builtin_amdgcn_readlane(mine, __builtin_ctzll(next)) : j0;
-                next &= ~__ballot(mine == j1);
-                const uint16_t* src = from + (lane < 32 ? j0 : j1) * ad.up_stride;
-                __builtin_amdgcn_global_load_lds((global_void*)src, (lds_void*)(ups + y * 1024), 16,
-                                                 0, 0);
-            }
-            __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-            asm volatile("" ::: "memory");
-            for (int y = 0; todo != next; y += 4) {
-                bf16x8 b[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int at = min(y + x, 2 * PIECES - 1);
-                    b[x] = *reinterpret_cast<const bf16x8*>(ups + at * 512 + col * 32 +
-                                                            (quad & 1) * 16);
-                    if (past) b[x] = bf16x8{};
-                }
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    if (todo == next) break;
-                    const int j = __builtin_amdgcn_readlane(mine, __builtin_ctzll(todo));
-                    const uint64_t has = __ballot(mine == j);
-                    todo &= ~has;
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        const uint32_t mask = (uint32_t)(has >> (16 * t)) & 0xFFFFu;
-                        if (mask == 0) continue;
-                        const f32x4 d =
-                            __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[x], fu[t], acc[t], 0, 0, 0);
-                        const bool hit = (mask >> col) & 1;
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) acc[t][v] = hit ? d[v] : acc[t][v];
-                    }
-                }
-            }
-            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this quarter is read
-            asm volatile("" ::: "memory");
-        }
+            acc[t] += *reinterpret_cast<const f32x4*>(sums + (16 * t + col) * SROW + 16 * wave +
+                                                      4 * quad);
     }
 
     // rows of 64 columns through LDS, so that a position's 128 bytes go out together
@@ -353,12 +429,13 @@ __device__ __forceinline__ void adapter_rows(const uint16_t* __restrict__ a,
 }
 
 template <int MT, int NS>
-__global__ void __launch_bounds__(256) adapter_rows_kernel(const uint16_t* __restrict__ a,
+__global__ void __launch_bounds__(256, 2) adapter_rows_kernel(const uint16_t* __restrict__ a,
                                                            const uint16_t* __restrict__ w,
                                                            const AddAdapters ad, int M, int N, int K,
                                                            uint16_t* __restrict__ kv, int tiles_m,
                                                            int tiles_n, int per_xcd) {
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * (16 * MT + 64) * 128];
+    static_assert(NS * (16 * MT + 64) * 128 <= 81920, "the ring");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[81920];
     adapter_rows<MT, NS>(a, w, ad, M, N, K, kv, tiles_m, tiles_n, per_xcd, smem);
 }
 
