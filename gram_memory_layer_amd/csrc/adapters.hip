@@ -54,10 +54,16 @@ __global__ void __launch_bounds__(kBuckets) adapter_order_kernel(const AddAdapte
     bool bad = false;
     hist[tid] = 0;
     __syncthreads();
-    for (int m = tid; m < end; m += kBuckets) {
-        const int j = adapter(m);
-        bad |= j == -1 && ad.bad(m);
-        count(j);
+    constexpr int AT = 4;  // positions of a thread on their way
+    for (int m = tid; m < end; m += AT * kBuckets) {
+        int j[AT];
+#pragma unroll
+        for (int x = 0; x < AT; ++x) j[x] = adapter(m + x * kBuckets);
+#pragma unroll
+        for (int x = 0; x < AT; ++x) {
+            bad |= j[x] == -1 && ad.bad(m + x * kBuckets);
+            count(j[x]);
+        }
     }
     if (bad && err) atomicOr(err, ENGRAM_ERRBIT_ADAPTER);
     __syncthreads();
@@ -74,9 +80,15 @@ __global__ void __launch_bounds__(kBuckets) adapter_order_kernel(const AddAdapte
     for (int w = 0; w < wave; ++w) before += wave_sum[w];
     hist[tid] = before + sum - own;
     __syncthreads();
-    for (int m = tid; m < end; m += kBuckets) {
-        const int j = adapter(m), at = count(j);
-        if (m < M) tile[at] = make_int2(m, j);
+    for (int m = tid; m < end; m += AT * kBuckets) {
+        int j[AT];
+#pragma unroll
+        for (int x = 0; x < AT; ++x) j[x] = adapter(m + x * kBuckets);
+#pragma unroll
+        for (int x = 0; x < AT; ++x) {
+            const int at = count(j[x]);
+            if (m + x * kBuckets < M) tile[at] = make_int2(m + x * kBuckets, j[x]);
+        }
     }
     for (int p = M + tid; p < (M + 255) / 256 * 256; p += kBuckets) tile[p] = make_int2(M - 1, -1);
 }
@@ -91,7 +103,8 @@ __global__ void __launch_bounds__(64 * kDownWaves) adapter_down_kernel(
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, quad = lane >> 4;
-    const int rank = ad.rank, rp = ad.rp;
+    // ranks of this workgroup
+    const int first_r = 16 * RT * blockIdx.z, rank = ad.rank, rp = ad.rp;
     int m = min(m0 + col, M - 1), mine = -1;
     if (ad.tile) {
         const int2 own = ad.tile[m0 + col];
@@ -99,7 +112,7 @@ __global__ void __launch_bounds__(64 * kDownWaves) adapter_down_kernel(
         mine = own.y;
     } else if (m0 + col < M) {
         mine = ad.id_of(m);
-        if (mine < 0 && err && blockIdx.y == 0 && tid < 16 && ad.bad(m))
+        if (mine < 0 && err && blockIdx.y == 0 && blockIdx.z == 0 && tid < 16 && ad.bad(m))
             atomicOr(err, ENGRAM_ERRBIT_ADAPTER);
     }
     const int steps = K / 32, per = (steps + kDownWaves - 1) / kDownWaves;
@@ -117,7 +130,7 @@ __global__ void __launch_bounds__(64 * kDownWaves) adapter_down_kernel(
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             acc[t] = f32x4{0, 0, 0, 0};
-            dr[t] = dj + (int64_t)min(16 * t + col, rank - 1) * K;
+            dr[t] = dj + (int64_t)min(first_r + 16 * t + col, rank - 1) * K;
         }
         // AT k-steps on their way (behind the last: that one again, unused)
         constexpr int AT = RT <= 4 ? 6 : 3;
@@ -147,10 +160,11 @@ __global__ void __launch_bounds__(64 * kDownWaves) adapter_down_kernel(
         __syncthreads();
         const float sc = scale ? scale[j] : 1.0f;
         // (mine is the same in every wave and quad: lane % 16 names the position)
-        for (int r = tid >> 4; r < rp; r += 4 * kDownWaves) {
+        for (int l = tid >> 4; l < 16 * RT && first_r + l < rp; l += 4 * kDownWaves) {
+            const int r = first_r + l;
             float sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kDownWaves; ++w) sum += part[w][r][col];
+            for (int w = 0; w < kDownWaves; ++w) sum += part[w][l][col];
             const float f = r < rank ? sc * sum : 0.0f;
             const __bf16 hi = (__bf16)f;
             // (an infinite value has no rest)
@@ -165,16 +179,24 @@ __global__ void __launch_bounds__(64 * kDownWaves) adapter_down_kernel(
     }
 }
 
-template <int RT>
 hipError_t run_down(const uint16_t* a, const Adapters& ad, const AddAdapters& add, int M, int K,
                     uint16_t* u, uint32_t* err, hipStream_t s) {
     // positions in order of their adapters meet one or two in 16; others up to 16
     int ny = add.tile ? 2 : 16;
     if (ny > ad.n) ny = ad.n;
     if (ny > M) ny = M;
-    adapter_down_kernel<RT><<<dim3((M + 15) / 16, ny), dim3(64 * kDownWaves), 0, s>>>(
-        a, ad.down, ad.scale, add, M, K, u, err);
-    return hipGetLastError();
+    const int tiles = (M + 15) / 16, rt = add.rp / 16;
+    auto go = [&](auto kern, int each) {
+        kern<<<dim3(tiles, ny, (rt + each - 1) / each), dim3(64 * kDownWaves), 0, s>>>(
+            a, ad.down, ad.scale, add, M, K, u, err);
+        return hipGetLastError();
+    };
+    // few positions: a workgroup for each 16 ranks (rank 64 at 64 positions: 6.5 us
+    // against 10.6 with all in one); many: the positions are fetched once for 64
+    // (rank 64 at 4096 positions: 11.9 us against 17.3)
+    if (rt == 1 || M <= 1024) return go(adapter_down_kernel<1>, 1);
+    if (rt == 2) return go(adapter_down_kernel<2>, 2);
+    return go(adapter_down_kernel<4>, 4);
 }
 
 // The projection with adapters for a decode batch (16 MT positions a workgroup, K
@@ -482,13 +504,12 @@ hipError_t launch_wkv_adapters(const uint16_t* a, const uint16_t* w, const Adapt
         int2* order = rows ? nullptr : tile + m0;
         const AddAdapters add{ad.up, um, ids, order, m0, ad.n, ad.rank, rp, seg,
                               (int64_t)N * ad.rank};
-        auto down = rt <= 1 ? run_down<1> : rt <= 2 ? run_down<2> : rt <= 4 ? run_down<4> : run_down<8>;
         hipError_t e = hipSuccess;
         if (order) {
             adapter_order_kernel<<<dim3(1), dim3(kBuckets), 0, s>>>(add, m, order, err);
             e = hipGetLastError();
         }
-        if (e == hipSuccess) e = down(am, ad, add, m, K, um, err, s);
+        if (e == hipSuccess) e = run_down(am, ad, add, m, K, um, err, s);
         if (e != hipSuccess) return e;
         if (!rows)
             e = launch_wkv_added(am, w, m, N, K, add, kvm, s);

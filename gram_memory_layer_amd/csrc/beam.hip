@@ -23,14 +23,13 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// exp(x) for x <= 0 in 64 bits, to 1e-10 relative; exp_neg(0) is 1, below -700
-// it is 0 or below 1e-304.  2^t = 2^n * 2^f with n the nearest whole number, f
+// exp(x) for -700 <= x <= 0 in 64 bits, to 1e-10 relative; exp_near(0) is 1, a NaN
+// stays one.  2^t = 2^n * 2^f with n the nearest whole number, f
 // in [-1/2, 1/2] and 2^f = 1 + f P(f), P the polynomial that meets
 // (2^f - 1) / f at the seven Chebyshev points.  Adding 1.5 * 2^52 rounds t to n
 // and leaves n in the sum's low word, from where it goes into the exponent.
-__device__ __forceinline__ double exp_neg(double x) {
+__device__ __forceinline__ double exp_near(double x) {
     constexpr double kLog2e = 1.4426950408889634074, kRound = 6755399441055744.0;
-    x = fmax(x, -700.0);
     const double r = __builtin_fma(x, kLog2e, kRound);
     const double f = __builtin_fma(x, kLog2e, -(r - kRound));
     double p = 1.5297323742797923e-05;
@@ -43,6 +42,9 @@ __device__ __forceinline__ double exp_neg(double x) {
     p = __builtin_fma(p, f, 1.0);
     return __hiloint2double(__double2hiint(p) + (__double2loint(r) << 20), __double2loint(p));
 }
+
+// The same for any x <= 0: below -700 it is below 1e-304.
+__device__ __forceinline__ double exp_neg(double x) { return exp_near(fmax(x, -700.0)); }
 
 // What one wave finds in its part of a row of logits.
 struct Partials {
@@ -211,22 +213,32 @@ __global__ void __launch_bounds__(64 * kWaves) beam_part_kernel(
     for (int i = 0; i < NL; ++i) raw[i] = r.fetch(first + 64 * i, V);
 #pragma unroll
     for (int i = 0; i < NL; ++i) r.unpack(raw[i], first + 64 * i, V, v[i]);
-    float m = -INFINITY;
-    bool bad = false;
+    float m = -INFINITY, least = INFINITY;  // (both pass a NaN over)
 #pragma unroll
     for (int i = 0; i < NL; ++i)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            bad |= !(v[i][e] < INFINITY);
             m = fmaxf(m, v[i][e]);
+            least = fminf(least, v[i][e]);
         }
     double s = 0.0;
-    if (m > -INFINITY) {
+    bool bad = false;
+    if (__all(m < INFINITY && least - m >= -600.0f)) {
+        // the common case: nothing masked, nothing to clamp; a NaN comes through
         const double md = m;
 #pragma unroll
         for (int i = 0; i < NL; ++i)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) s += exp_neg((double)v[i][e] - md);
+            for (int e = 0; e < VEC; ++e) s += exp_near((double)v[i][e] - md);
+        bad = s != s;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                bad |= !(v[i][e] < INFINITY);
+                if (m > -INFINITY) s += exp_neg((double)v[i][e] - (double)m);
+            }
     }
     float top = m;
     for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
@@ -333,19 +345,24 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(
             if (!live && c != -INFINITY && err) atomicOr(err, ENGRAM_ERRBIT_LOGIT);
         }
     }
-    for (int o = 1; o < group_lanes; o <<= 1) group = fmax(group, __shfl_xor(group, o, 64));
+    // (lanes equal modulo the groups of a wave, so that few parts spread over them)
+    const int per_wave = 64 / group_lanes;
+    for (int o = per_wave; o < 64; o <<= 1) group = fmax(group, __shfl_xor(group, o, 64));
     const int waves = W < kJoinWaves ? W : kJoinWaves;
-    const int groups = waves * (64 / group_lanes);
-    if (lane % group_lanes == 0 && wave < waves)
-        group_key[wave * (64 / group_lanes) + lane / group_lanes] = group;
+    const int groups = waves * per_wave;
+    if (lane < per_wave && wave < waves) group_key[wave * per_wave + lane] = group;
     __syncthreads();
-    if (tid < groups) {
-        const double k = group_key[tid];
+    // (sixteen lanes count for one)
+    const int one = tid >> 4, part16 = tid & 15;
+    for (int i = one; i < groups; i += NT / 16) {
+        const double k = group_key[i];
         int rank = 0;
-        for (int l = 0; l < groups; ++l) {
+#pragma unroll 8
+        for (int l = part16; l < groups; l += 16) {
             const double x = group_key[l];
-            rank += (x > k || (x == k && l < tid)) ? 1 : 0;
+            rank += (x > k || (x == k && l < i)) ? 1 : 0;
         }
+        for (int o = 1; o < 16; o <<= 1) rank += __shfl_xor(rank, o, 64);
         if (rank == W - 1) reach = k;  // -inf: fewer than W parts
     }
     __syncthreads();
@@ -451,13 +468,15 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(
     int found = count;
     if (found <= kList) {
         // (the list's order is not the same on every run; the ranks are)
-        for (int j = tid; j < found; j += NT) {
+        for (int j = one; j < found; j += NT / 16) {
             const double k = list_key[j];
             const int32_t i = list_idx[j];
             int rank = 0;
-            for (int l = 0; l < found; ++l)
+#pragma unroll 4
+            for (int l = part16; l < found; l += 16)
                 rank += (list_key[l] > k || (list_key[l] == k && list_idx[l] < i)) ? 1 : 0;
-            if (rank < W) emit(rank, k, i);
+            for (int o = 1; o < 16; o <<= 1) rank += __shfl_xor(rank, o, 64);
+            if (part16 == 0 && rank < W) emit(rank, k, i);
         }
     } else {
         // long runs of equal scores: W rounds, each for the best behind the last

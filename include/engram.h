@@ -341,8 +341,9 @@ engram_status engram_forward_adapted(const engram_geometry* g, const engram_hash
  *   ENGRAM_SCALE_F32_128   fp32 [rows, ceil(dim/128)]: max |y| / 448 of 128 values;
  *   ENGRAM_SCALE_F32_ROW   fp32 [rows]: max |y| / 448 of the row.
  * The last group of a row may be short.  A group of zeros has scale code 0 (or
- * scale 0) and codes 0.  A NaN or an infinity in y has code 0x7F (NaN); the
- * maximum passes NaN over.
+ * scale 0) and codes 0.  A NaN or an infinity in y has code 0x7F (NaN); a
+ * NaN or an infinity in h reaches its own row alone: a NaN makes all of it NaN
+ * (e8m0 scale codes 255), beside an infinity the finite values become 0.
  *   x bf16 [rows, dim]; residual the same or NULL (h = x); weight bf16 [dim] or
  *   NULL (1); total bf16 [rows, dim] or NULL, may be x or residual; codes uint8
  *   [rows, dim].  dim % 8 == 0, 8 <= dim <= 32768.  x, residual, weight and

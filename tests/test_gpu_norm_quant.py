@@ -137,8 +137,27 @@ def test_nan_and_infinity_stay_in_their_row(ge, fmt):
     for row in (0, 2, 4):
         assert torch.equal(codes[row], want[0][row]) and torch.equal(scales[row], want[1][row])
     assert (codes[1] == 0x7F).all()
+    assert (scales[1] == 255).all() if fmt == "e8m0_32" else torch.isnan(scales[1]).all()
     rest = torch.arange(264, device=dev) != 200
     assert int(codes[3, 200]) == 0x7F and ((codes[3, rest] & 0x7F) == 0).all()  # finite / inf = 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_overflow_of_y_is_a_nan_code(ge, fmt):
+    dev = torch.device("cuda:0")
+    say("norm overflow", fmt)
+    x = torch.ones(3, 256, device=dev, dtype=torch.bfloat16)
+    x[:, 1::2] = -1.0
+    x[1, 130] = 16.0                                       # y = 16 * rstd * 2^127 is past fp32
+    w = torch.ones(256, device=dev, dtype=torch.bfloat16)
+    w[130] = 2.0 ** 127
+    codes, scales, _ = ge.engram_norm_quant(x, w, scale_format=fmt)
+    assert int(codes[1, 130]) == 0x7F
+    ok = torch.ones_like(codes, dtype=torch.bool)
+    ok[1, 130] = False
+    assert ((codes[ok] & 0x7F) != 0x7F).all()
+    check(x[:, :128].contiguous(), None, None, 1e-6, fmt,
+          *ge.engram_norm_quant(x[:, :128].contiguous(), scale_format=fmt))
 
 
 def test_refusals(ge):
