@@ -102,113 +102,151 @@ __device__ __forceinline__ int slot_pair(int row, int c) {
 __device__ __forceinline__ int slot_up(int row, int c) { return c ^ ((row >> 2) & 1); }
 
 // The adapters of a whole BT x BT tile (rows p0 .. of M, columns n0 .. of N),
-// through LDS: per adapter of the tile's rows and up to 64 ranks, the rows'
-// pairs and the adapter's up rows arrive by DMA in groups of 16 ranks (whole
-// 1 KiB pieces; loaded straight into the fragment layout, every wave fetches 32
-// lines a load), then each wave multiplies as in the projection's own k-steps.
+// through LDS in up to 64 ranks at a time: the rows' pairs, and the up rows of
+// as many of the tile's adapters as fit, arrive by DMA in groups of 16 ranks
+// (whole 1 KiB pieces; loaded straight into the fragment layout, every wave
+// fetches 32 lines a load), then each wave multiplies as in the projection's
+// own k-steps.  The pairs of the first 64 ranks are fetched beside the
+// projection's last k-tile, into the LDS stage that it leaves free.
 //   own[k]: position and adapter of row p0 + 64 k + lane
-// NW waves, the calling one at rows wm * 32 TI, columns wn * 32 TJ; smem
-// (4 groups of BT * 96 bytes) is free, before and after.
+// NW waves, the calling one at rows wm * 32 TI, columns wn * 32 TJ.
+constexpr int kPairBytes = 64, kUpBytes = 32;  // of a row in a group of 16 ranks
+
+template <int BT, int NW>
+__device__ __forceinline__ void load_pairs(const AddAdapters& ad, const int2 (&own)[BT / 64],
+                                           int64_t M, int wave, int lane, int r0, uint8_t* pairs) {
+    constexpr int LU = BT / 16;  // DMA instructions of a group: 16 rows of 4 chunks
+    static_assert(LU % NW == 0, "DMA shares");
+    const __amdgpu_buffer_rsrc_t ru = make_rsrc(ad.u, (uint32_t)(M * ad.rp * 4));
+    const int groups = min(4, (ad.rp - r0) / 16);
+#pragma unroll
+    for (int i = 0; i < LU / NW; ++i) {
+        const int seg = (LU / NW) * wave + i;
+        const int row = seg * 16 + (lane >> 2);
+        const int c = slot_pair(row, lane & 3);
+        int m = 0;
+#pragma unroll
+        for (int k = 0; k < BT / 64; ++k) {
+            const int x = __shfl(own[k].x, row & 63, 64);
+            m = (row >> 6) == k ? x : m;
+        }
+        const uint32_t off = (uint32_t)m * (uint32_t)(ad.rp * 4) + (uint32_t)(r0 * 4 + c * 16);
+        for (int g = 0; g < groups; ++g)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                ru, (lds_void*)(pairs + g * (BT * kPairBytes) + seg * 1024), 16, off, g * 64, 0, 0);
+    }
+}
+
+// whether a row of the tile has an adapter (every wave holds the same rows)
+template <int R>
+__device__ __forceinline__ bool any_adapter(const int2 (&own)[R]) {
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < R; ++k) any |= __ballot(own[k].y >= 0) != 0;
+    return any;
+}
+
+// `pairs`: BT * 256 bytes, holding the first ranks' (or on their way there);
+// `ups`: BT * 256 bytes, free.  Both are free afterwards.
 template <int BT, int NW, int TI, int TJ>
 __device__ __forceinline__ void add_tile(const AddAdapters& ad, f32x16 (&acc)[TJ][TI],
                                          const int2 (&own)[BT / 64], int64_t M, int n0, int N,
-                                         int wm, int wn, int wave, int lane, uint8_t* smem) {
-    constexpr int GROUP = BT * 96, UP = BT * 64;  // bytes of a group; its up rows start at UP
-    constexpr int LU = BT / 16, LB = BT / 32;     // DMA instructions of a group
-    static_assert(LU % NW == 0 && LB % NW == 0, "DMA shares");
+                                         int wm, int wn, int wave, int lane, uint8_t* pairs,
+                                         uint8_t* ups) {
+    constexpr int LB = BT / 32;  // DMA instructions of an adapter's group: 32 rows of 2 chunks
+    static_assert(LB % NW == 0, "DMA shares");
     const int lrow = lane & 31, lhalf = lane >> 5;
-    const __amdgpu_buffer_rsrc_t ru = make_rsrc(ad.u, (uint32_t)(M * ad.rp * 4));
-    bool any = false;
-#pragma unroll
-    for (int k = 0; k < BT / 64; ++k) any |= __ballot(own[k].y >= 0) != 0;
-    if (!any) return;  // (every wave holds the same rows)
+    if (!any_adapter(own)) return;
     for (int r0 = 0; r0 < ad.rp; r0 += 64) {
         const int groups = min(4, (ad.rp - r0) / 16);
-#pragma unroll
-        for (int i = 0; i < LU / NW; ++i) {
-            const int seg = (LU / NW) * wave + i;  // 16 rows of 4 chunks
-            const int row = seg * 16 + (lane >> 2);
-            const int c = slot_pair(row, lane & 3);
-            int m = 0;
-#pragma unroll
-            for (int k = 0; k < BT / 64; ++k) {
-                const int x = __shfl(own[k].x, row & 63, 64);
-                m = (row >> 6) == k ? x : m;
-            }
-            const uint32_t off = (uint32_t)m * (uint32_t)(ad.rp * 4) + (uint32_t)(r0 * 4 + c * 16);
-            for (int g = 0; g < groups; ++g)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    ru, (lds_void*)(smem + g * GROUP + seg * 1024), 16, off, g * 64, 0, 0);
-        }
+        const int fit = 8 / groups;  // adapters at once
+        if (r0) load_pairs<BT, NW>(ad, own, M, wave, lane, r0, pairs);
         uint64_t todo[BT / 64];
 #pragma unroll
         for (int k = 0; k < BT / 64; ++k) todo[k] = __ballot(own[k].y >= 0);
-        for (;;) {
+        // the next adapter of `left`, which loses it; -1: none
+        auto next = [&](uint64_t (&left)[BT / 64], uint64_t (&has)[BT / 64]) {
             int j = -1;
 #pragma unroll
             for (int k = BT / 64 - 1; k >= 0; --k)
-                if (todo[k]) j = __builtin_amdgcn_readlane(own[k].y, __builtin_ctzll(todo[k]));
-            if (j < 0) break;
-            uint64_t has[BT / 64];
+                if (left[k]) j = __builtin_amdgcn_readlane(own[k].y, __builtin_ctzll(left[k]));
 #pragma unroll
             for (int k = 0; k < BT / 64; ++k) {
                 has[k] = __ballot(own[k].y == j);
-                todo[k] &= ~has[k];
+                left[k] &= ~has[k];
             }
-            const __amdgpu_buffer_rsrc_t rb =
-                make_rsrc(ad.up + j * ad.up_stride + (int64_t)n0 * ad.rank,
-                          (uint32_t)(min(BT, N - n0) * ad.rank * 2));
+            return j;
+        };
+        for (;;) {
+            uint64_t load[BT / 64], has[BT / 64];
 #pragma unroll
-            for (int i = 0; i < LB / NW; ++i) {
-                const int seg = (LB / NW) * wave + i;  // 32 rows of 2 chunks
-                const int row = seg * 32 + (lane >> 1);
-                const int c = slot_up(row, lane & 1);
-                for (int g = 0; g < groups; ++g) {
-                    // (ranks past the last read as zeros)
-                    const int r = r0 + 16 * g + 8 * c;
-                    const uint32_t off =
-                        r < ad.rank ? (uint32_t)(row * ad.rank + r) * 2u : 0xFFFFFFF0u;
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                        rb, (lds_void*)(smem + g * GROUP + UP + seg * 1024), 16, off, 0, 0, 0);
-                }
-            }
-            __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-            __syncthreads();
+            for (int k = 0; k < BT / 64; ++k) load[k] = todo[k];
+            int taken = 0;
+            for (; taken < fit; ++taken) {
+                const int j = next(load, has);
+                if (j < 0) break;
+                const __amdgpu_buffer_rsrc_t rb =
+                    make_rsrc(ad.up + j * ad.up_stride + (int64_t)n0 * ad.rank,
+                              (uint32_t)(min(BT, N - n0) * ad.rank * 2));
 #pragma unroll
-            for (int i = 0; i < TI; ++i) {
-                const int first = (wm * TI + i) * 32;  // this wave's 32 rows
-                uint64_t h = 0;
-#pragma unroll
-                for (int k = 0; k < BT / 64; ++k) h = (first >> 6) == k ? has[k] : h;
-                const uint32_t mask = (uint32_t)(h >> (first & 32));
-                if (mask == 0) continue;
-                const bool hit = (mask >> lrow) & 1;
-                const int row = first + lrow;
-                f32x16 d[TJ];
-#pragma unroll
-                for (int t = 0; t < TJ; ++t) d[t] = acc[t][i];
-#pragma unroll 1
-                for (int g = 0; g < groups; ++g) {
-                    const uint8_t* at = smem + g * GROUP;
-                    const bf16x8 hi = *reinterpret_cast<const bf16x8*>(
-                        at + row * 64 + slot_pair(row, 2 * lhalf) * 16);
-                    const bf16x8 lo = *reinterpret_cast<const bf16x8*>(
-                        at + row * 64 + slot_pair(row, 2 * lhalf + 1) * 16);
-#pragma unroll
-                    for (int t = 0; t < TJ; ++t) {
-                        const int brow = (wn * TJ + t) * 32 + lrow;
-                        const bf16x8 b = *reinterpret_cast<const bf16x8*>(
-                            at + UP + brow * 32 + slot_up(brow, lhalf) * 16);
-                        d[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, hi, d[t], 0, 0, 0);
-                        d[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, lo, d[t], 0, 0, 0);
+                for (int i = 0; i < LB / NW; ++i) {
+                    const int seg = (LB / NW) * wave + i;
+                    const int row = seg * 32 + (lane >> 1);
+                    const int c = slot_up(row, lane & 1);
+                    for (int g = 0; g < groups; ++g) {
+                        // (ranks past the last read as zeros)
+                        const int r = r0 + 16 * g + 8 * c;
+                        const uint32_t off =
+                            r < ad.rank ? (uint32_t)(row * ad.rank + r) * 2u : 0xFFFFFFF0u;
+                        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                            rb,
+                            (lds_void*)(ups + (taken * groups + g) * (BT * kUpBytes) + seg * 1024),
+                            16, off, 0, 0, 0);
                     }
                 }
-#pragma unroll
-                for (int t = 0; t < TJ; ++t)
-#pragma unroll
-                    for (int v = 0; v < 16; ++v) acc[t][i][v] = hit ? d[t][v] : acc[t][i][v];
             }
-            __syncthreads();  // the up rows are read (and, behind the last one, all of it)
+            if (taken == 0) break;
+            __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+            __syncthreads();
+            for (int x = 0; x < taken; ++x) {
+                next(todo, has);
+#pragma unroll
+                for (int i = 0; i < TI; ++i) {
+                    const int first = (wm * TI + i) * 32;  // this wave's 32 rows
+                    uint64_t h = 0;
+#pragma unroll
+                    for (int k = 0; k < BT / 64; ++k) h = (first >> 6) == k ? has[k] : h;
+                    const uint32_t mask = (uint32_t)(h >> (first & 32));
+                    if (mask == 0) continue;
+                    const bool hit = (mask >> lrow) & 1;
+                    const int row = first + lrow;
+                    f32x16 d[TJ];
+#pragma unroll
+                    for (int t = 0; t < TJ; ++t) d[t] = acc[t][i];
+#pragma unroll 1
+                    for (int g = 0; g < groups; ++g) {
+                        const uint8_t* pu = pairs + g * (BT * kPairBytes) + row * kPairBytes;
+                        const uint8_t* pb = ups + (x * groups + g) * (BT * kUpBytes);
+                        const bf16x8 hi = *reinterpret_cast<const bf16x8*>(
+                            pu + slot_pair(row, 2 * lhalf) * 16);
+                        const bf16x8 lo = *reinterpret_cast<const bf16x8*>(
+                            pu + slot_pair(row, 2 * lhalf + 1) * 16);
+#pragma unroll
+                        for (int t = 0; t < TJ; ++t) {
+                            const int brow = (wn * TJ + t) * 32 + lrow;
+                            const bf16x8 b = *reinterpret_cast<const bf16x8*>(
+                                pb + brow * kUpBytes + slot_up(brow, lhalf) * 16);
+                            d[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, hi, d[t], 0, 0, 0);
+                            d[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, lo, d[t], 0, 0, 0);
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < TJ; ++t)
+#pragma unroll
+                        for (int v = 0; v < 16; ++v) acc[t][i][v] = hit ? d[t][v] : acc[t][i][v];
+                }
+            }
+            __syncthreads();  // the up rows (and, behind the last round, the pairs) are read
         }
     }
 }

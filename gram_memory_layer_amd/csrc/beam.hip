@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(
 // rows fill the machine with long parts (fewer partial sums to join), few rows
 // are cut short so that one row spreads over many compute units.
 int elements_of(int64_t rows, int V) {
-    return rows * ((V + 8191) / 8192) >= 1024 ? 32 : 8;
+    return rows * ((V + 8191) / 8192) >= 2048 ? 32 : 8;
 }
 
 int parts_of(int64_t rows, int V) {

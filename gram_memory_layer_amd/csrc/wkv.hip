@@ -376,10 +376,15 @@ __device__ __forceinline__ void wkv_tile(const uint16_t* __restrict__ A,
     __syncthreads();
     read_frags(0, 0, 0);
     for (int kt = 0; kt + 1 < nk; ++kt) k_tile(kt, T{});
+    // the last k-tile leaves the other stage free
+    uint8_t* const free_stage = smem + (nk & 1) * STAGE;
+    if constexpr (D::on)
+        if (any_adapter(own)) load_pairs<BT, NW>(ad, own, M, wave, lane, 0, free_stage);
     k_tile(nk - 1, F{});
     __syncthreads();  // every wave is done with the operand stages
     if constexpr (D::on)
-        add_tile<BT, NW, TI, TJ>(ad, acc, own, M, n0, N, wm, wn, wave, lane, smem);
+        add_tile<BT, NW, TI, TJ>(ad, acc, own, M, n0, N, wm, wn, wave, lane, free_stage,
+                                 smem + ((nk + 1) & 1) * STAGE);
 
     // ---- epilogue through LDS.  D[n][m]: lane holds m = lane%32 (+32 i) and
     // n = 32 j + 8 (v/4) + 4 (lane/32) + v%4.  Each wave writes its WM x WN
