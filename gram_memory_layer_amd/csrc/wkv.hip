@@ -246,26 +246,41 @@ __device__ __forceinline__ void wkv_tile(const uint16_t* __restrict__ A,
         voff[i] = (uint32_t)(row * K * 2 + slot128(row, lane & 7) * 16);
     }
     uint32_t aoff[NLD];
+    auto place_a = [&]() {
 #pragma unroll
-    for (int i = 0; i < NLD; ++i) {
-        aoff[i] = voff[i];
-        if constexpr (D::on) {
-            const int row = (NW * i + wave) * 8 + (lane >> 3);
-            aoff[i] = (uint32_t)ad.tile[m0 + row].x * (uint32_t)(K * 2) +
-                      (uint32_t)(slot128(row, lane & 7) * 16);
+        for (int i = 0; i < NLD; ++i) {
+            aoff[i] = voff[i];
+            if constexpr (D::on) {
+                const int row = (NW * i + wave) * 8 + (lane >> 3);
+                int m = 0;
+#pragma unroll
+                for (int k = 0; k < BT / 64; ++k) {
+                    const int x = __shfl(own[k].x, row & 63, 64);
+                    m = (row >> 6) == k ? x : m;
+                }
+                aoff[i] = (uint32_t)m * (uint32_t)(K * 2) +
+                          (uint32_t)(slot128(row, lane & 7) * 16);
+            }
         }
-    }
-    auto issue_loads = [&](int kt, int stage) {
+    };
+    auto issue_a = [&](int kt, int stage) {
         uint8_t* st = smem + stage * STAGE;
-        const int soff = kt * 128;
 #pragma unroll
         for (int i = 0; i < NLD; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                ra, (lds_void*)(st + (NW * i + wave) * 1024), 16, aoff[i], soff, 0, 0);
+                ra, (lds_void*)(st + (NW * i + wave) * 1024), 16, aoff[i], kt * 128, 0, 0);
+    };
+    auto issue_w = [&](int kt, int stage) {
+        uint8_t* st = smem + stage * STAGE;
 #pragma unroll
         for (int i = 0; i < NLD; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rw, (lds_void*)(st + BM * 128 + (NW * i + wave) * 1024), 16, voff[i], soff, 0, 0);
+                rw, (lds_void*)(st + BM * 128 + (NW * i + wave) * 1024), 16, voff[i], kt * 128, 0,
+                0);
+    };
+    auto issue_loads = [&](int kt, int stage) {
+        issue_a(kt, stage);
+        issue_w(kt, stage);
     };
 
     const int lrow = lane & 31, lhalf = lane >> 5;
@@ -371,7 +386,14 @@ __device__ __forceinline__ void wkv_tile(const uint16_t* __restrict__ A,
     using F = std::false_type;
 
     const int nk = K / BK;
-    issue_loads(0, 0);
+    if constexpr (D::on) {  // W needs no positions
+        issue_w(0, 0);
+        place_a();
+        issue_a(0, 0);
+    } else {
+        place_a();
+        issue_loads(0, 0);
+    }
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
     __syncthreads();
     read_frags(0, 0, 0);
@@ -418,7 +440,14 @@ __device__ __forceinline__ void wkv_tile(const uint16_t* __restrict__ A,
         const int64_t m = m0 + wm * WM + r;
         const int n = n0 + wn * WN + csub * 8;
         int64_t to = m;
-        if constexpr (D::on) to = ad.tile[m].x;
+        if constexpr (D::on) {
+            const int row = wm * WM + r;  // its position is lane row % 64's
+#pragma unroll
+            for (int k = 0; k < BT / 64; ++k) {
+                const int x = __shfl(own[k].x, row & 63, 64);
+                to = (row >> 6) == k ? x : to;
+            }
+        }
         if (m < M && n < N) *reinterpret_cast<uint4*>(C + to * ldc + n) = v;
     }
 }
