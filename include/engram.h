@@ -285,7 +285,10 @@ engram_status engram_forward_noalloc(const engram_geometry* g, const engram_hash
                                      float* gate, uint32_t* err, void* stream);
 
 /* ---- Around the layer in serving: adapters, the next product's input, beams.
- * These calls extend the pages' path; the pages do not describe them. */
+ * These calls extend the pages' path; the pages do not describe them.  A
+ * scratch argument may be reused by the next call on the same stream, and by
+ * captured graphs that are replayed one after the other; calls that overlap
+ * need one each. */
 
 /* Low-rank adapters of the wkv projection.  rank % 8 == 0, 8 <= rank <= 128
  * (smaller ones are padded with zeros); 1 <= n <= 65536. */

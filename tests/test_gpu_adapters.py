@@ -88,6 +88,16 @@ CASES = [
     (257, 200, 2, 3, 96, 9, 72, "random"), (300, 1032, 1, 24, 64, 6, 64, "spans"),
     (1023, 264, 1, 4, 64, 8, 16, "random"), (1024, 264, 1, 4, 64, 8, 16, "spans"),
     (1300, 1288, 1, 6, 64, 8, 64, "spans"), (1100, 136, 2, 3, 32, 5, 16, "random"),
+    # every position its own adapter, at the ranks and batch sizes that share LDS differently
+    (64, 136, 1, 4, 64, 64, 128, "each"), (64, 72, 1, 2, 64, 64, 16, "each"),
+    (48, 136, 1, 4, 64, 48, 72, "each"), (32, 264, 1, 2, 64, 32, 64, "each"),
+    (32, 136, 1, 2, 64, 32, 128, "each"), (16, 72, 1, 2, 64, 16, 128, "each"),
+    (9, 72, 1, 2, 64, 16, 48, "each"), (3, 200, 4, 24, 64, 2, 56, "each"),
+    # mid-sized batches on both sides of the decode kernel's share of the machine
+    (600, 264, 1, 4, 64, 8, 16, "random"), (613, 2056, 2, 24, 64, 5, 8, "spans"),
+    (200, 5120, 1, 4, 64, 30, 24, "random"), (400, 5120, 2, 2, 64, 7, 112, "random"),
+    # more adapters than the order has buckets
+    (1500, 136, 1, 2, 64, 2100, 8, "each"), (2100, 136, 1, 2, 64, 2000, 16, "random"),
 ]
 
 
@@ -151,6 +161,42 @@ def test_ids_outside_count_as_none_and_flag(ge, M):
     got = ge.engram_wkv_adapters(g, ad, a, w, bad, err=err)
     assert int(err.item()) == ge.ERRBIT_ADAPTER
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+def test_more_positions_than_one_launch_takes(ge):
+    dev = torch.device("cuda:0")
+    say("adapters, 262,144 positions and 300 more")
+    M = 262144 + 300
+    g = geometry(ge, 8, 1, 1)
+    a, w, down, up, scale, ids = inputs(dev, M, g.N, g.K, 5, 16, "random", 3)
+    kv = ge.engram_wkv_adapters(g, ge.Adapters(down, up, scale), a, w, ids)
+    ref, bound = reference(a, w, down, up, scale, ids)
+    check(kv, ref, bound, "two launches")
+
+
+@pytest.mark.parametrize("M", [8, 90000])
+def test_offsets_past_32_bits(ge, M):
+    dev = torch.device("cuda:0")
+    say("adapters far", M)
+    g = geometry(ge, 5120, 4, 1)
+    # M = 8: 700 adapters whose up rows take 4.6 GB; M = 90000: a result of 4.6 GB
+    n, rank = (700, 128) if M == 8 else (6, 16)
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(M)
+    r = lambda *s, std=1.0: (torch.randn(s, generator=gen, device=dev) * std).to(torch.bfloat16)  # noqa: E731
+    a, w, down = r(M, g.K), r(g.N, g.K, std=g.K ** -0.5), r(n, rank, g.K, std=g.K ** -0.5)
+    up = torch.empty(n, g.N, rank, dtype=torch.bfloat16, device=dev)
+    for j in range(n):
+        up[j] = r(g.N, rank, std=rank ** -0.5)
+    ids = (torch.arange(M, device=dev) * 97 + n - 1) % n
+    kv = ge.engram_wkv_adapters(g, ge.Adapters(down, up), a, w, ids.to(torch.int32))
+    at = torch.arange(M, device=dev) if M == 8 else torch.tensor([0, 1, 41943, 41944, 83885, 83886, 83887, M - 1],
+                                                                 device=dev)
+    some = ids[at]
+    ref, bound = reference(a[at], w, down[some], up[some], None, torch.arange(at.numel()))
+    check(kv[at], ref, bound, "far")
+    del up, kv
+    torch.cuda.empty_cache()
 
 
 def test_no_positions_and_refusals(ge):

@@ -85,7 +85,7 @@ def draw(dev, B, W, V, dtype, seed, ld=None):
 
 CASES = [(1, 1, 1), (1, 1, 2), (1, 4, 5), (2, 3, 7), (4, 1, 100), (3, 5, 1000), (1, 2, 511), (2, 4, 513),
          (2, 32, 4097), (5, 8, 2049), (1, 17, 8191), (1, 4, 129280), (3, 16, 20011), (40, 8, 32003),
-         (64, 4, 1000), (200, 7, 333)]
+         (64, 4, 1000), (200, 7, 333), (64, 8, 20000), (1, 32, 40), (16, 32, 9000), (300, 1, 5000)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
@@ -280,6 +280,23 @@ def test_reorder(ge, B, W):
             for (buf, st), (lo, hi) in zip(base, edge):
                 assert torch.equal(buf[:skew], lo) and torch.equal(buf[skew + st.numel():], hi)
             assert int(err.item()) == 0
+
+
+def test_reorder_past_32_bit_offsets(ge):
+    dev = torch.device("cuda:0")
+    say("reorder far")
+    B, W, words = 2, 4, 180_000_003                        # 5.8 GB in all
+    st = torch.empty(B * W, words, dtype=torch.int32, device=dev)
+    mark = torch.arange(B * W, device=dev, dtype=torch.int32)
+    cols = torch.tensor([0, 1, 2, words // 2, words - 2, words - 1], device=dev)
+    st[:, cols] = mark[:, None] * 100 + torch.arange(6, device=dev, dtype=torch.int32)
+    before = st[:, cols].clone()
+    parents = torch.tensor([[1, 1, 3, 0], [3, 0, 2, 2]], dtype=torch.int32, device=dev)
+    ge.engram_beam_reorder([st], parents)
+    rows = (torch.arange(B, device=dev)[:, None] * W + parents).reshape(-1).long()
+    assert torch.equal(st[:, cols], before[rows])
+    del st
+    torch.cuda.empty_cache()
 
 
 def test_reorder_types_bad_parents_and_refusals(ge):

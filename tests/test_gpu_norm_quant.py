@@ -88,6 +88,21 @@ def test_norm_quant(ge, fmt, rows, dim):
     assert (buf[rows] == 77).all()
 
 
+def test_rows_past_32_bit_offsets(ge):
+    dev = torch.device("cuda:0")
+    say("norm far rows")
+    rows, dim = 430000, 5120                               # 2.2e9 values
+    x = torch.zeros(rows, dim, dtype=torch.bfloat16, device=dev)
+    at = torch.tensor([0, 1, 209715, 209716, 419430, 419431, rows - 1], device=dev)
+    x[at] = torch.randn(at.numel(), dim, device=dev).to(torch.bfloat16)
+    codes, scales, total = ge.engram_norm_quant(x, residual=x, total=x)  # in place: total = 2 x
+    few = (x[at].float() / 2).to(torch.bfloat16)
+    check(few, few, None, 1e-6, "e8m0_32", codes[at], scales[at], x[at])
+    assert (codes[2] == 0).all() and (codes[rows - 2] == 0).all()
+    del x, codes, scales, total
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_total_may_be_an_input(ge, fmt):
     dev = torch.device("cuda:0")
