@@ -809,7 +809,8 @@ def engram_beam_reorder(states, parents, err=None):
     rows, n = B * W, len(states)
     ptr, size = [], []
     for st in states:
-        _dev(st, "state", st.dtype if isinstance(st, torch.Tensor) else None, None, dev)
+        if not (type(st) is torch.Tensor and st.is_cuda and st.is_contiguous() and st.device == dev):
+            _dev(st, "state", st.dtype if isinstance(st, torch.Tensor) else None, None, dev)
         shape = st.shape
         if not len(shape) or (shape[0] != rows and tuple(shape[:2]) != (B, W)):
             raise ValueError("a state must be [B*W, ...] or [B, W, ...] (got %s)" % (tuple(shape),))

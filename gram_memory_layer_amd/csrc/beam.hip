@@ -300,6 +300,20 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(
 
     double group = none;  // the largest score of this lane's group of parts
     for (int w = wave; w < W; w += kJoinWaves) {
+        // the first parts are on their way before it is known whether they count
+        // (a dead or finished beam's are not written: they are not looked at)
+        constexpr int AT = 4;
+        float t[AT];
+        double x[AT];
+        auto load = [&](int p0) {
+#pragma unroll
+            for (int i = 0; i < AT; ++i) {
+                const int p = p0 + 64 * i;
+                t[i] = p < parts ? tops[w * parts + p] : -INFINITY;
+                x[i] = p < parts ? sums[w * parts + p] : 0.0;
+            }
+        };
+        load(lane);
         const float c = cum[b * W + w];
         const bool fin = finished && finished[b * W + w];
         const bool live = c > -INFINITY && c < INFINITY;
@@ -309,26 +323,21 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(
             double s = 0.0;
             float m = -INFINITY;
             bool bad = false;
-            for (int p0 = lane; p0 < parts; p0 += 64 * 4) {
-                float t[4];
-                double x[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int p = p0 + 64 * i;
-                    t[i] = p < parts ? tops[w * parts + p] : -INFINITY;
-                    x[i] = p < parts ? sums[w * parts + p] : 0.0;
-                }
+            for (int p0 = lane;;) {
                 float nm = m;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < AT; ++i) {
                     bad |= t[i] != t[i];
                     nm = fmaxf(nm, t[i]);
                 }
                 if (m > -INFINITY) s *= exp_neg((double)m - (double)nm);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < AT; ++i)
                     if (t[i] > -INFINITY) s += x[i] * exp_neg((double)t[i] - (double)nm);
                 m = nm;
+                p0 += 64 * AT;
+                if (p0 - lane >= parts) break;
+                load(p0);
             }
             all = m;
             for (int o = 1; o < 64; o <<= 1) all = fmaxf(all, __shfl_xor(all, o, 64));
@@ -413,37 +422,34 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(
         __syncthreads();
     }
 
-    // the listed parts' logits that may reach the bound: f(score, beam * V + token)
+    // the listed parts' logits that may reach the bound, a wave a part:
+    // f(score, beam * V + token).  Nearly all fail a comparison with the logit at
+    // the bound (a little lower, against its rounding).
     auto scan = [&](auto f) {
-        constexpr int AT = 4;  // pieces on their way
-        for (int i0 = 0; i0 < n_listed * NL * 64; i0 += NT * AT) {
-            uint4 raw[AT];
-            int w[AT];
-            int64_t piece[AT];
+        for (int q = wave; q < n_listed; q += kJoinWaves) {
+            const int at = __builtin_amdgcn_readfirstlane(listed[q]);
+            const int w = at / parts;
+            const int64_t first = (int64_t)(at - w * parts) * (NL * 64) + lane;
+            const Row<T> r(logits + (b * W + w) * ld);
+            uint4 raw[NL];
 #pragma unroll
-            for (int a = 0; a < AT; ++a) {
-                const int i = i0 + a * NT + tid, q = i / (NL * 64);
-                const int at = q < n_listed ? listed[q] : -1;
-                w[a] = at < 0 ? -1 : at / parts;
-                piece[a] = (int64_t)(at - w[a] * parts) * (NL * 64) + i % (NL * 64);
-                if (at >= 0) raw[a] = Row<T>(logits + (b * W + w[a]) * ld).fetch(piece[a], V);
-            }
+            for (int i = 0; i < NL; ++i) raw[i] = r.fetch(first + 64 * i, V);
+            const float c = own[w], m = top[w];
+            const double lo = low[w];
+            float edge = (float)((double)m + ((t - (double)c) + lo));
+            edge -= (fabsf(edge) + fabsf(m)) * 0x1p-22f;
 #pragma unroll
-            for (int a = 0; a < AT; ++a) {
-                if (w[a] < 0) continue;
-                const Row<T> r(logits + (b * W + w[a]) * ld);
+            for (int i = 0; i < NL; ++i) {
                 float x[VEC];
-                r.unpack(raw[a], piece[a], V, x);
-                const int base = w[a] * V + (int)r.column(piece[a]);
-                const float c = own[w[a]], m = top[w[a]];
-                const double lo = low[w[a]];
+                r.unpack(raw[i], first + 64 * i, V, x);
                 float most = x[0];
 #pragma unroll
                 for (int e = 1; e < VEC; ++e) most = fmaxf(most, x[e]);
-                if (!(most > -INFINITY) || score_of(c, m, lo, most) < t) continue;
+                if (!(most >= edge)) continue;
+                const int base = w * V + (int)r.column(first + 64 * i);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
-                    if (x[e] > -INFINITY) f(score_of(c, m, lo, x[e]), base + e);
+                    if (x[e] >= edge && x[e] > -INFINITY) f(score_of(c, m, lo, x[e]), base + e);
             }
         }
         if (tid < W && done[tid] && own[tid] > -INFINITY && own[tid] < INFINITY)
