@@ -424,7 +424,9 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(
 
     // the listed parts' logits that may reach the bound, a wave a part:
     // f(score, beam * V + token).  Nearly all fail a comparison with the logit at
-    // the bound (a little lower, against its rounding).
+    // the bound, lowered by more than its roundings: 2^-22 for the one to fp32,
+    // 2^-49 of every term for those in 64 bits, which are what counts where the
+    // logits are near 0 and the terms cancel (a row of zeros).
     auto scan = [&](auto f) {
         for (int q = wave; q < n_listed; q += kJoinWaves) {
             const int at = __builtin_amdgcn_readfirstlane(listed[q]);
@@ -436,8 +438,9 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(
             for (int i = 0; i < NL; ++i) raw[i] = r.fetch(first + 64 * i, V);
             const float c = own[w], m = top[w];
             const double lo = low[w];
-            float edge = (float)((double)m + ((t - (double)c) + lo));
-            edge -= (fabsf(edge) + fabsf(m)) * 0x1p-22f;
+            const double at_t = (double)m + ((t - (double)c) + lo);
+            const float edge = (float)(at_t - (fabs(at_t) + fabs((double)m)) * 0x1p-22 -
+                                       (fabs(t) + fabs((double)c) + fabs(lo)) * 0x1p-49);
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
                 float x[VEC];
@@ -581,6 +584,7 @@ struct ReorderArgs {
     int64_t words[kMaxStates];         // 4-byte words of a row
     int64_t first[kMaxStates + 1];     // first workgroup of each state
     int32_t per_seq[kMaxStates];       // workgroups a sequence (0: sequences share them)
+    int64_t start;                     // first workgroup of this launch
     int n;
 };
 
@@ -612,10 +616,11 @@ __global__ void __launch_bounds__(256) beam_reorder_kernel(const ReorderArgs a,
                                                            int B, int W,
                                                            uint32_t* __restrict__ err) {
     typedef typename Column<UNIT>::type vec;
+    const int64_t at = a.start + blockIdx.x;
     int st = 0;
-    while ((int64_t)blockIdx.x >= a.first[st + 1]) ++st;
+    while (at >= a.first[st + 1]) ++st;
     const int64_t words = a.words[st], cols = words / UNIT;
-    const int64_t block = blockIdx.x - a.first[st];
+    const int64_t block = at - a.first[st];
     int64_t col;
     int b;
     if (a.per_seq[st]) {
@@ -658,13 +663,18 @@ hipError_t run_reorder(ReorderArgs& a, const int32_t* parents, int64_t B, int W,
         a.per_seq[i] = cols > 128 ? (int32_t)((cols + 255) / 256) : 0;
         a.first[i + 1] = a.first[i] + (cols > 128 ? B * a.per_seq[i] : (B * cols + 255) / 256);
     }
-    if (a.first[a.n] > INT32_MAX) return hipErrorInvalidValue;
     auto k = W <= 4    ? beam_reorder_kernel<UNIT, 4>
              : W <= 8  ? beam_reorder_kernel<UNIT, 8>
              : W <= 16 ? beam_reorder_kernel<UNIT, 16>
                        : beam_reorder_kernel<UNIT, 32>;
-    k<<<dim3((uint32_t)a.first[a.n]), dim3(256), 0, s>>>(a, parents, (int)B, W, err);
-    return hipGetLastError();
+    constexpr int64_t most = ((int64_t)1 << 31) / 256;  // a launch has fewer than 2^32 threads
+    for (a.start = 0; a.start < a.first[a.n]; a.start += most) {
+        const int64_t blocks = a.first[a.n] - a.start < most ? a.first[a.n] - a.start : most;
+        k<<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(a, parents, (int)B, W, err);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace

@@ -234,6 +234,41 @@ def test_rows_past_32_bit_offsets(ge):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,W,V", [(2, 4, 300), (1, 2, 129280), (3, 5, 777), (1, 1, 1)])
+def test_flat_rows_at_any_score(ge, B, W, V, dtype):
+    """Rows of one value (a fresh head's zeros), where score and log sum cancel to
+    rounding errors, also with scores beside which the logits vanish."""
+    dev = torch.device("cuda:0")
+    for value in (0.0, 1e-30, -5.0, 2.0 ** 100):
+        x = torch.full((B * W, V), value, dtype=dtype, device=dev)
+        for c0 in (0.0, -0.1, -3.7, -11.77, -1234.5, -1e6, -3e38, 1e30):
+            say("beam flat", B, W, V, dtype, value, c0)
+            same = torch.full((B, W), c0, device=dev)
+            check(ge.engram_beam_select(x, same), x, same)
+            apart = same - 0.37 * torch.arange(W, device=dev)
+            check(ge.engram_beam_select(x, apart), x, apart)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_nearly_flat_rows(ge, dtype):
+    dev = torch.device("cuda:0")
+    B, W, V = 2, 4, 5000
+    for step in (2.0 ** -20, 2.0 ** -100):
+        x = torch.zeros(B * W, V, dtype=dtype, device=dev)
+        x[:, 4321], x[:, 17], x[:, 99] = step, 2 * step, -step
+        c = -torch.rand(B, W, device=dev, generator=torch.Generator(device=dev).manual_seed(3)) - 1
+        tokens, parents, new, _ = (t.cpu() for t in ge.engram_beam_select(x, c))
+        best = c.argmax(1).cpu()
+        assert torch.equal(parents, best[:, None].expand(B, W).int())
+        if step == 2.0 ** -20:  # steps of 1e-6 show in a 64-bit score, 1e-30 is a tie
+            assert tokens.tolist() == [[17, 4321, 0, 1]] * B
+        else:
+            assert tokens.tolist() == [[0, 1, 2, 3]] * B
+        want = c.double().cpu().gather(1, best[:, None]) - np.log(V)
+        assert ((new.double() - want).abs() <= 2.0 ** -24 * want.abs() + 1e-9 + 2 * step).all()
+
+
 def test_selection_refusals(ge):
     dev = torch.device("cuda:0")
     x, c = draw(dev, 2, 3, 40, torch.float32, 1)
@@ -297,6 +332,23 @@ def test_reorder_past_32_bit_offsets(ge):
     assert torch.equal(st[:, cols], before[rows])
     del st
     torch.cuda.empty_cache()
+
+
+def test_reorder_of_more_threads_than_a_launch_takes(ge):
+    """Rows of 2^31 + 4097 words: more than 2^23 workgroups, in several launches."""
+    dev = torch.device("cuda:0")
+    R = 2 ** 31 + 4097
+    if torch.cuda.mem_get_info()[0] < 2.2 * 8 * R:
+        pytest.skip("needs %d GB" % (8 * R >> 30))
+    say("reorder launches", R)
+    st = torch.zeros(2 * R + 1, dtype=torch.int32, device=dev)[1:].view(2, R)
+    at = torch.tensor([0, 1, 2 ** 31 - 1, 2 ** 31, 2 ** 31 + 255, R - 257, R - 1], device=dev)
+    st[0, at] = torch.arange(7, dtype=torch.int32, device=dev) + 1
+    st[1, at] = torch.arange(7, dtype=torch.int32, device=dev) + 11
+    ge.engram_beam_reorder([st], torch.tensor([[1, 0]], dtype=torch.int32, device=dev))
+    assert st[0, at].tolist() == list(range(11, 18)) and st[1, at].tolist() == list(range(1, 8))
+    ge.engram_beam_reorder([st], torch.tensor([[1, 1]], dtype=torch.int32, device=dev))
+    assert st[0, at].tolist() == list(range(1, 8)) and st[1, at].tolist() == list(range(1, 8))
 
 
 def test_reorder_types_bad_parents_and_refusals(ge):
