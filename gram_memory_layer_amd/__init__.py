@@ -844,6 +844,8 @@ class EngramLayer:
 
     def forward(self, x, ids, mask=None, state=None, out=None, gate=None, err=None, adapters=None,
                 adapter_ids=None):
+        if adapters is None and adapter_ids is not None:
+            raise ValueError("adapter_ids without adapters")
         if adapters is not None:
             need = max(engram_forward_adapted_workspace_size(self.g, adapters, ids.numel()), 1)
             if self._ws is None or self._ws.numel() < need:

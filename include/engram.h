@@ -305,7 +305,8 @@ typedef struct engram_adapters {
  * and the projection alone for j = -1; sums in fp32 (down's result enters the
  * second product as a pair of bf16 values, which hold it to 2^-16), one rounding
  * to bf16.  A position's output depends on its own adapter alone: a
- * NaN or an infinity in another one does not reach it.
+ * NaN or an infinity in another one does not reach it.  (An infinity in its own
+ * up row gives a NaN: it meets the pair's second value, mostly of either sign.)
  *   a, w, kv as in engram_wkv; adapter_ids int32 [M], in any order;
  *   scratch  device memory of engram_wkv_adapters_scratch_size bytes,
  *            256-byte aligned; contents on entry do not matter.
@@ -344,7 +345,7 @@ engram_status engram_forward_adapted(const engram_geometry* g, const engram_hash
  *   ENGRAM_SCALE_F32_128   fp32 [rows, ceil(dim/128)]: max |y| / 448 of 128 values;
  *   ENGRAM_SCALE_F32_ROW   fp32 [rows]: max |y| / 448 of the row.
  * The last group of a row may be short.  A group of zeros has scale code 0 (or
- * scale 0) and codes 0.  A NaN or an infinity in y has code 0x7F (NaN); a
+ * scale 0) and codes 0 (with eps = 0 a row of zeros is 0/0: all NaN).  A NaN or an infinity in y has code 0x7F (NaN); a
  * NaN or an infinity in h reaches its own row alone: a NaN makes all of it NaN
  * (e8m0 scale codes 255), beside an infinity the finite values become 0.
  *   x bf16 [rows, dim]; residual the same or NULL (h = x); weight bf16 [dim] or
@@ -362,7 +363,8 @@ engram_status engram_norm_quant(const uint16_t* x, const uint16_t* residual,
 /* Beam search's selection: per sequence the W best of W * V continuations.
  *   score(w, v) = scores[w] + logits[w][v] - log sum_v' exp(logits[w][v'])
  * in order of falling score, equal scores by the lowest w * V + v; compared and
- * summed in 64 bits, new_scores rounded to fp32.
+ * summed in 64 bits (each exponential to 1e-10 of itself), new_scores rounded to
+ * fp32.
  *   logits   bf16 (logits_f32 = 0) or fp32 [B * W] rows of V, ld >= V elements
  *            apart; rows may start at any element.
  *   scores   fp32 [B, W]; a beam at -infinity is dead and offers nothing (the

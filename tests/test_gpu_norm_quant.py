@@ -175,6 +175,31 @@ def test_overflow_of_y_is_a_nan_code(ge, fmt):
           *ge.engram_norm_quant(x[:, :128].contiguous(), scale_format=fmt))
 
 
+def test_more_threads_than_a_launch_takes(ge):
+    """2^26 + 13 short rows, in several launches: each as in a call of a few."""
+    dev = torch.device("cuda:0")
+    period, times = 17, 3947581
+    say("norm launches", period * times)
+    x = torch.randn(period, 8, device=dev, generator=torch.Generator(device=dev).manual_seed(5)).bfloat16()
+    for fmt in ("e8m0_32", "f32_row"):
+        few_codes, few_scales, _ = ge.engram_norm_quant(x, scale_format=fmt)
+        codes = torch.full((period * times, 8), 0x7F, dtype=torch.uint8, device=dev)
+        scales = torch.full((period * times, 1), 99, dtype=few_scales.dtype, device=dev)
+        ge.engram_norm_quant(x.repeat(times, 1), scale_format=fmt, codes=codes, scales=scales)
+        assert bool((codes.view(times, period, 8) == few_codes).all())
+        assert bool((scales.view(times, period, 1) == few_scales).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_row_of_zeros_without_eps(ge, fmt):
+    dev = torch.device("cuda:0")
+    x = torch.zeros(2, 64, dtype=torch.bfloat16, device=dev)
+    x[1] = 1
+    codes, scales, _ = ge.engram_norm_quant(x, eps=0.0, scale_format=fmt)
+    assert bool((codes[0] == 0x7F).all()) and bool((codes[1] != 0x7F).all())
+    assert bool((scales[0] == 255).all() if fmt == "e8m0_32" else scales[0].isnan().all())
+
+
 def test_refusals(ge):
     dev = torch.device("cuda:0")
     x = torch.zeros(4, 64, dtype=torch.bfloat16, device=dev)

@@ -142,4 +142,8 @@ def test_binding_refuses_what_is_not_on_the_device():
         ge.engram_beam_select(torch.zeros(4, 64), torch.zeros(1, 4))
     with pytest.raises(ValueError):
         ge.engram_beam_reorder([torch.zeros(4, 2)], torch.zeros(1, 4, dtype=torch.int32))
+    layer = ge.EngramLayer.__new__(ge.EngramLayer)
+    with pytest.raises(ValueError):  # ids that no adapters go with
+        layer.forward(torch.zeros(1, 1, 4, 5120, dtype=torch.bfloat16), torch.zeros(1, 1),
+                      adapter_ids=torch.zeros(1, dtype=torch.int32))
     assert g.K == 1536
