@@ -23,15 +23,17 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// exp(x) for -700 <= x <= 0 in 64 bits, to 1e-10 relative; exp_near(0) is 1, a NaN
-// stays one.  2^t = 2^n * 2^f with n the nearest whole number, f
-// in [-1/2, 1/2] and 2^f = 1 + f P(f), P the polynomial that meets
-// (2^f - 1) / f at the seven Chebyshev points.  Adding 1.5 * 2^52 rounds t to n
-// and leaves n in the sum's low word, from where it goes into the exponent.
-__device__ __forceinline__ double exp_near(double x) {
-    constexpr double kLog2e = 1.4426950408889634074, kRound = 6755399441055744.0;
-    const double r = __builtin_fma(x, kLog2e, kRound);
-    const double f = __builtin_fma(x, kLog2e, -(r - kRound));
+// exp(x) 2^-N in 64 bits, to 1e-10 relative, for -700 <= x - N ln 2 <= 1 and |x| <=
+// 5000, with `round` = 1.5 * 2^52 - N; a NaN stays one.  2^t = 2^n * 2^f with n the
+// nearest whole number, f in [-1/2, 1/2] and 2^f = 1 + f P(f), P the polynomial
+// that meets (2^f - 1) / f at the seven Chebyshev points.  Adding `round` rounds t
+// to n and leaves n - N in the sum's low word, from where it goes into the
+// exponent.
+constexpr double kLog2e = 1.4426950408889634074, kLn2 = 0.69314718055994530942;
+constexpr double kRound = 6755399441055744.0;
+__device__ __forceinline__ double exp2_near(double x, double round) {
+    const double r = __builtin_fma(x, kLog2e, round);
+    const double f = __builtin_fma(x, kLog2e, -(r - round));
     double p = 1.5297323742797923e-05;
     p = __builtin_fma(p, f, 0.00015461444700206743);
     p = __builtin_fma(p, f, 0.001333350238623972);
@@ -43,12 +45,29 @@ __device__ __forceinline__ double exp_near(double x) {
     return __hiloint2double(__double2hiint(p) + (__double2loint(r) << 20), __double2loint(p));
 }
 
-// The same for any x <= 0: below -700 it is below 1e-304.
-__device__ __forceinline__ double exp_neg(double x) { return exp_near(fmax(x, -700.0)); }
+// exp(x) for any x <= 1: below -700 it is below 1e-304.
+__device__ __forceinline__ double exp_neg(double x) { return exp2_near(fmax(x, -700.0), kRound); }
+
+// What a sum of exponentials of logits up to `top` is relative to: 2^whole_of(top),
+// a power of two next to exp(top), so that a logit's term has the same bits
+// wherever its part begins and sums go from one power to another exactly; for
+// tops too large for exp2_near, exp(top).
+__device__ __forceinline__ bool has_whole(float top) { return fabsf(top) <= 4096.0f; }
+__device__ __forceinline__ double whole_of(float top) { return rint((double)top * kLog2e); }
+// its logarithm less top
+__device__ __forceinline__ double base_over(float top) {
+    return has_whole(top) ? __builtin_fma(whole_of(top), kLn2, -(double)top) : 0.0;
+}
+// a sum relative to `from`'s, relative to that of `to` >= from
+__device__ __forceinline__ double rebase(double sum, float from, float to) {
+    if (has_whole(from) && has_whole(to))
+        return ldexp(sum, (int)(whole_of(from) - whole_of(to)));
+    return sum * exp_neg(((double)from - (double)to) + (base_over(from) - base_over(to)));
+}
 
 // What one wave finds in its part of a row of logits.
 struct Partials {
-    double* sum;  // [parts] sum exp(logit - top)
+    double* sum;  // [parts] sum exp(logit), relative to top's power of two
     float* top;   // [parts] the part's largest logit; NaN: a NaN or +inf in it
 };
 
@@ -167,7 +186,7 @@ struct Row {
         if (whole(i, V)) raw = *reinterpret_cast<const uint4*>(src + column(i));
         return raw;
     }
-    __device__ void unpack(const uint4& raw, int64_t i, int V, float (&x)[VEC]) const {
+    __device__ void values(const uint4& raw, float (&x)[VEC]) const {
         const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
@@ -176,6 +195,9 @@ struct Row {
             else
                 x[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
         }
+    }
+    __device__ void unpack(const uint4& raw, int64_t i, int V, float (&x)[VEC]) const {
+        values(raw, x);
         if (whole(i, V)) return;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
@@ -202,19 +224,31 @@ __global__ void __launch_bounds__(64 * kWaves) beam_part_kernel(
     uint32_t* __restrict__ err) {
     constexpr int VEC = Row<T>::VEC, NL = E / VEC;
     const int64_t row = blockIdx.y;
-    if (finished && finished[row]) return;
+    // (both on their way at once)
+    const uint8_t fin = finished ? finished[row] : 0;
     const float c = cum[row];
-    if (!(c > -INFINITY && c < INFINITY)) return;  // offers nothing
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (fin || !(c > -INFINITY && c < INFINITY)) return;  // offers nothing
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int part = blockIdx.x * kWaves + wave;
     const Row<T> r(logits + row * ld);
     const int64_t first = (int64_t)part * NL * 64 + lane;
-    uint4 raw[NL];
     float v[NL][VEC];
+    if (r.column((int64_t)part * NL * 64) >= 0 && r.column((int64_t)(part + 1) * NL * 64) <= V) {
+        // all of it inside the row
+        const uint4* from = reinterpret_cast<const uint4*>(r.src + r.column(first));
+        uint4 raw[NL];
 #pragma unroll
-    for (int i = 0; i < NL; ++i) raw[i] = r.fetch(first + 64 * i, V);
+        for (int i = 0; i < NL; ++i) raw[i] = from[64 * i];
 #pragma unroll
-    for (int i = 0; i < NL; ++i) r.unpack(raw[i], first + 64 * i, V, v[i]);
+        for (int i = 0; i < NL; ++i) r.values(raw[i], v[i]);
+    } else {
+        uint4 raw[NL];
+#pragma unroll
+        for (int i = 0; i < NL; ++i) raw[i] = r.fetch(first + 64 * i, V);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) r.unpack(raw[i], first + 64 * i, V, v[i]);
+    }
     float m = -INFINITY, least = INFINITY;  // (both pass a NaN over)
 #pragma unroll
     for (int i = 0; i < NL; ++i)
@@ -223,28 +257,37 @@ __global__ void __launch_bounds__(64 * kWaves) beam_part_kernel(
             m = fmaxf(m, v[i][e]);
             least = fminf(least, v[i][e]);
         }
+    float top = m;
+    for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
     double s = 0.0;
     bool bad = false;
-    if (__all(m < INFINITY && least - m >= -600.0f)) {
-        // the common case: nothing masked, nothing to clamp; a NaN comes through
-        const double md = m;
+    if (has_whole(top)) {
+        const double round = kRound - whole_of(top);
+        if (__all(least - top >= -600.0f)) {
+            // the common case: nothing masked, nothing to clamp; a NaN comes through
 #pragma unroll
-        for (int i = 0; i < NL; ++i)
+            for (int i = 0; i < NL; ++i)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) s += exp_near((double)v[i][e] - md);
-        bad = s != s;
+                for (int e = 0; e < VEC; ++e) s += exp2_near((double)v[i][e], round);
+            bad = s != s;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    bad |= !(v[i][e] < INFINITY);
+                    s += exp2_near((double)fmaxf(v[i][e], top - 700.0f), round);
+                }
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < NL; ++i)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 bad |= !(v[i][e] < INFINITY);
-                if (m > -INFINITY) s += exp_neg((double)v[i][e] - (double)m);
+                if (top > -INFINITY) s += exp_neg((double)v[i][e] - (double)top);
             }
     }
-    float top = m;
-    for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-    if (m > -INFINITY) s *= exp_neg((double)m - (double)top);
     for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
     bad = __any(bad);
     if (lane == 0) {
@@ -330,10 +373,10 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(
                     bad |= t[i] != t[i];
                     nm = fmaxf(nm, t[i]);
                 }
-                if (m > -INFINITY) s *= exp_neg((double)m - (double)nm);
+                if (m > -INFINITY) s = rebase(s, m, nm);
 #pragma unroll
                 for (int i = 0; i < AT; ++i)
-                    if (t[i] > -INFINITY) s += x[i] * exp_neg((double)t[i] - (double)nm);
+                    if (t[i] > -INFINITY) s += rebase(x[i], t[i], nm);
                 m = nm;
                 p0 += 64 * AT;
                 if (p0 - lane >= parts) break;
@@ -341,10 +384,12 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(
             }
             all = m;
             for (int o = 1; o < 64; o <<= 1) all = fmaxf(all, __shfl_xor(all, o, 64));
-            if (m > -INFINITY) s *= exp_neg((double)m - (double)all);
+            if (m > -INFINITY) s = rebase(s, m, all);
             for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
             if (!__any(bad) && all > -INFINITY) {
-                lo = log(s);
+                // in steps of 2^-36: rows of the same logits that lie differently
+                // are summed in another order, and are to tie all the same
+                lo = rint((log(s) + base_over(all)) * 0x1p36) * 0x1p-36;
                 if (m > -INFINITY) group = fmax(group, score_of(c, all, lo, m));
             }
         }

@@ -363,8 +363,8 @@ engram_status engram_norm_quant(const uint16_t* x, const uint16_t* residual,
 /* Beam search's selection: per sequence the W best of W * V continuations.
  *   score(w, v) = scores[w] + logits[w][v] - log sum_v' exp(logits[w][v'])
  * in order of falling score, equal scores by the lowest w * V + v; compared and
- * summed in 64 bits (each exponential to 1e-10 of itself), new_scores rounded to
- * fp32.
+ * summed in 64 bits (each exponential to 1e-10 of itself, the log sum in steps of
+ * 2^-36), new_scores rounded to fp32.
  *   logits   bf16 (logits_f32 = 0) or fp32 [B * W] rows of V, ld >= V elements
  *            apart; rows may start at any element.
  *   scores   fp32 [B, W]; a beam at -infinity is dead and offers nothing (the

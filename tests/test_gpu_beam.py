@@ -251,6 +251,19 @@ def test_flat_rows_at_any_score(ge, B, W, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V", [1001, 32003])
+def test_beams_of_the_same_logits_tie(ge, dtype, V):
+    """Rows that start at different places of a 16-byte line, the same in each."""
+    dev = torch.device("cuda:0")
+    B, W = 4, 5
+    say("beam same rows", V, dtype)
+    x, _ = draw(dev, B, 1, V, dtype, V)
+    x = x.view(B, 1, V).expand(B, W, V).reshape(B * W, V).contiguous()
+    c = torch.full((B, W), -1.25, device=dev)
+    check(ge.engram_beam_select(x, c), x, c)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 def test_nearly_flat_rows(ge, dtype):
     dev = torch.device("cuda:0")
     B, W, V = 2, 4, 5000
