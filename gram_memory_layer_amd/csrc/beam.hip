@@ -213,10 +213,11 @@ struct Row {
     }
 };
 
-// One wave a part: 64 lanes of E logits, E / VEC pieces of 64 lanes.  Each lane
-// sums against its own largest logit; the lanes meet at the end.  (512 rows of
-// 129,280: fp32 52 us, 5.1 TB/s, bound by memory; bf16 54 us, bound by the 64-bit
-// instructions of the exponentials, 13 a logit.)
+// One wave a part: 64 lanes of E logits, E / VEC pieces of 64 lanes.  (512 rows of
+// 129,280: fp32 46-50 us, 5.3-5.8 TB/s, bound by memory; bf16 49 us, bound by the
+// 64-bit instructions of the exponentials, 13 a logit.  Parts of twice the length,
+// or a wave that goes through several with the next one's loads ahead, gain
+// nothing: 55 and 57 us a bf16 call against 54.)
 template <class T, int E>
 __global__ void __launch_bounds__(64 * kWaves) beam_part_kernel(
     const T* __restrict__ logits, int64_t ld, const float* __restrict__ cum,
@@ -651,7 +652,7 @@ struct Column<4> {
 // state[b][w] = state[b][parents[b][w]], in place: a thread owns one column of
 // all W rows of a sequence, reads every row's parent, then writes the rows
 // that change.  No other thread touches its column.  Memory bounds it (two states
-// of 8 x 8 rows of 4 MiB: 155 us, 5.3 TB/s read and written); stores with the
+// of 8 x 8 rows of 4 MiB: 151 us, 5.3 TB/s read and written); stores with the
 // nontemporal hint (64 x 8 rows of 40 KiB, 8 states: 52.8 -> 43.0 us).  Loading
 // only the rows that move, behind a branch each, serialises the loads and
 // doubles the time.
