@@ -515,6 +515,199 @@ hipError_t run_rows(const uint16_t* a, const uint16_t* w, const AddAdapters& ad,
     return hipGetLastError();
 }
 
+// The projection with adapters for a few tiles a compute unit: 128 x 128 tiles,
+// four waves of 64 x 64.  One workgroup a compute unit has nobody to hide its
+// loads behind, so its k-tiles arrive in a ring of NS stages, up to NS of them on
+// their way, each k-step's fragments are read beside the last one's products
+// (the next k-tile's first behind the one barrier of a k-tile), and the pairs
+// have LDS of their own and come with the first k-tile.  (613 positions of 1536 ->
+// 6168, 245 tiles: 22.5 us with adapters of rank 8, 19.4 without any; 13.7 of
+// them the 24 k-tiles, whose LDS traffic, 96 KB each with what arrives, takes
+// 7.7 at the least.  With two stages, which cannot hide a load: 25.7 us; with the
+// ring alone, each k-step's reads before its products: 25.2.)
+constexpr int kTile = 128, kStages = 4;
+__device__ __forceinline__ void adapter_tile(const uint16_t* __restrict__ a,
+                                             const uint16_t* __restrict__ w, const AddAdapters& ad,
+                                             int M, int N, int K, uint16_t* __restrict__ kv,
+                                             int tiles_m, int tiles_n, int per_xcd,
+                                             uint8_t* smem) {
+    constexpr int BT = kTile, NS = kStages, STAGE = 2 * BT * 128, NLD = BT / 8 / 4;
+    int mt, nt;
+    if (!tile_of(blockIdx.x, per_xcd, tiles_m, tiles_n, &mt, &nt)) return;
+    const int m0 = mt * BT, n0 = nt * BT;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1, lrow = lane & 31, lhalf = lane >> 5;
+    uint8_t* const pairs = smem + NS * STAGE;
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a, (uint32_t)(M * K * 2));
+    const __amdgpu_buffer_rsrc_t rw =
+        make_rsrc(w + (int64_t)n0 * K, (uint32_t)(min(BT, N - n0) * K * 2));
+    int2 own[2];  // position and adapter of rows m0 + 64 k + lane
+#pragma unroll
+    for (int k = 0; k < 2; ++k) own[k] = ad.tile[m0 + 64 * k + lane];
+    // instruction i of a wave fills rows 8 (4 i + wave) .. of an operand
+    uint32_t wo[NLD], ao[NLD];
+#pragma unroll
+    for (int i = 0; i < NLD; ++i) {
+        const int row = (4 * i + wave) * 8 + (lane >> 3);
+        wo[i] = (uint32_t)(row * K * 2 + slot128(row, lane & 7) * 16);
+    }
+    auto issue_w = [&](int kt, int stage) {
+        uint8_t* st = smem + stage * STAGE + BT * 128;
+#pragma unroll
+        for (int i = 0; i < NLD; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(st + (4 * i + wave) * 1024),
+                                                     16, wo[i], kt * 128, 0, 0);
+    };
+    auto issue_a = [&](int kt, int stage) {
+        uint8_t* st = smem + stage * STAGE;
+#pragma unroll
+        for (int i = 0; i < NLD; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + (4 * i + wave) * 1024),
+                                                     16, ao[i], kt * 128, 0, 0);
+    };
+    const int nk = K / 64;
+    // W first, which needs no positions
+#pragma unroll
+    for (int p = 0; p < NS; ++p)
+        if (p < nk) issue_w(p, p);
+#pragma unroll
+    for (int i = 0; i < NLD; ++i) {
+        const int row = (4 * i + wave) * 8 + (lane >> 3);
+        const int lo = __shfl(own[0].x, row & 63, 64), hi = __shfl(own[1].x, row & 63, 64);
+        ao[i] = (uint32_t)(row < 64 ? lo : hi) * (uint32_t)(K * 2) +
+                (uint32_t)(slot128(row, lane & 7) * 16);
+    }
+    if (any_adapter(own)) load_pairs<BT, 4>(ad, own, M, wave, lane, 0, pairs);
+#pragma unroll
+    for (int p = 0; p < NS; ++p)
+        if (p < nk) issue_a(p, p);
+
+    f32x16 acc[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[j][i][v] = 0.0f;
+    bf16x8 fa[2][2], fw[2][2];
+    auto read = [&](int stage, int ks, int to) {
+        const uint8_t* st = smem + stage * STAGE;
+        const int c = 2 * ks + lhalf;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int ar = wm * 64 + i * 32 + lrow, wr = wn * 64 + i * 32 + lrow;
+            fa[to][i] = *reinterpret_cast<const bf16x8*>(st + ar * 128 + slot128(ar, c) * 16);
+            fw[to][i] =
+                *reinterpret_cast<const bf16x8*>(st + BT * 128 + wr * 128 + slot128(wr, c) * 16);
+        }
+    };
+    auto multiply = [&](int from) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fw[from][j], fa[from][i],
+                                                                    acc[j][i], 0, 0, 0);
+        // the next fragments' reads between them
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // A k-tile has landed once only what was issued behind its last load is on
+    // its way.  (The first NS had their W ahead of every A.)
+    static_assert(NS == 4, "the waits below");
+    if (nk >= 4)
+        arrived<3 * NLD>();
+    else
+        arrived<0>();
+    read(0, 0, 0);
+    int stage = 0;
+    for (int kt = 0; kt < nk; ++kt) {
+        const int after = (stage + 1) & (NS - 1);
+        read(stage, 1, 1);
+        multiply(0);
+        read(stage, 2, 0);
+        multiply(1);
+        read(stage, 3, 1);
+        multiply(0);
+        if (kt + 1 < nk) {
+            // k-tile kt + 1 is there, behind the barrier for everyone, and this
+            // one's stage is free
+            if (kt < 2) {
+                if (kt == 0 && nk >= 4)
+                    arrived<2 * NLD>();
+                else if (kt == 1 && nk >= 5)
+                    arrived<3 * NLD>();
+                else
+                    arrived<0>();
+            } else if (kt + 3 < nk) {
+                arrived<4 * NLD>();
+            } else if (kt + 3 == nk) {
+                arrived<2 * NLD>();
+            } else {
+                arrived<0>();
+            }
+            if (kt + NS < nk) {
+                issue_w(kt + NS, stage);
+                issue_a(kt + NS, stage);
+            }
+            read(after, 0, 0);
+        }
+        multiply(1);
+        stage = after;
+    }
+    __syncthreads();
+    add_tile<BT, 4, 2, 2>(ad, acc, own, M, n0, N, wm, wn, wave, lane, pairs, smem);
+
+    // a wave's 64 x 64 block as bf16 rows through LDS, so that 8 lanes store a
+    // position's 128 bytes
+    uint8_t* ep = smem + STAGE + wave * 8192;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int r = i * 32 + lrow, ch = (4 * j + g) ^ (r & 7);
+                *reinterpret_cast<uint2*>(ep + r * 128 + ch * 16 + lhalf * 8) =
+                    make_uint2(pack_bf16(acc[j][i][4 * g], acc[j][i][4 * g + 1]),
+                               pack_bf16(acc[j][i][4 * g + 2], acc[j][i][4 * g + 3]));
+            }
+    const int rsub = lane >> 3, csub = lane & 7, n = n0 + wn * 64 + csub * 8;
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+        const int r = it * 8 + rsub;
+        const uint4 v =
+            *reinterpret_cast<const uint4*>(ep + r * 128 + ((csub ^ (r & 7)) << 4));
+        const int lo = __shfl(own[0].x, r, 64), hi = __shfl(own[1].x, r, 64);
+        if (m0 + wm * 64 + r < M && n < N)
+            *reinterpret_cast<uint4*>(kv + (int64_t)(wm ? hi : lo) * N + n) = v;
+    }
+}
+
+__global__ void __launch_bounds__(256, 1) adapter_tile_kernel(const uint16_t* __restrict__ a,
+                                                              const uint16_t* __restrict__ w,
+                                                              const AddAdapters ad, int M, int N,
+                                                              int K, uint16_t* __restrict__ kv,
+                                                              int tiles_m, int tiles_n,
+                                                              int per_xcd) {
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[kStages * 2 * kTile * 128 + kTile * 256];
+    adapter_tile(a, w, ad, M, N, K, kv, tiles_m, tiles_n, per_xcd, smem);
+}
+
+hipError_t run_tiles(const uint16_t* a, const uint16_t* w, const AddAdapters& ad, int M, int N,
+                     int K, uint16_t* kv, hipStream_t s) {
+    const int tiles_m = (M + kTile - 1) / kTile, tiles_n = (N + kTile - 1) / kTile;
+    const int per_xcd = (tiles_m * tiles_n + N_XCD - 1) / N_XCD;
+    adapter_tile_kernel<<<dim3(per_xcd * N_XCD), dim3(256), 0, s>>>(a, w, ad, M, N, K, kv, tiles_m,
+                                                                    tiles_n, per_xcd);
+    return hipGetLastError();
+}
+
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // Positions of one launch: the tiles address the positions and the pairs with
@@ -543,18 +736,31 @@ hipError_t launch_wkv_adapters(const uint16_t* a, const uint16_t* w, const Adapt
         const uint16_t* am = a + m0 * K;
         uint16_t *um = u + m0 * rp * 2, *kvm = kv + m0 * N;
         // the decode kernel as long as two of its workgroups a compute unit take
-        // all at once (613 positions of 1536 -> 2560: 22 us against 33 with the
-        // tiles; 128 of -> 25600, twice too many: 45 either way)
-        const int tn = (N + 63) / 64;
-        const bool rows = K % 64 == 0 && (int64_t)K * 2 * 64 < (1ll << 31) &&
-                          (m <= 64 || (int64_t)((m + 63) / 64) * tn <= 2 * cu_count());
+        // all at once (128 positions of rank 16 -> 6168: 18 us against 26 with the
+        // tiles; 128 of -> 25600, twice too many: 41 against 35), or one, where the
+        // products of a high rank on the vector units would take longer than the
+        // tiles' on the matrix cores (512 of rank 64 -> 2560: 38 against 30; 384,
+        // one workgroup each: 25 against 30)
+        const int64_t tn = (N + 63) / 64, blocks = (int64_t)((m + 63) / 64) * tn;
+        const bool rows =
+            K % 64 == 0 && (int64_t)K * 2 * 64 < (1ll << 31) &&
+            (m <= 64 || blocks <= (ad.rank > 32 && m >= 256 ? 1 : 2) * (int64_t)cu_count());
+        // the ring of tiles where they all run at once (613 of rank 8 -> 6168: 22.5 us
+        // the kernel against 25.7 of the projection's own tiles; 800, two rounds: 42
+        // us the call against 33, there two workgroups of the latter share a
+        // compute unit)
+        const bool ring = K % 64 == 0 && (int64_t)K * 2 * kTile < (1ll << 31) &&
+                          (int64_t)((m + kTile - 1) / kTile) * ((N + kTile - 1) / kTile) <=
+                              cu_count();
         int2* order = rows ? nullptr : tile + m0;
         AddAdapters add{ad.up, um, ids, nullptr, m0, ad.n, ad.rank, rp, seg,
                         (int64_t)N * ad.rank};
         hipError_t e = run_down(am, ad, add, m, K, um, order, err, s);
         if (e != hipSuccess) return e;
         add.tile = order;
-        if (!rows)
+        if (!rows && ring)
+            e = run_tiles(am, w, add, m, N, K, kvm, s);
+        else if (!rows)
             e = launch_wkv_added(am, w, m, N, K, add, kvm, s);
         else if (m <= 16)
             e = run_rows<1, 6>(am, w, add, m, N, K, kvm, s);

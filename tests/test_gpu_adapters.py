@@ -96,6 +96,12 @@ CASES = [
     # mid-sized batches on both sides of the decode kernel's share of the machine
     (600, 264, 1, 4, 64, 8, 16, "random"), (613, 2056, 2, 24, 64, 5, 8, "spans"),
     (200, 5120, 1, 4, 64, 30, 24, "random"), (400, 5120, 2, 2, 64, 7, 112, "random"),
+    # a 128 x 128 tile a compute unit: every count of k-tiles that the ring starts and ends with
+    (65, 5120, 4, 1, 64, 3, 16, "spans"), (127, 5120, 4, 2, 64, 4, 40, "random"),
+    (128, 5120, 4, 3, 64, 8, 8, "each"), (100, 5120, 4, 4, 64, 2, 128, "random"),
+    (81, 5120, 4, 5, 64, 30, 16, "each"), (113, 5120, 4, 6, 64, 5, 72, "spans"),
+    (128, 5000, 4, 7, 64, 128, 24, "each"), (90, 5120, 4, 24, 64, 6, 64, "none"),
+    (613, 1544, 3, 9, 64, 8, 64, "random"), (512, 1280, 1, 4, 64, 8, 64, "each"),
     # more adapters than the order has buckets
     (1500, 136, 1, 2, 64, 2100, 8, "each"), (2100, 136, 1, 2, 64, 2000, 16, "random"),
 ]
@@ -124,11 +130,11 @@ def test_projection_with_adapters(ge, case):
     assert torch.equal(again.view(torch.int16), kv[:M].view(torch.int16))  # the same on every run
 
 
-@pytest.mark.parametrize("M", [5, 64, 70, 1050])
-def test_another_requests_weights_do_not_reach_a_position(ge, M):
+@pytest.mark.parametrize("M,dim,hc", [(5, 136, 1), (64, 136, 1), (70, 136, 1), (1050, 136, 1), (100, 5120, 4)])
+def test_another_requests_weights_do_not_reach_a_position(ge, M, dim, hc):
     dev = torch.device("cuda:0")
-    say("adapter isolation", M)
-    g = geometry(ge, 136, 1, 4)
+    say("adapter isolation", M, dim, hc)
+    g = geometry(ge, dim, hc, 4)
     a, w, down, up, scale, ids = inputs(dev, M, g.N, g.K, 4, 16, "random", 5)
     want = ge.engram_wkv_adapters(g, ge.Adapters(down, up, scale), a, w, ids)
     down, up, a = down.clone(), up.clone(), a.clone()
