@@ -8,8 +8,11 @@
 //   fp32 (groups of 128, or the row): scale = amax / 448;
 //   code = e4m3(y / scale), round to nearest even.
 //
-// h, the sum of squares, y and the scale are fp32; the norm is taken of h
-// before it is rounded for `total` (one rounding for each output).
+// h, the squares, y and the scale are fp32; the norm is taken of h before it is
+// rounded for `total` (one rounding for each output).  An e8m0 scale is a step of
+// two: where fp32's roundings could decide it, 64 bits do.
+#include <type_traits>
+
 #include "internal.h"
 
 namespace engram {
@@ -54,7 +57,7 @@ __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
 
 // One workgroup a row; thread t holds the 8-value chunks t, t + nthr, ... from
 // the loads to the codes, so every byte is moved once: memory bounds it (16384
-// rows of 5120 with a residual, 587 MB: 99 us, 5.9 TB/s), next to the vector
+// rows of 5120 with a residual, 587 MB: 100 us, 5.9 TB/s), next to the vector
 // instructions, about ten a value.  They are kept few: h * weight is formed
 // once, the maximum is taken of it, and one factor (rstd over the group's
 // scale) goes on top.  The outputs are stored with the nontemporal hint
@@ -64,8 +67,10 @@ template <int NCH, int SC>
 __global__ void __launch_bounds__(1024) norm_quant_kernel(
     const uint16_t* x, const uint16_t* res, const uint16_t* __restrict__ weight, int dim,
     float eps, uint16_t* total, uint8_t* __restrict__ codes, void* __restrict__ scales,
-    int64_t row0) {
-    __shared__ float red[2][16];
+    int64_t row0, double per_dim, int kept) {
+    extern __shared__ u32x4 keep[];  // [dim / 8] of the input that total replaces
+    __shared__ std::conditional_t<SC == SCALE_E8M0_32, double, float> sums[16];
+    __shared__ float tops[16];
     const int tid = threadIdx.x, nthr = blockDim.x, d8 = dim / 8;
     const int lane = tid & 63, wave = tid >> 6, nw = nthr >> 6;
     const int64_t row = row0 + blockIdx.x;
@@ -77,6 +82,7 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(
         if (c < d8) {
             hx[i] = *reinterpret_cast<const u32x4*>(x + row * dim + c * 8);
             if (res) hr[i] = *reinterpret_cast<const u32x4*>(res + row * dim + c * 8);
+            if (kept) keep[c] = kept & 1 ? hx[i] : hr[i];
         }
     }
     float y[NCH][8];
@@ -130,22 +136,26 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(
     float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) top = fmaxf(top, amax[i]);
+    // (the threads' sums meet in 64 bits where they decide an e8m0 scale)
+    typedef std::conditional_t<SC == SCALE_E8M0_32, double, float> sum_t;
+    sum_t all = ss;
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) {
-        ss += __shfl_xor(ss, o, 64);
+        all += __shfl_xor(all, o, 64);
         if constexpr (SC == SCALE_F32_ROW) top = fmaxf(top, __shfl_xor(top, o, 64));
     }
     if (lane == 0) {
-        red[0][wave] = ss;
-        red[1][wave] = top;
+        sums[wave] = all;
+        tops[wave] = top;
     }
     __syncthreads();
-    ss = 0.0f;
+    all = 0;
     for (int w = 0; w < nw; ++w) {
-        ss += red[0][w];
-        if constexpr (SC == SCALE_F32_ROW) top = fmaxf(top, red[1][w]);
+        all += sums[w];
+        if constexpr (SC == SCALE_F32_ROW) top = fmaxf(top, tops[w]);
     }
-    const float rstd = rsqrtf(ss / (float)dim + eps);
+    const sum_t var = all * (sum_t)per_dim + (sum_t)eps;
+    const float rstd = rsqrtf((float)var);
 
     const int groups = SC == SCALE_E8M0_32 ? (dim + 31) / 32 : SC == SCALE_F32_128 ? (dim + 127) / 128 : 1;
 #pragma unroll
@@ -159,7 +169,38 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(
         const float lift = tiny ? 0x1p100f : 1.0f;
         float factor;
         if constexpr (SC == SCALE_E8M0_32) {
-            const uint32_t code = e8m0_code(most);
+            uint32_t code = e8m0_code(most);
+            // A maximum within 4 steps of fp32 of 448 times a power of two: which
+            // side of it, in 64 bits (the group's lanes come here together).
+            const uint32_t bits = __float_as_uint(most);
+            if ((bits & 0x7FFFFFu) - 0x5FFFFCu <= 8u) {
+                // x and the residual once more, from LDS where total is in their place
+                u32x4 ww = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+                u32x4 xx = {0, 0, 0, 0}, rr = {0, 0, 0, 0};
+                if (weight) ww = *reinterpret_cast<const u32x4*>(weight + c * 8);
+                if (kept & 1)
+                    xx = keep[c];
+                else
+                    xx = *reinterpret_cast<const u32x4*>(x + row * dim + c * 8);
+                if (kept & 2)
+                    rr = keep[c];
+                else if (res)
+                    rr = *reinterpret_cast<const u32x4*>(res + row * dim + c * 8);
+                double wide = 0.0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const double lo = (double)lo_f(xx[e]) + (double)lo_f(rr[e]);
+                    const double hi = (double)hi_f(xx[e]) + (double)hi_f(rr[e]);
+                    wide = fmax(wide, fmax(fabs(lo * (double)lo_f(ww[e])),
+                                           fabs(hi * (double)hi_f(ww[e]))));
+                }
+                wide = fmax(wide, __shfl_xor(wide, 1, 64));
+                wide = fmax(wide, __shfl_xor(wide, 2, 64));
+                const double r = rstd;  // one step from it to 1 / sqrt(var)
+                const uint32_t edge = (bits & 0xFF800000u) | 0x600000u;
+                const bool in = wide * (r * (1.5 - 0.5 * (double)var * r * r)) <= (double)__uint_as_float(edge);
+                code = e8m0_code(__uint_as_float(in ? edge : edge + 1));
+            }
             factor = e8m0_inverse(code);
             if (tiny) factor *= 0x1p-100f;
             if (c % 4 == 0) ((uint8_t*)scales)[row * groups + c / 4] = (uint8_t)(most == most ? code : 255u);
@@ -192,11 +233,12 @@ hipError_t run(const uint16_t* x, const uint16_t* res, const uint16_t* weight, i
     auto k = nch == 1   ? norm_quant_kernel<1, SC>
              : nch == 2 ? norm_quant_kernel<2, SC>
                         : norm_quant_kernel<4, SC>;
+    const int kept = SC != SCALE_E8M0_32 || !total ? 0 : (total == x ? 1 : 0) | (total == res ? 2 : 0);
     const int64_t most = ((int64_t)1 << 31) / nthr;  // a launch has fewer than 2^32 threads
     for (int64_t r0 = 0; r0 < rows; r0 += most) {
         const int64_t n = rows - r0 < most ? rows - r0 : most;
-        k<<<dim3((uint32_t)n), dim3(nthr), 0, s>>>(x, res, weight, dim, eps, total, codes, scales,
-                                                   r0);
+        k<<<dim3((uint32_t)n), dim3(nthr), kept ? dim * 2 : 0, s>>>(x, res, weight, dim, eps, total, codes, scales,
+                                                   r0, 1.0 / dim, kept);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

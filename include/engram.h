@@ -341,7 +341,8 @@ engram_status engram_forward_adapted(const engram_geometry* g, const engram_hash
  * in fp32, each output rounded once (to nearest even).  The scales:
  *   ENGRAM_SCALE_E8M0_32   uint8 [rows, ceil(dim/32)]: for each 32 values the
  *                          smallest code c >= 0 with max |y| <= 448 * 2^(c-127)
- *                          (the embedding table's format);
+ *                          (the embedding table's format; where fp32's roundings
+ *                          could decide the code, 64 bits do);
  *   ENGRAM_SCALE_F32_128   fp32 [rows, ceil(dim/128)]: max |y| / 448 of 128 values;
  *   ENGRAM_SCALE_F32_ROW   fp32 [rows]: max |y| / 448 of the row.
  * The last group of a row may be short.  A group of zeros has scale code 0 (or

@@ -200,6 +200,43 @@ def test_a_row_of_zeros_without_eps(ge, fmt):
     assert bool((scales[0] == 255).all() if fmt == "e8m0_32" else scales[0].isnan().all())
 
 
+@pytest.mark.parametrize("dim", [64, 1032, 5120, 20488, 32768])
+def test_a_step_of_the_scale_is_decided_in_64_bits(ge, dim):
+    """eps puts a group's maximum within a few fp32 steps of 448 times a power of two.
+    h is whole numbers, so that its squares' sum is exact; what is left is 64-bit
+    rounding, 1e-12.  In place too."""
+    dev = torch.device("cuda:0")
+    g = torch.Generator(device=dev)
+    g.manual_seed(dim)
+    rows, near = 32, 0
+    whole = lambda: torch.randint(-6, 7, (rows, dim), generator=g, device=dev).bfloat16()  # noqa: E731
+    x, r = whole(), whole()
+    w = (1 + 0.1 * torch.randn(dim, generator=g, device=dev)).bfloat16()
+    h = x.double() + r.double()
+    ms, top = (h * h).mean(1), (h * w.double()).abs()
+    for row in range(rows):
+        say("norm step", dim, row)
+        m = top[row, :32].max().item()
+        lim = 1.75 * 2.0 ** np.floor(np.log2(0.9 * m / ms[row].item() ** 0.5 / 1.75))
+        at = (m / lim) ** 2 - ms[row].item()
+        if at <= 0:
+            continue
+        for step in range(-3, 4):
+            eps = float(np.float32(at) + step * np.spacing(np.float32(at)))
+            y = torch.nn.functional.pad(top / torch.sqrt(ms + eps)[:, None], (0, -dim % 32))
+            y = torch.log2(y.reshape(rows, -1, 32).amax(2) / 448).cpu()
+            sure = (y - y.round()).abs() > 1e-12
+            want = (torch.ceil(y) + 127).to(torch.uint8)
+            near += int((y[row, 0] - y[row, 0].round()).abs() < 2.0 ** -21)
+            codes, scales, _ = ge.engram_norm_quant(x, w, residual=r, eps=eps)
+            assert torch.equal(scales.cpu()[sure], want[sure]), (row, step)
+            for inplace in (0, 1):
+                a, b = x.clone(), r.clone()
+                c2, s2, _ = ge.engram_norm_quant(a, w, residual=b, eps=eps, total=(a, b)[inplace])
+                assert torch.equal(s2, scales) and torch.equal(c2, codes), (row, step, inplace)
+    assert near > 50
+
+
 def test_refusals(ge):
     dev = torch.device("cuda:0")
     x = torch.zeros(4, 64, dtype=torch.bfloat16, device=dev)
