@@ -535,9 +535,21 @@ template <class D>
 hipError_t project(const uint16_t* a, const uint16_t* w, int64_t M, int N, int K, uint16_t* kv,
                    const D& ad, hipStream_t s) {
     if (M == 0) return hipSuccess;
-    if constexpr (D::on)
-        if (M < 1024 && K % BK == 0 && (int64_t)K * 2 * 256 < (1ll << 31))
-            return run_fast<128>(a, w, M, N, K, kv, N, ad, s);
+    if constexpr (D::on) {
+        // Two workgroups of 128 x 128 tiles share a compute unit: as many of them as
+        // compute units take 20 us (K = 1536), as many 256 x 256 tiles 50 us.  (1536
+        // -> 25600, rank 16: 500 positions 77 us with the small ones, 61 with the
+        // large, 600 78 and 102, 1000 129 and 106; -> 6168: 1024 positions 34 and 46.)
+        auto rounds = [&](int64_t t) {
+            const int64_t tiles = ((M + t - 1) / t) * ((N + t - 1) / t), cus = cu_count();
+            return (tiles + cus - 1) / cus;
+        };
+        if (K % BK == 0 && (int64_t)K * 2 * 256 < (1ll << 31)) {
+            if (2 * rounds(128) <= 5 * rounds(256))
+                return run_fast<128>(a, w, M, N, K, kv, N, ad, s);
+            return run_main(a, w, M, N, K, kv, ad, s);
+        }
+    }
     if (M >= 1024 && K % BK == 0 && (int64_t)K * 2 * 256 < (1ll << 31))
         return run_main(a, w, M, N, K, kv, ad, s);
     if (M >= 1024) return run<256, 256, 128, 64>(a, w, M, N, K, kv, ad, s);

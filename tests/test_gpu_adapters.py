@@ -102,6 +102,9 @@ CASES = [
     (81, 5120, 4, 5, 64, 30, 16, "each"), (113, 5120, 4, 6, 64, 5, 72, "spans"),
     (128, 5000, 4, 7, 64, 128, 24, "each"), (90, 5120, 4, 24, 64, 6, 64, "none"),
     (613, 1544, 3, 9, 64, 8, 64, "random"), (512, 1280, 1, 4, 64, 8, 64, "each"),
+    # on both sides of the large tiles
+    (300, 5120, 4, 2, 64, 5, 16, "random"), (600, 5120, 4, 1, 64, 9, 40, "each"),
+    (1030, 2056, 2, 3, 64, 4, 64, "random"), (450, 5000, 4, 3, 64, 450, 8, "each"),
     # more adapters than the order has buckets
     (1500, 136, 1, 2, 64, 2100, 8, "each"), (2100, 136, 1, 2, 64, 2000, 16, "random"),
 ]
