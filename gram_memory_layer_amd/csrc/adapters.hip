@@ -408,12 +408,13 @@ __device__ __forceinline__ void adapter_rows(const uint16_t* __restrict__ a,
     // The second product on the vector units: with an adapter for each position
     // the matrix cores have nothing to share, and going through the adapters one
     // by one costs 0.4 us each in scalar work (32 adapters of rank 16 at 64
-    // positions: 17 us beside the projection's 17, against 11 this way).  Here a lane takes one position and a few columns,
-    // whatever the other positions have: its pairs are in registers, its
-    // adapter's up rows come from LDS, and v_dot2_f32_bf16 adds two products in
-    // fp32.  The up rows of all distinct adapters arrive by DMA in the ring's
-    // memory, as many of the 64 columns a round as fit (the four waves split
-    // them); 16 bytes between two adapters spread equal rows over the banks.
+    // positions: 17 us beside the projection's 17, against 11 this way).  Here a
+    // lane takes one position and a few columns, whatever the other positions
+    // have: its pairs are in registers, its adapter's up rows come from LDS, and
+    // v_dot2_f32_bf16 adds two products in fp32.  The up rows of all distinct
+    // adapters arrive by DMA in the ring's memory, as many of the 64 columns a
+    // round as fit (the four waves split them); 16 bytes between two adapters
+    // spread equal rows over the banks.
     if (distinct) {
         // [position][SROW]
         float* sums = reinterpret_cast<float*>(smem + (early ? 0 : UPS));
