@@ -38,13 +38,16 @@ struct AddAdapters {
     int n, rank, rp, seg;
     int64_t up_stride;  // n_out * rank
 
+    __device__ __forceinline__ int raw(int64_t m) const {
+        return ids[seg == 1 ? first + m : (first + m) / seg];
+    }
     __device__ __forceinline__ int id_of(int64_t m) const {
-        const int j = ids[seg == 1 ? first + m : (first + m) / seg];
+        const int j = raw(m);
         return j >= 0 && j < n ? j : -1;
     }
     // whether position m's id is one that is neither an adapter nor -1
     __device__ __forceinline__ bool bad(int64_t m) const {
-        const int j = ids[seg == 1 ? first + m : (first + m) / seg];
+        const int j = raw(m);
         return j < -1 || j >= n;
     }
     // u's 8 ranks from r on, as hi or lo

@@ -26,10 +26,16 @@ __device__ __forceinline__ void order_positions(const AddAdapters& ad, int M, in
                                                 int (&wave_sum)[16]) {
     constexpr int PER = kBuckets / NT;  // buckets a thread
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    auto adapter = [&](int m) { return m < M ? ad.id_of(m) : -2; };  // -2: no position
+    bool bad = false;
+    auto adapter = [&](int m) {  // -2: no position
+        const int j = ad.raw(min(m, M - 1));
+        bad |= j < -1 || j >= ad.n;
+        return m >= M ? -2 : j >= 0 && j < ad.n ? j : -1;
+    };
+    auto bucket_of = [&](int j) { return j < 0 ? j + 1 : 1 + j % (kBuckets - 1); };
     // the place of a lane's position in its bucket, counted on from hist
     auto count = [&](int j) {
-        const int bucket = j < 0 ? j + 1 : 1 + j % (kBuckets - 1);
+        const int bucket = bucket_of(j);
         const int first = __builtin_amdgcn_readfirstlane(bucket);
         if (__all(bucket == first)) {
             int at = 0;
@@ -40,18 +46,14 @@ __device__ __forceinline__ void order_positions(const AddAdapters& ad, int M, in
     };
     constexpr int AT = 4;  // positions of a thread on their way
     const int end = (M + 63) / 64 * 64;  // (whole waves count)
-    bool bad = false;
+    int j[AT], at[AT];
     for (int i = tid; i < kBuckets; i += NT) hist[i] = 0;
     __syncthreads();
     for (int m = tid; m < end; m += AT * NT) {
-        int j[AT];
 #pragma unroll
         for (int x = 0; x < AT; ++x) j[x] = adapter(m + x * NT);
 #pragma unroll
-        for (int x = 0; x < AT; ++x) {
-            bad |= j[x] == -1 && ad.bad(m + x * NT);
-            count(j[x]);
-        }
+        for (int x = 0; x < AT; ++x) at[x] = count(j[x]);
     }
     if (bad && err) atomicOr(err, ENGRAM_ERRBIT_ADAPTER);
     __syncthreads();
@@ -67,21 +69,29 @@ __device__ __forceinline__ void order_positions(const AddAdapters& ad, int M, in
     if (lane == 63) wave_sum[wave] = sum;
     __syncthreads();
     int before = sum - mine;
-    for (int w = 0; w < wave; ++w) before += wave_sum[w];
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) before += w < wave ? wave_sum[w] : 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         hist[tid * PER + i] = before;
         before += own[i];
     }
     __syncthreads();
-    for (int m = tid; m < end; m += AT * NT) {
-        int j[AT];
-#pragma unroll
-        for (int x = 0; x < AT; ++x) j[x] = adapter(m + x * NT);
+    if (end <= AT * NT) {  // all of them still in registers
 #pragma unroll
         for (int x = 0; x < AT; ++x) {
-            const int at = count(j[x]);
-            if (m + x * NT < M) tile[at] = make_int2(m + x * NT, j[x]);
+            const int m = tid + x * NT;
+            if (m < M) tile[hist[bucket_of(j[x])] + at[x]] = make_int2(m, j[x]);
+        }
+    } else {
+        for (int m = tid; m < end; m += AT * NT) {
+#pragma unroll
+            for (int x = 0; x < AT; ++x) j[x] = adapter(m + x * NT);
+#pragma unroll
+            for (int x = 0; x < AT; ++x) {
+                const int to = count(j[x]);
+                if (m + x * NT < M) tile[to] = make_int2(m + x * NT, j[x]);
+            }
         }
     }
     for (int p = M + tid; p < (M + 255) / 256 * 256; p += NT) tile[p] = make_int2(M - 1, -1);
@@ -540,7 +550,7 @@ __device__ __forceinline__ void adapter_tile(const uint16_t* __restrict__ a,
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1, lrow = lane & 31, lhalf = lane >> 5;
     uint8_t* const pairs = smem + NS * STAGE;
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a, (uint32_t)(M * K * 2));
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a, (uint32_t)M * (uint32_t)K * 2u);
     const __amdgpu_buffer_rsrc_t rw =
         make_rsrc(w + (int64_t)n0 * K, (uint32_t)(min(BT, N - n0) * K * 2));
     int2 own[2];  // position and adapter of rows m0 + 64 k + lane
