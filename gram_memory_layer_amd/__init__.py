@@ -176,9 +176,12 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_Tensor = torch.Tensor
+
+
 def _dev(t, name, dtype, shape=None, device=None):
     # what nearly every call passes, in a few comparisons; the rest below says what is wrong
-    if (type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+    if (type(t) is _Tensor and t.is_cuda and t.dtype is dtype and t.is_contiguous()
             and (shape is None or t.shape == shape) and (device is None or t.device == device)):
         return t
     if not isinstance(t, torch.Tensor):
@@ -568,10 +571,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+# the current device, without the check that torch is initialised (a tensor is there)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _launch(name, fn, dev, *args):
     """Call a C entry on `dev`'s current stream, with `dev` the current device."""
     index = dev.index
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
@@ -698,8 +705,8 @@ def engram_norm_quant(x, weight=None, residual=None, eps=1e-6, scale_format="e8m
     if scale_format not in _SCALE_FORMATS:
         raise ValueError("scale_format must be one of %s" % ", ".join(_SCALE_FORMATS))
     _dev(x, "x", torch.bfloat16)
-    dev, shape = x.device, tuple(x.shape)
-    if x.dim() < 1 or shape[-1] == 0:
+    dev, shape = x.device, x.shape
+    if not shape or shape[-1] == 0:
         raise ValueError("x must be [..., dim]")
     dim = shape[-1]
     if weight is not None:
@@ -712,13 +719,15 @@ def engram_norm_quant(x, weight=None, residual=None, eps=1e-6, scale_format="e8m
         _dev(total, "total", torch.bfloat16, shape, dev)
     if codes is None:
         codes = torch.empty(shape, dtype=torch.uint8, device=dev)
-    _dev(codes, "codes", torch.uint8, shape, dev)
+    else:
+        _dev(codes, "codes", torch.uint8, shape, dev)
     group = 32 if scale_format == "e8m0_32" else 128 if scale_format == "f32_128" else dim
     kind = torch.uint8 if scale_format == "e8m0_32" else torch.float32
-    s_shape = shape[:-1] + ((dim + group - 1) // group,)
+    s_shape = (*shape[:-1], (dim + group - 1) // group)
     if scales is None:
         scales = torch.empty(s_shape, dtype=kind, device=dev)
-    _dev(scales, "scales", kind, s_shape, dev)
+    else:
+        _dev(scales, "scales", kind, s_shape, dev)
     _launch("engram_norm_quant", L.engram_norm_quant, dev, x.data_ptr(), _ptr(residual),
             _ptr(weight), x.numel() // dim, dim, float(eps), _SCALE_FORMATS[scale_format],
             _ptr(total), codes.data_ptr(), scales.data_ptr())
@@ -738,35 +747,45 @@ def engram_beam_select(logits, scores, finished=None, eos_id=-1, pad_id=0, token
     L = load()
     dev = logits.device
     _dev(scores, "scores", torch.float32, None, dev)
-    if scores.dim() != 2:
+    shape = scores.shape
+    if len(shape) != 2:
         raise ValueError("scores must be [B, W]")
-    B, W = shape = tuple(scores.shape)
-    if logits.device.type != "cuda":
-        raise ValueError("logits must be a device tensor (got %s)" % logits.device)
-    if logits.dtype not in (torch.float32, torch.bfloat16):
+    B, W = shape
+    if not logits.is_cuda:
+        raise ValueError("logits must be a device tensor (got %s)" % dev)
+    f32 = logits.dtype is torch.float32
+    if not f32 and logits.dtype is not torch.bfloat16:
         raise TypeError("logits must be torch.float32 or torch.bfloat16 (got %s)" % logits.dtype)
     V = logits.shape[-1] if logits.dim() else 0
-    if tuple(logits.shape) not in ((B * W, V), (B, W, V)):
+    if logits.shape != (B * W, V) and logits.shape != (B, W, V):
         raise ValueError("logits must be [B*W, V] or [B, W, V]")
-    ld = logits.stride(-2) if B * W > 1 else V
-    if logits.dim() == 3 and W == 1 and B > 1:
-        ld = logits.stride(0)
-    if (V > 1 and logits.stride(-1) != 1) or ld < V or (
-            logits.dim() == 3 and B > 1 and W > 1 and logits.stride(0) != W * ld):
+    stride = logits.stride()
+    ld = stride[-2] if B * W > 1 else V
+    if len(stride) == 3 and W == 1 and B > 1:
+        ld = stride[0]
+    if (V > 1 and stride[-1] != 1) or ld < V or (
+            len(stride) == 3 and B > 1 and W > 1 and stride[0] != W * ld):
         raise ValueError("logits must have contiguous rows, evenly apart")
     if finished is not None:
-        if finished.dtype == torch.bool:
+        if finished.dtype is torch.bool:
             finished = finished.view(torch.uint8)
         _dev(finished, "finished", torch.uint8, shape, dev)
-
-    def buf(t, name, dtype):
-        if t is None:
-            return torch.empty(shape, dtype=dtype, device=dev)
-        return _dev(t, name, dtype, shape, dev)
-    tokens = buf(tokens, "tokens", torch.int32)
-    parents = buf(parents, "parents", torch.int32)
-    new_scores = buf(new_scores, "new_scores", torch.float32)
-    new_finished = buf(new_finished, "new_finished", torch.uint8)
+    if tokens is None:
+        tokens = torch.empty(shape, dtype=torch.int32, device=dev)
+    else:
+        _dev(tokens, "tokens", torch.int32, shape, dev)
+    if parents is None:
+        parents = torch.empty(shape, dtype=torch.int32, device=dev)
+    else:
+        _dev(parents, "parents", torch.int32, shape, dev)
+    if new_scores is None:
+        new_scores = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        _dev(new_scores, "new_scores", torch.float32, shape, dev)
+    if new_finished is None:
+        new_finished = torch.empty(shape, dtype=torch.uint8, device=dev)
+    else:
+        _dev(new_finished, "new_finished", torch.uint8, shape, dev)
     if scratch is None:
         scratch = torch.empty(max(engram_beam_select_scratch_size(B, W, V), 1), dtype=torch.uint8,
                               device=dev)
@@ -774,7 +793,7 @@ def engram_beam_select(logits, scores, finished=None, eos_id=-1, pad_id=0, token
     if err is not None:
         _dev(err, "err", torch.int32, (1,), dev)
     _launch("engram_beam_select", L.engram_beam_select, dev, logits.data_ptr(),
-            int(logits.dtype == torch.float32), ld, scores.data_ptr(), _ptr(finished), B, W, V,
+            1 if f32 else 0, ld, scores.data_ptr(), _ptr(finished), B, W, V,
             int(eos_id), int(pad_id), tokens.data_ptr(), parents.data_ptr(),
             new_scores.data_ptr(), new_finished.data_ptr(), scratch.data_ptr(), scratch.numel(),
             _ptr(err))
