@@ -156,12 +156,25 @@ __global__ void __launch_bounds__(64 * kDownWaves) adapter_down_kernel(
     const int steps = K / 32, per = (steps + kDownWaves - 1) / kDownWaves;
     const int s0 = wave * per, s1 = min(steps, s0 + per);
     const uint16_t* am = a + (int64_t)m * K + 8 * quad;
+    // AT k-steps on their way (behind the last: that one again, unused); where
+    // they are all of this wave's, the workgroup of the first adapter fetches
+    // the positions' once, ahead of the ids
+    constexpr int AT = RT <= 4 ? 6 : 3;
+    bf16x8 fa[AT];
+    auto load_a = [&](int s) {
+#pragma unroll
+        for (int x = 0; x < AT; ++x)
+            fa[x] = *reinterpret_cast<const bf16x8*>(am + 32 * max(min(s + x, s1 - 1), 0));
+    };
+    const bool ahead = s1 - s0 <= AT && blockIdx.y == 0;
+    if (ahead) load_a(s0);
 
     uint32_t todo = (uint32_t)__ballot(mine >= 0) & 0xFFFFu;
     for (int turn = 0; todo; ++turn) {
         const int j = __builtin_amdgcn_readlane(mine, __builtin_ctz(todo));
         todo &= ~(uint32_t)__ballot(mine == j);
         if (turn % gridDim.y != blockIdx.y) continue;
+        const float sc = scale ? scale[j] : 1.0f;
         const uint16_t* dj = down + (int64_t)j * rank * K + 8 * quad;
         f32x4 acc[RT];
         const uint16_t* dr[RT];
@@ -170,14 +183,12 @@ __global__ void __launch_bounds__(64 * kDownWaves) adapter_down_kernel(
             acc[t] = f32x4{0, 0, 0, 0};
             dr[t] = dj + (int64_t)min(first_r + 16 * t + col, rank - 1) * K;
         }
-        // AT k-steps on their way (behind the last: that one again, unused)
-        constexpr int AT = RT <= 4 ? 6 : 3;
         for (int s = s0; s < s1; s += AT) {
-            bf16x8 fa[AT], fd[AT][RT];
+            bf16x8 fd[AT][RT];
+            if (!ahead) load_a(s);
 #pragma unroll
             for (int x = 0; x < AT; ++x) {
                 const int k = 32 * min(s + x, s1 - 1);
-                fa[x] = *reinterpret_cast<const bf16x8*>(am + k);
 #pragma unroll
                 for (int t = 0; t < RT; ++t) fd[x][t] = *reinterpret_cast<const bf16x8*>(dr[t] + k);
             }
@@ -196,7 +207,6 @@ __global__ void __launch_bounds__(64 * kDownWaves) adapter_down_kernel(
 #pragma unroll
             for (int v = 0; v < 4; ++v) part[wave][16 * t + 4 * quad + v][col] = acc[t][v];
         __syncthreads();
-        const float sc = scale ? scale[j] : 1.0f;
         // (mine is the same in every wave and quad: lane % 16 names the position)
         for (int l = tid >> 4; l < 16 * RT && first_r + l < rp; l += 4 * kDownWaves) {
             const int r = first_r + l;
