@@ -156,8 +156,9 @@ __device__ __forceinline__ void add_tile(const AddAdapters& ad, f32x16 (&acc)[TJ
                                          const int2 (&own)[BT / 64], int64_t M, int n0, int N,
                                          int wm, int wn, int wave, int lane, uint8_t* pairs,
                                          uint8_t* ups) {
-    constexpr int LB = BT / 32;  // DMA instructions of an adapter's group: 32 rows of 2 chunks
-    static_assert(LB % NW == 0, "DMA shares");
+    // DMA instructions of an adapter's group: 32 rows of 2 chunks
+    constexpr int LB = BT / 32, EACH = LB > NW ? LB / NW : 1;
+    static_assert(LB % NW == 0 || LB < NW, "DMA shares");
     const int lrow = lane & 31, lhalf = lane >> 5;
     if (!any_adapter(own)) return;
     for (int r0 = 0; r0 < ad.rp; r0 += 64) {
@@ -192,8 +193,9 @@ __device__ __forceinline__ void add_tile(const AddAdapters& ad, f32x16 (&acc)[TJ
                     make_rsrc(ad.up + j * ad.up_stride + (int64_t)n0 * ad.rank,
                               (uint32_t)(min(BT, N - n0) * ad.rank * 2));
 #pragma unroll
-                for (int i = 0; i < LB / NW; ++i) {
-                    const int seg = (LB / NW) * wave + i;
+                for (int i = 0; i < EACH; ++i) {
+                    const int seg = EACH * wave + i;
+                    if (LB < NW && seg >= LB) break;
                     const int row = seg * 32 + (lane >> 1);
                     const int c = slot_up(row, lane & 1);
                     for (int g = 0; g < groups; ++g) {

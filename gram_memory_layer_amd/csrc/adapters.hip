@@ -536,29 +536,30 @@ hipError_t run_rows(const uint16_t* a, const uint16_t* w, const AddAdapters& ad,
     return hipGetLastError();
 }
 
-// The projection with adapters for a few tiles a compute unit: 128 x 128 tiles,
-// four waves of 64 x 64.  One workgroup a compute unit has nobody to hide its
+// The projection with adapters for at most one tile a compute unit: 128 x 128
+// tiles, eight waves of 64 x 64, four for each half of a k-tile, whose sums meet
+// in LDS at the end.  One workgroup a compute unit has nobody to hide its
 // loads behind, so its k-tiles arrive in a ring of NS stages, up to NS of them on
 // their way, each k-step's fragments are read beside the last one's products
 // (the next k-tile's first behind the one barrier of a k-tile), and the pairs
 // have LDS of their own and come with the first k-tile.  (613 positions of 1536 ->
-// 6168, 245 tiles: 22.5 us with adapters of rank 8, 19.4 without any; 13.7 of
-// them the 24 k-tiles, whose LDS traffic, 96 KB each with what arrives, takes
-// 7.7 at the least.  With two stages, which cannot hide a load: 25.7 us; with the
-// ring alone, each k-step's reads before its products: 25.2.)
+// 6168, 245 tiles: 21.3 us with adapters of rank 8, 19.4 without any, of which
+// 5.7 are start and end; a k-tile takes 0.57 us for the 32 KB that it brings, 14
+// TB/s from the L2s in all.  Four waves for all of K: 22.5 us, the same without
+// adapters; its reads not ahead of the products: 25.2; two stages: 25.7.)
 constexpr int kTile = 128, kStages = 4;
 __device__ __forceinline__ void adapter_tile(const uint16_t* __restrict__ a,
                                              const uint16_t* __restrict__ w, const AddAdapters& ad,
                                              int M, int N, int K, uint16_t* __restrict__ kv,
                                              int tiles_m, int tiles_n, int per_xcd,
                                              uint8_t* smem) {
-    constexpr int BT = kTile, NS = kStages, STAGE = 2 * BT * 128, NLD = BT / 8 / 4;
+    constexpr int BT = kTile, NS = kStages, STAGE = 2 * BT * 128, NLD = BT / 8 / 8;
     int mt, nt;
     if (!tile_of(blockIdx.x, per_xcd, tiles_m, tiles_n, &mt, &nt)) return;
     const int m0 = mt * BT, n0 = nt * BT;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave >> 1, wn = wave & 1, lrow = lane & 31, lhalf = lane >> 5;
+    const int wm = (wave >> 1) & 1, wn = wave & 1, wk = wave >> 2, lrow = lane & 31, lhalf = lane >> 5;
     uint8_t* const pairs = smem + NS * STAGE;
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(a, (uint32_t)M * (uint32_t)K * 2u);
     const __amdgpu_buffer_rsrc_t rw =
@@ -570,21 +571,21 @@ __device__ __forceinline__ void adapter_tile(const uint16_t* __restrict__ a,
     uint32_t wo[NLD], ao[NLD];
 #pragma unroll
     for (int i = 0; i < NLD; ++i) {
-        const int row = (4 * i + wave) * 8 + (lane >> 3);
+        const int row = (8 * i + wave) * 8 + (lane >> 3);
         wo[i] = (uint32_t)(row * K * 2 + slot128(row, lane & 7) * 16);
     }
     auto issue_w = [&](int kt, int stage) {
         uint8_t* st = smem + stage * STAGE + BT * 128;
 #pragma unroll
         for (int i = 0; i < NLD; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(st + (4 * i + wave) * 1024),
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(st + (8 * i + wave) * 1024),
                                                      16, wo[i], kt * 128, 0, 0);
     };
     auto issue_a = [&](int kt, int stage) {
         uint8_t* st = smem + stage * STAGE;
 #pragma unroll
         for (int i = 0; i < NLD; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + (4 * i + wave) * 1024),
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + (8 * i + wave) * 1024),
                                                      16, ao[i], kt * 128, 0, 0);
     };
     const int nk = K / 64;
@@ -594,12 +595,12 @@ __device__ __forceinline__ void adapter_tile(const uint16_t* __restrict__ a,
         if (p < nk) issue_w(p, p);
 #pragma unroll
     for (int i = 0; i < NLD; ++i) {
-        const int row = (4 * i + wave) * 8 + (lane >> 3);
+        const int row = (8 * i + wave) * 8 + (lane >> 3);
         const int lo = __shfl(own[0].x, row & 63, 64), hi = __shfl(own[1].x, row & 63, 64);
         ao[i] = (uint32_t)(row < 64 ? lo : hi) * (uint32_t)(K * 2) +
                 (uint32_t)(slot128(row, lane & 7) * 16);
     }
-    if (any_adapter(own)) load_pairs<BT, 4>(ad, own, M, wave, lane, 0, pairs);
+    if (any_adapter(own)) load_pairs<BT, 8>(ad, own, M, wave, lane, 0, pairs);
 #pragma unroll
     for (int p = 0; p < NS; ++p)
         if (p < nk) issue_a(p, p);
@@ -645,15 +646,11 @@ __device__ __forceinline__ void adapter_tile(const uint16_t* __restrict__ a,
         arrived<3 * NLD>();
     else
         arrived<0>();
-    read(0, 0, 0);
+    read(0, 2 * wk, 0);
     int stage = 0;
     for (int kt = 0; kt < nk; ++kt) {
         const int after = (stage + 1) & (NS - 1);
-        read(stage, 1, 1);
-        multiply(0);
-        read(stage, 2, 0);
-        multiply(1);
-        read(stage, 3, 1);
+        read(stage, 2 * wk + 1, 1);
         multiply(0);
         if (kt + 1 < nk) {
             // k-tile kt + 1 is there, behind the barrier for everyone, and this
@@ -676,41 +673,68 @@ __device__ __forceinline__ void adapter_tile(const uint16_t* __restrict__ a,
                 issue_w(kt + NS, stage);
                 issue_a(kt + NS, stage);
             }
-            read(after, 0, 0);
+            read(after, 2 * wk, 0);
         }
         multiply(1);
         stage = after;
     }
     __syncthreads();
-    add_tile<BT, 4, 2, 2>(ad, acc, own, M, n0, N, wm, wn, wave, lane, pairs, smem);
-
-    // a wave's 64 x 64 block as bf16 rows through LDS, so that 8 lanes store a
-    // position's 128 bytes
-    uint8_t* ep = smem + STAGE + wave * 8192;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
+    // The two halves of K meet: a wave keeps 32 of its 64 columns, the other half
+    // of K's wave the others.
+    f32x16 sum[1][2];
+    {
+        uint8_t* mine = smem + wave * 8192 + lane * 16;
+        const uint8_t* other = smem + (wave ^ 4) * 8192 + lane * 16;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int r = i * 32 + lrow, ch = (4 * j + g) ^ (r & 7);
-                *reinterpret_cast<uint2*>(ep + r * 128 + ch * 16 + lhalf * 8) =
-                    make_uint2(pack_bf16(acc[j][i][4 * g], acc[j][i][4 * g + 1]),
-                               pack_bf16(acc[j][i][4 * g + 2], acc[j][i][4 * g + 3]));
-            }
-    const int rsub = lane >> 3, csub = lane & 7, n = n0 + wn * 64 + csub * 8;
+            for (int q = 0; q < 4; ++q) {
+                f32x4 x;
 #pragma unroll
-    for (int it = 0; it < 8; ++it) {
-        const int r = it * 8 + rsub;
+                for (int v = 0; v < 4; ++v)
+                    x[v] = wk ? acc[0][i][4 * q + v] : acc[1][i][4 * q + v];
+                *reinterpret_cast<f32x4*>(mine + (4 * i + q) * 1024) = x;
+            }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f32x4 x = *reinterpret_cast<const f32x4*>(other + (4 * i + q) * 1024);
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    sum[0][i][4 * q + v] =
+                        (wk ? acc[1][i][4 * q + v] : acc[0][i][4 * q + v]) + x[v];
+            }
+    }
+    const int wc = 2 * wn + wk;  // its 32 columns
+    add_tile<BT, 8, 2, 1>(ad, sum, own, M, n0, N, wm, wc, wave, lane, pairs, smem + 2 * STAGE);
+
+    // a wave's 64 x 32 block as bf16 rows through LDS, so that 4 lanes store a
+    // position's 64 bytes
+    uint8_t* ep = smem + 3 * STAGE + wave * 4096;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int r = i * 32 + lrow, ch = q ^ ((r >> 1) & 3);
+            *reinterpret_cast<uint2*>(ep + r * 64 + ch * 16 + lhalf * 8) =
+                make_uint2(pack_bf16(sum[0][i][4 * q], sum[0][i][4 * q + 1]),
+                           pack_bf16(sum[0][i][4 * q + 2], sum[0][i][4 * q + 3]));
+        }
+    const int rsub = lane >> 2, csub = lane & 3, n = n0 + wc * 32 + csub * 8;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int r = it * 16 + rsub;
         const uint4 v =
-            *reinterpret_cast<const uint4*>(ep + r * 128 + ((csub ^ (r & 7)) << 4));
+            *reinterpret_cast<const uint4*>(ep + r * 64 + ((csub ^ ((r >> 1) & 3)) << 4));
         const int lo = __shfl(own[0].x, r, 64), hi = __shfl(own[1].x, r, 64);
         if (m0 + wm * 64 + r < M && n < N)
             *reinterpret_cast<uint4*>(kv + (int64_t)(wm ? hi : lo) * N + n) = v;
     }
 }
 
-__global__ void __launch_bounds__(256, 1) adapter_tile_kernel(const uint16_t* __restrict__ a,
+__global__ void __launch_bounds__(512, 1) adapter_tile_kernel(const uint16_t* __restrict__ a,
                                                               const uint16_t* __restrict__ w,
                                                               const AddAdapters ad, int M, int N,
                                                               int K, uint16_t* __restrict__ kv,
@@ -724,7 +748,7 @@ hipError_t run_tiles(const uint16_t* a, const uint16_t* w, const AddAdapters& ad
                      int K, uint16_t* kv, hipStream_t s) {
     const int tiles_m = (M + kTile - 1) / kTile, tiles_n = (N + kTile - 1) / kTile;
     const int per_xcd = (tiles_m * tiles_n + N_XCD - 1) / N_XCD;
-    adapter_tile_kernel<<<dim3(per_xcd * N_XCD), dim3(256), 0, s>>>(a, w, ad, M, N, K, kv, tiles_m,
+    adapter_tile_kernel<<<dim3(per_xcd * N_XCD), dim3(512), 0, s>>>(a, w, ad, M, N, K, kv, tiles_m,
                                                                     tiles_n, per_xcd);
     return hipGetLastError();
 }
@@ -766,7 +790,7 @@ hipError_t launch_wkv_adapters(const uint16_t* a, const uint16_t* w, const Adapt
         const bool rows =
             K % 64 == 0 && (int64_t)K * 2 * 64 < (1ll << 31) &&
             (m <= 64 || blocks <= (ad.rank > 32 && m >= 256 ? 1 : 2) * (int64_t)cu_count());
-        // the ring of tiles where they all run at once (613 of rank 8 -> 6168: 22.5 us
+        // the ring of tiles where they all run at once (613 of rank 8 -> 6168: 21.3 us
         // the kernel against 25.7 of the projection's own tiles; 800, two rounds: 42
         // us the call against 33, there two workgroups of the latter share a
         // compute unit)
