@@ -85,7 +85,8 @@ def draw(dev, B, W, V, dtype, seed, ld=None):
 
 CASES = [(1, 1, 1), (1, 1, 2), (1, 4, 5), (2, 3, 7), (4, 1, 100), (3, 5, 1000), (1, 2, 511), (2, 4, 513),
          (2, 32, 4097), (5, 8, 2049), (1, 17, 8191), (1, 4, 129280), (3, 16, 20011), (40, 8, 32003),
-         (64, 4, 1000), (200, 7, 333), (64, 8, 20000), (1, 32, 40), (16, 32, 9000), (300, 1, 5000)]
+         (64, 4, 1000), (200, 7, 333), (64, 8, 20000), (1, 32, 40), (16, 32, 9000), (300, 1, 5000),
+         (300, 8, 7001), (100, 8, 20011)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
