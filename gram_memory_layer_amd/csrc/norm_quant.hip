@@ -8,11 +8,9 @@
 //   fp32 (groups of 128, or the row): scale = amax / 448;
 //   code = e4m3(y / scale), round to nearest even.
 //
-// h, the squares, y and the scale are fp32; the norm is taken of h before it is
-// rounded for `total` (one rounding for each output).  An e8m0 scale is a step of
+// h, the squares, y and the scale are fp32, in the order written; the norm is
+// taken of h before it is rounded for `total` (one rounding for each output).  An e8m0 scale is a step of
 // two: where fp32's roundings could decide it, 64 bits do.
-#include <type_traits>
-
 #include "internal.h"
 
 namespace engram {
@@ -58,18 +56,22 @@ __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
 // One workgroup a row; thread t holds the 8-value chunks t, t + nthr, ... from
 // the loads to the codes, so every byte is moved once: memory bounds it (16384
 // rows of 5120 with a residual, 587 MB: 100 us, 5.9 TB/s), next to the vector
-// instructions, about ten a value.  They are kept few: h * weight is formed
-// once, the maximum is taken of it, and one factor (rstd over the group's
-// scale) goes on top.  The outputs are stored with the nontemporal hint
-// (4096 rows: 32.2 -> 25.4 us); the same hint on the loads, and a wave a row
-// instead of a workgroup (no barrier, ten chunks a lane: 160 us), were slower.
+// instructions, about ten a value.  y is formed in the formula's order, so that
+// nothing leaves fp32's range that y does not leave, and y / scale is that
+// quotient, rounded as a division rounds it: a product with the inverse and a
+// correction, two more instructions a value (a power of two needs neither).  In
+// another order, or with the inverse alone, one of 10^4 values gets another
+// code: bf16 products put that many quotients halfway between two codes.  The
+// outputs are stored with the nontemporal hint (4096 rows: 32.2 -> 25.4 us); the
+// same hint on the loads, and a wave a row instead of a workgroup (no barrier,
+// ten chunks a lane: 160 us), were slower.
 template <int NCH, int SC>
 __global__ void __launch_bounds__(1024) norm_quant_kernel(
     const uint16_t* x, const uint16_t* res, const uint16_t* __restrict__ weight, int dim,
     float eps, uint16_t* total, uint8_t* __restrict__ codes, void* __restrict__ scales,
     int64_t row0, double per_dim, int kept) {
     extern __shared__ u32x4 keep[];  // [dim / 8] of the input that total replaces
-    __shared__ std::conditional_t<SC == SCALE_E8M0_32, double, float> sums[16];
+    __shared__ double sums[16];
     __shared__ float tops[16];
     const int tid = threadIdx.x, nthr = blockDim.x, d8 = dim / 8;
     const int lane = tid & 63, wave = tid >> 6, nw = nthr >> 6;
@@ -110,64 +112,68 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss += y[i][e] * y[i][e];
     }
-    // h * weight and its largest magnitude (a group's, or the row's)
-    float amax[NCH];
+    u32x4 ww[NCH];
+    if (weight)
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int c = tid + i * nthr;
+            ww[i] = u32x4{0, 0, 0, 0};
+            if (c < d8) ww[i] = *reinterpret_cast<const u32x4*>(weight + c * 8);
+        }
+    // (the threads' sums meet in 64 bits)
+    double all = ss;
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) all += __shfl_xor(all, o, 64);
+    if (lane == 0) sums[wave] = all;
+    __syncthreads();
+    all = 0;
+    for (int w = 0; w < nw; ++w) all += sums[w];
+    const double var = all * per_dim + (double)eps;
+    // rounded once: a step of Newton's from the approximate root, in 64 bits
+    float rstd = rsqrtf((float)var);
+    const bool usual = rstd > 0.0f && rstd < INFINITY;  // no NaN or infinity in h, not all 0 / 0
+    if (usual) rstd = (float)(rstd * (1.5 - 0.5 * var * rstd * rstd));
+
+    // y and its largest magnitude (a group's, or the row's; a NaN is passed over)
+    float amax[NCH], top = 0.0f;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-        const int c = tid + i * nthr;
-        if (weight) {
-            u32x4 ww = {0, 0, 0, 0};
-            if (c < d8) ww = *reinterpret_cast<const u32x4*>(weight + c * 8);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[i][e] *= rstd;
+        if (weight)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                y[i][2 * e] *= lo_f(ww[e]);
-                y[i][2 * e + 1] *= hi_f(ww[e]);
+                y[i][2 * e] *= lo_f(ww[i][e]);
+                y[i][2 * e + 1] *= hi_f(ww[i][e]);
             }
-        }
         amax[i] = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax[i] = fmaxf(amax[i], fabsf(y[i][e]));
+        if (!usual)  // a NaN here is h's: its group's scale is one too (below)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax[i] = y[i][e] == y[i][e] ? amax[i] : INFINITY;
         // a group is 4 or 16 consecutive chunks, so as many consecutive lanes
         if constexpr (SC != SCALE_F32_ROW)
 #pragma unroll
             for (int o = 1; o < (SC == SCALE_E8M0_32 ? 4 : 16); o <<= 1)
                 amax[i] = fmaxf(amax[i], __shfl_xor(amax[i], o, 64));
+        top = fmaxf(top, amax[i]);
     }
-    float top = 0.0f;
+    if constexpr (SC == SCALE_F32_ROW) {
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) top = fmaxf(top, amax[i]);
-    // (the threads' sums meet in 64 bits where they decide an e8m0 scale)
-    typedef std::conditional_t<SC == SCALE_E8M0_32, double, float> sum_t;
-    sum_t all = ss;
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
-        all += __shfl_xor(all, o, 64);
-        if constexpr (SC == SCALE_F32_ROW) top = fmaxf(top, __shfl_xor(top, o, 64));
+        for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+        if (lane == 0) tops[wave] = top;
+        __syncthreads();
+        for (int w = 0; w < nw; ++w) top = fmaxf(top, tops[w]);
     }
-    if (lane == 0) {
-        sums[wave] = all;
-        tops[wave] = top;
-    }
-    __syncthreads();
-    all = 0;
-    for (int w = 0; w < nw; ++w) {
-        all += sums[w];
-        if constexpr (SC == SCALE_F32_ROW) top = fmaxf(top, tops[w]);
-    }
-    const sum_t var = all * (sum_t)per_dim + (sum_t)eps;
-    const float rstd = rsqrtf((float)var);
 
     const int groups = SC == SCALE_E8M0_32 ? (dim + 31) / 32 : SC == SCALE_F32_128 ? (dim + 127) / 128 : 1;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
         const int c = tid + i * nthr;
         if (c >= d8) continue;
-        const float most = (SC == SCALE_F32_ROW ? top : amax[i]) * rstd;
-        // For a tiny maximum the factor would overflow: rstd and a power of two go
-        // to the values first (exact but for rstd's rounding).
-        const bool tiny = most < 0x1p-100f;
-        const float lift = tiny ? 0x1p100f : 1.0f;
-        float factor;
+        float most = SC == SCALE_F32_ROW ? top : amax[i];
+        if (!usual) most *= 0.0f;  // (an infinity: NaN)
         if constexpr (SC == SCALE_E8M0_32) {
             uint32_t code = e8m0_code(most);
             // A maximum within 4 steps of fp32 of 448 times a power of two: which
@@ -175,9 +181,9 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(
             const uint32_t bits = __float_as_uint(most);
             if ((bits & 0x7FFFFFu) - 0x5FFFFCu <= 8u) {
                 // x and the residual once more, from LDS where total is in their place
-                u32x4 ww = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+                u32x4 wt = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
                 u32x4 xx = {0, 0, 0, 0}, rr = {0, 0, 0, 0};
-                if (weight) ww = *reinterpret_cast<const u32x4*>(weight + c * 8);
+                if (weight) wt = ww[i];
                 if (kept & 1)
                     xx = keep[c];
                 else
@@ -191,32 +197,46 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(
                 for (int e = 0; e < 4; ++e) {
                     const double lo = (double)lo_f(xx[e]) + (double)lo_f(rr[e]);
                     const double hi = (double)hi_f(xx[e]) + (double)hi_f(rr[e]);
-                    wide = fmax(wide, fmax(fabs(lo * (double)lo_f(ww[e])),
-                                           fabs(hi * (double)hi_f(ww[e]))));
+                    wide = fmax(wide, fmax(fabs(lo * (double)lo_f(wt[e])),
+                                           fabs(hi * (double)hi_f(wt[e]))));
                 }
                 wide = fmax(wide, __shfl_xor(wide, 1, 64));
                 wide = fmax(wide, __shfl_xor(wide, 2, 64));
-                const double r = rstd;  // one step from it to 1 / sqrt(var)
                 const uint32_t edge = (bits & 0xFF800000u) | 0x600000u;
-                const bool in = wide * (r * (1.5 - 0.5 * (double)var * r * r)) <= (double)__uint_as_float(edge);
+                const double lim = (double)__uint_as_float(edge);
+                const bool in = wide * wide <= lim * lim * var;
                 code = e8m0_code(__uint_as_float(in ? edge : edge + 1));
             }
-            factor = e8m0_inverse(code);
-            if (tiny) factor *= 0x1p-100f;
+            const float inverse = e8m0_inverse(code);
             if (c % 4 == 0) ((uint8_t*)scales)[row * groups + c / 4] = (uint8_t)(most == most ? code : 255u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[i][e] *= inverse;
         } else {
-            factor = most > 0.0f ? 448.0f / (most * lift) : 0.0f;
+            const float scale = most / 448.0f;
             if (SC == SCALE_F32_128 ? c % 16 == 0 : c == 0)
-                ((float*)scales)[row * groups + (SC == SCALE_F32_128 ? c / 16 : 0)] = most / 448.0f;
-        }
-        if (tiny) {
+                ((float*)scales)[row * groups + (SC == SCALE_F32_128 ? c / 16 : 0)] = scale;
+            if (most >= 0x1p-100f || !(most > 0.0f)) {
+                // y / scale as a product with the inverse and one correction (by zeros
+                // where there is no scale: a finite y becomes 0)
+                const bool there = most > 0.0f && most < INFINITY;
+                const float by = there ? scale : 0.0f;
+                float inverse = __builtin_amdgcn_rcpf(scale);
+                inverse = there ? __builtin_fmaf(__builtin_fmaf(-scale, inverse, 1.0f), inverse, inverse) : 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[i][e] = y[i][e] * rstd * lift;
-        } else {
-            factor *= rstd;
-        }
+                for (int e = 0; e < 8; ++e) {
+                    const float q = y[i][e] * inverse;
+                    y[i][e] = __builtin_fmaf(__builtin_fmaf(-q, by, y[i][e]), inverse, q);
+                }
+            } else {
+                // the scale may be subnormal, and by rounding short of most / 448
+                const float by = scale * 0x1p100f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[i][e] *= factor;
+                for (int e = 0; e < 8; ++e) {
+                    const float q = by > 0.0f ? y[i][e] * 0x1p100f / by : y[i][e] * 0.0f;
+                    y[i][e] = q > 448.0f ? 448.0f : q < -448.0f ? -448.0f : q;
+                }
+            }
+        }
         const u32x2 o = {e4m3_codes(y[i][0], y[i][1], y[i][2], y[i][3]),
                          e4m3_codes(y[i][4], y[i][5], y[i][6], y[i][7])};
         __builtin_nontemporal_store(o, reinterpret_cast<u32x2*>(codes + row * dim + c * 8));

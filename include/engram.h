@@ -338,7 +338,8 @@ engram_status engram_forward_adapted(const engram_geometry* g, const engram_hash
  * row of dim values (for instance one stream of one position):
  *   h = x + residual;  total = bf16(h);
  *   y = h * rsqrt(mean(h^2) + eps) * weight;  codes = e4m3(y / scale),
- * in fp32, each output rounded once (to nearest even).  The scales:
+ * in fp32 and in that order, each output rounded once (to nearest even), the
+ * codes by the scale that is stored.  The scales:
  *   ENGRAM_SCALE_E8M0_32   uint8 [rows, ceil(dim/32)]: for each 32 values the
  *                          smallest code c >= 0 with max |y| <= 448 * 2^(c-127)
  *                          (the embedding table's format; where fp32's roundings
@@ -346,9 +347,11 @@ engram_status engram_forward_adapted(const engram_geometry* g, const engram_hash
  *   ENGRAM_SCALE_F32_128   fp32 [rows, ceil(dim/128)]: max |y| / 448 of 128 values;
  *   ENGRAM_SCALE_F32_ROW   fp32 [rows]: max |y| / 448 of the row.
  * The last group of a row may be short.  A group of zeros has scale code 0 (or
- * scale 0) and codes 0 (with eps = 0 a row of zeros is 0/0: all NaN).  A NaN or an infinity in y has code 0x7F (NaN); a
+ * scale 0) and codes 0, as has one whose fp32 scale rounds to 0 (with eps = 0 a
+ * row of zeros is 0/0: all NaN).  A NaN or an infinity in y has code 0x7F (NaN); a
  * NaN or an infinity in h reaches its own row alone: a NaN makes all of it NaN
- * (e8m0 scale codes 255), beside an infinity the finite values become 0.
+ * (e8m0 scale codes 255), beside an infinity the finite values become 0 (as
+ * they do where the squares' sum leaves fp32: values of about 2^60 and more).
  *   x bf16 [rows, dim]; residual the same or NULL (h = x); weight bf16 [dim] or
  *   NULL (1); total bf16 [rows, dim] or NULL, may be x or residual; codes uint8
  *   [rows, dim].  dim % 8 == 0, 8 <= dim <= 32768.  x, residual, weight and
