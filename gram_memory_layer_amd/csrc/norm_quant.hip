@@ -171,27 +171,29 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
         const int c = tid + i * nthr;
-        if (c >= d8) continue;
+        const bool there = c < d8;  // (lanes past a short group's end go along)
         float most = SC == SCALE_F32_ROW ? top : amax[i];
         if (!usual) most *= 0.0f;  // (an infinity: NaN)
         if constexpr (SC == SCALE_E8M0_32) {
             uint32_t code = e8m0_code(most);
             // A maximum within 4 steps of fp32 of 448 times a power of two: which
-            // side of it, in 64 bits (the group's lanes come here together).
+            // side of it, in 64 bits (the group's four lanes come here together).
             const uint32_t bits = __float_as_uint(most);
             if ((bits & 0x7FFFFFu) - 0x5FFFFCu <= 8u) {
                 // x and the residual once more, from LDS where total is in their place
                 u32x4 wt = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
                 u32x4 xx = {0, 0, 0, 0}, rr = {0, 0, 0, 0};
                 if (weight) wt = ww[i];
-                if (kept & 1)
-                    xx = keep[c];
-                else
-                    xx = *reinterpret_cast<const u32x4*>(x + row * dim + c * 8);
-                if (kept & 2)
-                    rr = keep[c];
-                else if (res)
-                    rr = *reinterpret_cast<const u32x4*>(res + row * dim + c * 8);
+                if (there) {
+                    if (kept & 1)
+                        xx = keep[c];
+                    else
+                        xx = *reinterpret_cast<const u32x4*>(x + row * dim + c * 8);
+                    if (kept & 2)
+                        rr = keep[c];
+                    else if (res)
+                        rr = *reinterpret_cast<const u32x4*>(res + row * dim + c * 8);
+                }
                 double wide = 0.0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -208,20 +210,21 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(
                 code = e8m0_code(__uint_as_float(in ? edge : edge + 1));
             }
             const float inverse = e8m0_inverse(code);
-            if (c % 4 == 0) ((uint8_t*)scales)[row * groups + c / 4] = (uint8_t)(most == most ? code : 255u);
+            if (there && c % 4 == 0)
+                ((uint8_t*)scales)[row * groups + c / 4] = (uint8_t)(most == most ? code : 255u);
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[i][e] *= inverse;
         } else {
             const float scale = most / 448.0f;
-            if (SC == SCALE_F32_128 ? c % 16 == 0 : c == 0)
+            if (there && (SC == SCALE_F32_128 ? c % 16 == 0 : c == 0))
                 ((float*)scales)[row * groups + (SC == SCALE_F32_128 ? c / 16 : 0)] = scale;
             if (most >= 0x1p-100f || !(most > 0.0f)) {
                 // y / scale as a product with the inverse and one correction (by zeros
                 // where there is no scale: a finite y becomes 0)
-                const bool there = most > 0.0f && most < INFINITY;
-                const float by = there ? scale : 0.0f;
+                const bool some = most > 0.0f && most < INFINITY;
+                const float by = some ? scale : 0.0f;
                 float inverse = __builtin_amdgcn_rcpf(scale);
-                inverse = there ? __builtin_fmaf(__builtin_fmaf(-scale, inverse, 1.0f), inverse, inverse) : 0.0f;
+                inverse = some ? __builtin_fmaf(__builtin_fmaf(-scale, inverse, 1.0f), inverse, inverse) : 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float q = y[i][e] * inverse;
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(
         }
         const u32x2 o = {e4m3_codes(y[i][0], y[i][1], y[i][2], y[i][3]),
                          e4m3_codes(y[i][4], y[i][5], y[i][6], y[i][7])};
-        __builtin_nontemporal_store(o, reinterpret_cast<u32x2*>(codes + row * dim + c * 8));
+        if (there) __builtin_nontemporal_store(o, reinterpret_cast<u32x2*>(codes + row * dim + c * 8));
     }
 }
 
