@@ -53,6 +53,8 @@ __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
+constexpr uint32_t kNear = 24;  // fp32 steps from an e8m0 step that 64 bits decide
+
 // One workgroup a row; thread t holds the 8-value chunks t, t + nthr, ... from
 // the loads to the codes, so every byte is moved once: memory bounds it (16384
 // rows of 5120 with a residual, 587 MB: 100 us, 5.9 TB/s), next to the vector
@@ -176,38 +178,51 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(
         if (!usual) most *= 0.0f;  // (an infinity: NaN)
         if constexpr (SC == SCALE_E8M0_32) {
             uint32_t code = e8m0_code(most);
-            // A maximum within 4 steps of fp32 of 448 times a power of two: which
-            // side of it, in 64 bits (the group's four lanes come here together).
+            // A maximum near 448 times a power of two: which side of it, in 64 bits, the
+            // row's squares too (a wave with such a group sums them once more).  fp32
+            // has the mean within 34 * 2^-24 (a thread's 32 squares, h's rounding) and
+            // the maximum within 21 * 2^-24: 19 of its steps here.
             const uint32_t bits = __float_as_uint(most);
-            if ((bits & 0x7FFFFFu) - 0x5FFFFCu <= 8u) {
+            const bool near = (bits & 0x7FFFFFu) - (0x600000u - kNear) <= 2 * kNear;
+            if (__any(near)) {
                 // x and the residual once more, from LDS where total is in their place
-                u32x4 wt = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-                u32x4 xx = {0, 0, 0, 0}, rr = {0, 0, 0, 0};
-                if (weight) wt = ww[i];
-                if (there) {
-                    if (kept & 1)
-                        xx = keep[c];
-                    else
-                        xx = *reinterpret_cast<const u32x4*>(x + row * dim + c * 8);
+                auto wide_h = [&](int at, double (&hh)[8]) {
+                    u32x4 rr = {0, 0, 0, 0};
+                    const u32x4 xx = kept & 1 ? keep[at] : *reinterpret_cast<const u32x4*>(x + row * dim + at * 8);
                     if (kept & 2)
-                        rr = keep[c];
+                        rr = keep[at];
                     else if (res)
-                        rr = *reinterpret_cast<const u32x4*>(res + row * dim + c * 8);
-                }
-                double wide = 0.0;
+                        rr = *reinterpret_cast<const u32x4*>(res + row * dim + at * 8);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const double lo = (double)lo_f(xx[e]) + (double)lo_f(rr[e]);
-                    const double hi = (double)hi_f(xx[e]) + (double)hi_f(rr[e]);
-                    wide = fmax(wide, fmax(fabs(lo * (double)lo_f(wt[e])),
-                                           fabs(hi * (double)hi_f(wt[e]))));
+                    for (int e = 0; e < 4; ++e) {
+                        hh[2 * e] = (double)lo_f(xx[e]) + (double)lo_f(rr[e]);
+                        hh[2 * e + 1] = (double)hi_f(xx[e]) + (double)hi_f(rr[e]);
+                    }
+                };
+                double hh[8], squares = 0.0, wide = 0.0;
+#pragma unroll 1
+                for (int at = lane; at < d8; at += 64) {
+                    wide_h(at, hh);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) squares += hh[e] * hh[e];
+                }
+#pragma unroll
+                for (int o = 32; o >= 1; o >>= 1) squares += __shfl_xor(squares, o, 64);
+                if (there) {
+                    wide_h(c, hh);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const double lo = weight ? (double)lo_f(ww[i][e]) : 1.0;
+                        const double hi = weight ? (double)hi_f(ww[i][e]) : 1.0;
+                        wide = fmax(wide, fmax(fabs(hh[2 * e] * lo), fabs(hh[2 * e + 1] * hi)));
+                    }
                 }
                 wide = fmax(wide, __shfl_xor(wide, 1, 64));
                 wide = fmax(wide, __shfl_xor(wide, 2, 64));
                 const uint32_t edge = (bits & 0xFF800000u) | 0x600000u;
                 const double lim = (double)__uint_as_float(edge);
-                const bool in = wide * wide <= lim * lim * var;
-                code = e8m0_code(__uint_as_float(in ? edge : edge + 1));
+                const bool in = wide * wide <= lim * lim * (squares / dim + (double)eps);
+                if (near) code = e8m0_code(__uint_as_float(in ? edge : edge + 1));
             }
             const float inverse = e8m0_inverse(code);
             if (there && c % 4 == 0)

@@ -59,3 +59,17 @@ def test_a_short_last_group(ge, dim):
     whole = lambda: torch.randint(-6, 7, (16, dim), generator=g, device=dev).bfloat16()  # noqa: E731
     w = (1 + 0.1 * torch.randn(dim, generator=g, device=dev)).bfloat16()
     assert at_the_border(ge, whole(), whole(), w, dim // 32 * 32, dim) > 30
+
+
+@pytest.mark.parametrize("dim", [32, 264, 1032, 5120, 32768])
+@pytest.mark.parametrize("spread", [1.0, 2.0 ** 20], ids=["even", "apart"])
+def test_any_row(ge, dim, spread):
+    """Squares whose sum 32 bits do not hold, and x and residual far `apart`, whose
+    sum they do not hold either."""
+    dev = torch.device("cuda:0")
+    say("norm step, any values", dim, spread)
+    g = torch.Generator(device=dev)
+    g.manual_seed(dim + 2)
+    r = lambda *s: torch.randn(s, generator=g, device=dev)  # noqa: E731
+    x, res, w = r(64, dim).bfloat16(), (r(64, dim) / spread).bfloat16(), (1 + 0.1 * r(dim)).bfloat16()
+    assert at_the_border(ge, x, res, w, 0, 32) > 100
