@@ -742,8 +742,9 @@ def engram_beam_select(logits, scores, finished=None, eos_id=-1, pad_id=0, token
                        parents=None, new_scores=None, new_finished=None, scratch=None, err=None):
     """Beam search's selection: logits bf16 or fp32 [B*W, V] (or [B, W, V]; rows
     may be strided), scores fp32 [B, W], finished bool/uint8 [B, W] or None ->
-    (tokens int32, parents int32, new_scores fp32, new_finished uint8), all
-    [B, W], best first.  new_scores may be scores, new_finished finished."""
+    (tokens int32, parents int32, new_scores fp32, new_finished uint8, or bool
+    if such a tensor is given), all [B, W], best first.  new_scores may be
+    scores, new_finished finished."""
     L = load()
     dev = logits.device
     _dev(scores, "scores", torch.float32, None, dev)
@@ -785,7 +786,8 @@ def engram_beam_select(logits, scores, finished=None, eos_id=-1, pad_id=0, token
     if new_finished is None:
         new_finished = torch.empty(shape, dtype=torch.uint8, device=dev)
     else:
-        _dev(new_finished, "new_finished", torch.uint8, shape, dev)
+        kind = torch.bool if getattr(new_finished, "dtype", None) is torch.bool else torch.uint8
+        _dev(new_finished, "new_finished", kind, shape, dev)
     if scratch is None:
         scratch = torch.empty(max(engram_beam_select_scratch_size(B, W, V), 1), dtype=torch.uint8,
                               device=dev)
