@@ -849,32 +849,38 @@ def engram_beam_reorder(states, parents, err=None):
 class EngramLayer:
     """One Engram layer's device-resident inputs: geometry, hash tables, the
     fp8 table and scales, the wkv weight and q/k weights, plus a reusable
-    workspace.  `forward` is engram_forward, or with adapters
+    workspace, which grows as calls need it (one that a graph was captured with
+    is kept).  `forward` is engram_forward, or with adapters
     engram_forward_adapted."""
 
     def __init__(self, g: Geometry, tables: dict, table, scales, w, q, k):
         self.g, self.tables = g, tables
         self.table, self.scales, self.w, self.q, self.k = table, scales, w, q, k
         self._ws = None
+        self._ws_captured, self._kept = False, []
+
+    def _room(self, need: int):
+        if self._ws is None or self._ws.numel() < need:
+            if self._ws_captured:  # the graph's replays write there
+                self._kept.append(self._ws)
+            self._ws = torch.empty(max(need, 1), dtype=torch.uint8, device=self.w.device)
+            self._ws_captured = False
+        if not self._ws_captured and self._ws.is_cuda:
+            self._ws_captured = torch.cuda.is_current_stream_capturing()
+        return self._ws
 
     def workspace(self, n_tok: int):
-        need = max(engram_forward_workspace_size(self.g, n_tok), 1)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(need, dtype=torch.uint8, device=self.w.device)
-        return self._ws
+        return self._room(engram_forward_workspace_size(self.g, n_tok))
 
     def forward(self, x, ids, mask=None, state=None, out=None, gate=None, err=None, adapters=None,
                 adapter_ids=None):
         if adapters is None and adapter_ids is not None:
             raise ValueError("adapter_ids without adapters")
         if adapters is not None:
-            need = max(engram_forward_adapted_workspace_size(self.g, adapters, ids.numel()), 1)
-            if self._ws is None or self._ws.numel() < need:
-                self._ws = torch.empty(need, dtype=torch.uint8, device=self.w.device)
+            ws = self._room(engram_forward_adapted_workspace_size(self.g, adapters, ids.numel()))
             return engram_forward_adapted(self.g, self.tables, adapters, self.table, self.scales,
                                           self.w, self.q, self.k, x, ids, adapter_ids, mask=mask,
-                                          state=state, out=out, gate=gate, workspace=self._ws,
-                                          err=err)
+                                          state=state, out=out, gate=gate, workspace=ws, err=err)
         return engram_forward(self.g, self.tables, self.table, self.scales, self.w, self.q, self.k,
                               x, ids, mask=mask, state=state, out=out, gate=gate,
                               workspace=self.workspace(ids.numel()), err=err)
