@@ -351,7 +351,8 @@ engram_status engram_forward_adapted(const engram_geometry* g, const engram_hash
  * row of zeros is 0/0: all NaN).  A NaN or an infinity in y has code 0x7F (NaN); a
  * NaN or an infinity in h reaches its own row alone: a NaN makes all of it NaN
  * (e8m0 scale codes 255), beside an infinity the finite values become 0 (as
- * they do where the squares' sum leaves fp32: values of about 2^60 and more).
+ * they do where the squares' sum leaves fp32: values of about 2^60 and more;
+ * with eps = 0, values below 2^-60 lose bits in their squares).
  *   x bf16 [rows, dim]; residual the same or NULL (h = x); weight bf16 [dim] or
  *   NULL (1); total bf16 [rows, dim] or NULL, may be x or residual; codes uint8
  *   [rows, dim].  dim % 8 == 0, 8 <= dim <= 32768.  x, residual, weight and
