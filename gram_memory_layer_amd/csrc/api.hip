@@ -600,6 +600,9 @@ engram_status engram_beam_reorder(void* const* states, const int64_t* row_bytes,
     for (int i = 0; i < n_states; ++i) {
         if (states[i] == nullptr || ((uintptr_t)states[i] & 3u) != 0) return ENGRAM_ERR_INVALID_ARG;
         const char* at = (const char*)states[i];
+        const char* par = (const char*)parents;  // read while the states change
+        if (at < par + (int64_t)B * W * 4 && par < at + (int64_t)B * W * row_bytes[i])
+            return ENGRAM_ERR_INVALID_ARG;
         for (int j = 0; j < i; ++j) {  // changed in place: no two may overlap
             const char* other = (const char*)states[j];
             if (at < other + (int64_t)B * W * row_bytes[j] &&

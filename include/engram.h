@@ -400,7 +400,8 @@ engram_status engram_beam_select(const void* logits, int32_t logits_f32, int64_t
  *   state[b][w] = (the state before the call)[b][parents[b][w]].
  *   states    host array of n_states device pointers, [B, W] rows of row_bytes[i]
  *             bytes each (engram_hash's state of a layer with B * W sequences:
- *             (max_ngram_size - 1) * 4); 4-byte aligned, no two overlapping.
+ *             (max_ngram_size - 1) * 4); 4-byte aligned, no two of them nor
+ *             one and parents overlapping.
  *   row_bytes host array, multiples of 4, >= 4.
  *   parents   int32 [B, W]; one outside [0, W) leaves its row as it was and sets
  *             ENGRAM_ERRBIT_PARENT.
