@@ -14,7 +14,8 @@ Functions carry the C names:
     engram_check_geometry,
     engram_wkv_adapters, engram_wkv_adapters_scratch_size, engram_forward_adapted,
     engram_forward_adapted_workspace_size, engram_norm_quant, engram_beam_select,
-    engram_beam_select_scratch_size, engram_beam_reorder
+    engram_beam_select_scratch_size, engram_beam_reorder,
+    engram_embed, engram_embed_grad, engram_embed_grad_scratch_size
 plus ``Geometry`` / ``HashTables`` (the C structs), ``Adapters`` (the low-rank
 adapters of a layer's projection) and ``EngramLayer``, a holder for one layer's
 device tables, weights and workspace.
@@ -35,6 +36,7 @@ __all__ = [
     "Adapters", "engram_wkv_adapters", "engram_wkv_adapters_scratch_size",
     "engram_forward_adapted", "engram_forward_adapted_workspace_size", "engram_norm_quant",
     "engram_beam_select", "engram_beam_select_scratch_size", "engram_beam_reorder",
+    "engram_embed", "engram_embed_grad", "engram_embed_grad_scratch_size",
     "ERRBIT_TOKEN", "ERRBIT_HASH", "ERRBIT_ROW", "ERRBIT_ADAPTER", "ERRBIT_LOGIT",
     "ERRBIT_PARENT",
 ]
@@ -163,6 +165,14 @@ def load():
                                      C.c_size_t, P, P]
     L.engram_beam_reorder.restype = C.c_int
     L.engram_beam_reorder.argtypes = [P, P, i32, P, i32, i32, P, P]
+    f32 = C.c_float
+    L.engram_embed.restype = C.c_int
+    L.engram_embed.argtypes = [P, i32, i64, i32, P, i64, f32, i32, P, i32, P, P]
+    L.engram_embed_grad_scratch_size.restype = C.c_size_t
+    L.engram_embed_grad_scratch_size.argtypes = [i64, i64, i32]
+    L.engram_embed_grad.restype = C.c_int
+    L.engram_embed_grad.argtypes = [P, i32, P, i64, i32, i64, i32, f32, i32, i32, P, i32, P,
+                                    C.c_size_t, P, P]
     _lib = L
     return L
 
@@ -844,6 +854,82 @@ def engram_beam_reorder(states, parents, err=None):
     _launch("engram_beam_reorder", L.engram_beam_reorder, dev, _ptr_array(n)(*ptr),
             _size_array(n)(*size), n, parents.data_ptr(), B, W, _ptr(err))
     return states
+
+
+# ------------------------------------------------------------------ the vocabulary's two ends
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def _float(t, name, shape=None, device=None):
+    """A bf16 or fp32 tensor on the device: whether it is fp32."""
+    kind = getattr(t, "dtype", None)
+    if isinstance(t, torch.Tensor) and kind not in _FLOATS:
+        raise TypeError("%s must be torch.float32 or torch.bfloat16 (got %s)" % (name, kind))
+    _dev(t, name, kind, shape, device)
+    return 1 if kind is torch.float32 else 0
+
+
+def engram_embed(table, ids, scale=1.0, streams=None, out=None, dtype=None, err=None):
+    """Embedding rows with a scale: table bf16 or fp32 [rows, dim], ids int32
+    [...] -> out [..., dim], or with streams [..., streams, dim] (every stream the
+    same), of type `dtype` (the table's if neither it nor out is given)."""
+    L = load()
+    t32 = _float(table, "table")
+    dev, shape = table.device, table.shape
+    if len(shape) != 2:
+        raise ValueError("table must be [rows, dim]")
+    rows, dim = shape
+    _dev(ids, "ids", torch.int32, None, dev)
+    o_shape = (*ids.shape, dim) if streams is None else (*ids.shape, int(streams), dim)
+    if out is None:
+        out = torch.empty(o_shape, dtype=dtype or table.dtype, device=dev)
+    elif dtype is not None and out.dtype is not dtype:
+        raise TypeError("out is %s, dtype %s" % (out.dtype, dtype))
+    o32 = _float(out, "out", o_shape, dev)
+    if err is not None:
+        _dev(err, "err", torch.int32, (1,), dev)
+    _launch("engram_embed", L.engram_embed, dev, table.data_ptr(), t32, rows, dim, ids.data_ptr(),
+            ids.numel(), scale, 1 if streams is None else int(streams), out.data_ptr(), o32,
+            _ptr(err))
+    return out
+
+
+def engram_embed_grad_scratch_size(n: int, rows: int, dim: int) -> int:
+    return load().engram_embed_grad_scratch_size(int(n), int(rows), int(dim))
+
+
+def engram_embed_grad(dout, ids, rows, scale=1.0, pad_id=-1, dtable=None, accumulate=False,
+                      dtype=None, scratch=None, err=None):
+    """The gradient of engram_embed in its table: dout bf16 or fp32 [..., dim] or
+    [..., streams, dim] with ids int32 [...] -> dtable [rows, dim] of type `dtype`
+    (fp32 if neither it nor dtable is given).  Positions with pad_id add nothing.
+    With accumulate it is added to the given dtable."""
+    L = load()
+    d32 = _float(dout, "dout")
+    dev, shape = dout.device, dout.shape
+    _dev(ids, "ids", torch.int32, None, dev)
+    lead = ids.shape
+    extra = len(shape) - len(lead)
+    if extra not in (1, 2) or shape[:len(lead)] != lead:
+        raise ValueError("dout must be [..., dim] or [..., streams, dim] for ids [...]")
+    n, rows, dim = ids.numel(), int(rows), shape[-1]
+    if dtable is None:
+        if accumulate:
+            raise ValueError("accumulate needs a dtable")
+        dtable = torch.empty((rows, dim), dtype=dtype or torch.float32, device=dev)
+    elif dtype is not None and dtable.dtype is not dtype:
+        raise TypeError("dtable is %s, dtype %s" % (dtable.dtype, dtype))
+    t32 = _float(dtable, "dtable", (rows, dim), dev)
+    if scratch is None:
+        scratch = torch.empty(max(engram_embed_grad_scratch_size(n, rows, dim), 1),
+                              dtype=torch.uint8, device=dev)
+    _dev(scratch, "scratch", torch.uint8, None, dev)
+    if err is not None:
+        _dev(err, "err", torch.int32, (1,), dev)
+    _launch("engram_embed_grad", L.engram_embed_grad, dev, dout.data_ptr(), d32, ids.data_ptr(), n,
+            1 if extra == 1 else shape[-2], rows, dim, scale, int(pad_id), 1 if accumulate else 0,
+            dtable.data_ptr(), t32, scratch.data_ptr(), scratch.numel(), _ptr(err))
+    return dtable
 
 
 class EngramLayer:

@@ -614,4 +614,61 @@ engram_status engram_beam_reorder(void* const* states, const int64_t* row_bytes,
                                                 (hipStream_t)stream));
 }
 
+// ---------------------------------------------------------------- the vocabulary's two ends
+
+// the sizes of a lookup and its gradient: 0, or the status that refuses them
+static engram_status embed_check(int64_t rows, int32_t dim, int64_t n, int32_t streams) {
+    if (rows < 1 || n < 0 || n >= kMaxTokens || streams < 1) return ENGRAM_ERR_INVALID_ARG;
+    if (rows >= ((int64_t)1 << 31) || dim < 8 || dim > 32768 || dim % 8 != 0 || streams > 8)
+        return ENGRAM_ERR_UNSUPPORTED;
+    return ENGRAM_OK;
+}
+
+engram_status engram_embed(const void* table, int32_t table_f32, int64_t rows, int32_t dim,
+                           const int32_t* ids, int64_t n, float scale, int32_t streams, void* out,
+                           int32_t out_f32, uint32_t* err, void* stream) {
+    const engram_status st = embed_check(rows, dim, n, streams);
+    if (st != ENGRAM_OK) return st;
+    if ((table_f32 != 0 && table_f32 != 1) || (out_f32 != 0 && out_f32 != 1) || !isfinite(scale))
+        return ENGRAM_ERR_INVALID_ARG;
+    if (n == 0) return ENGRAM_OK;
+    if (!table || !ids || !out) return ENGRAM_ERR_INVALID_ARG;
+    if (!aligned16(table) || !aligned16(out) || ((uintptr_t)ids & 3u) != 0)
+        return ENGRAM_ERR_INVALID_ARG;
+    return from_hip(engram::launch_embed(table, table_f32 != 0, rows, dim, ids, n, scale, streams,
+                                         out, out_f32 != 0, err, (hipStream_t)stream));
+}
+
+size_t engram_embed_grad_scratch_size(int64_t n, int64_t rows, int32_t dim) {
+    if (embed_check(rows, dim, n, 1) != ENGRAM_OK || n == 0 ||
+        !engram::embed_grad_supported(n, rows, dim))
+        return 0;
+    return engram::embed_grad_scratch_bytes(n, rows, dim);
+}
+
+engram_status engram_embed_grad(const void* dout, int32_t dout_f32, const int32_t* ids, int64_t n,
+                                int32_t streams, int64_t rows, int32_t dim, float scale,
+                                int32_t pad_id, int32_t accumulate, void* dtable,
+                                int32_t dtable_f32, void* scratch, size_t scratch_bytes,
+                                uint32_t* err, void* stream) {
+    const engram_status st = embed_check(rows, dim, n, streams);
+    if (st != ENGRAM_OK) return st;
+    if (!engram::embed_grad_supported(n, rows, dim)) return ENGRAM_ERR_UNSUPPORTED;
+    if ((dout_f32 != 0 && dout_f32 != 1) || (dtable_f32 != 0 && dtable_f32 != 1) ||
+        (accumulate != 0 && accumulate != 1) || !isfinite(scale) || pad_id < -1 || pad_id >= rows)
+        return ENGRAM_ERR_INVALID_ARG;
+    if (n == 0 && accumulate) return ENGRAM_OK;
+    if (!dtable || !aligned16(dtable)) return ENGRAM_ERR_INVALID_ARG;
+    if (n > 0) {
+        if (!dout || !ids || !aligned16(dout) || ((uintptr_t)ids & 3u) != 0)
+            return ENGRAM_ERR_INVALID_ARG;
+        if (scratch == nullptr || scratch_bytes < engram_embed_grad_scratch_size(n, rows, dim) ||
+            ((uintptr_t)scratch & 255u) != 0)
+            return ENGRAM_ERR_WORKSPACE;
+    }
+    return from_hip(engram::launch_embed_grad(dout, dout_f32 != 0, ids, n, streams, rows, dim,
+                                              scale, pad_id, accumulate != 0, dtable,
+                                              dtable_f32 != 0, scratch, err, (hipStream_t)stream));
+}
+
 }  // extern "C"

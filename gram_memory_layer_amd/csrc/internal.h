@@ -209,6 +209,18 @@ hipError_t launch_beam_reorder(void* const* states, const int64_t* row_bytes, in
                                const int32_t* parents, int64_t B, int W, uint32_t* err,
                                hipStream_t s);
 
+hipError_t launch_embed(const void* table, bool table_f32, int64_t rows, int dim,
+                        const int32_t* ids, int64_t n, float scale, int streams, void* out,
+                        bool out_f32, uint32_t* err, hipStream_t s);
+
+// (the sum kernel's threads have to fit a launch: embed_grad_supported)
+bool embed_grad_supported(int64_t n, int64_t rows, int dim);
+size_t embed_grad_scratch_bytes(int64_t n, int64_t rows, int dim);
+hipError_t launch_embed_grad(const void* dout, bool dout_f32, const int32_t* ids, int64_t n,
+                             int streams, int64_t rows, int dim, float scale, int32_t pad_id,
+                             bool accumulate, void* dtable, bool dtable_f32, void* scratch,
+                             uint32_t* err, hipStream_t s);
+
 // engram_forward split at its workspace: every other argument check, and the
 // launches given a workspace of engram_forward_workspace_size bytes.
 engram_status forward_check(const engram_geometry* g, const engram_hash_tables* t,

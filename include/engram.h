@@ -410,6 +410,47 @@ engram_status engram_beam_reorder(void* const* states, const int64_t* row_bytes,
                                   int32_t n_states, const int32_t* parents, int32_t B, int32_t W,
                                   uint32_t* err, void* stream);
 
+/* ---- The vocabulary's two ends: a token's row into the layer's streams, and
+ * the rows' gradient.  As above, the pages do not describe these calls, and a
+ * scratch argument may be reused by the next call on the same stream and by
+ * captured graphs that are replayed one after the other. */
+
+/* Embedding rows with a scale, copied to every stream:
+ *   out[i][s] = scale * table[ids[i]],  s < streams,
+ * the product in fp32, rounded once to out's type (nearest even).
+ *   table bf16 (table_f32 = 0) or fp32 [rows, dim] (token embeddings, or
+ *         trained rows of an Engram table before they become e4m3);
+ *   ids   int32 [n]; one outside [0, rows) gives zeros and sets ENGRAM_ERRBIT_ROW;
+ *   out   bf16 (out_f32 = 0) or fp32 [n, streams, dim] (the layer's x for streams
+ *         = hc_mult); not overlapping table or ids.
+ * 1 <= rows < 2^31, dim % 8 == 0, 8 <= dim <= 32768, 1 <= streams <= 8, scale
+ * finite; table and out 16-byte aligned. */
+engram_status engram_embed(const void* table, int32_t table_f32, int64_t rows, int32_t dim,
+                           const int32_t* ids, int64_t n, float scale, int32_t streams, void* out,
+                           int32_t out_f32, uint32_t* err, void* stream);
+
+/* Its gradient:
+ *   dtable[v] = scale * sum over i with ids[i] = v, and s, of dout[i][s]
+ * with accumulate = 0, every row written (zeros where no id names it), or that
+ * added to the row that is there with accumulate = 1, where rows that no id
+ * names are not touched.  Sums in fp32 in an order that n, dim and the ids
+ * decide (the same on every run); scale and the addition are one rounding to
+ * fp32, then, for a bf16 dtable, one to bf16.
+ *   dout   bf16 (dout_f32 = 0) or fp32 [n, streams, dim];
+ *   ids    int32 [n]; positions with pad_id (-1: none) add nothing, and those with an
+ *          id outside [0, rows) add nothing and set ENGRAM_ERRBIT_ROW;
+ *   dtable bf16 (dtable_f32 = 0) or fp32 [rows, dim]; not overlapping the others;
+ *   scratch engram_embed_grad_scratch_size bytes, 256-byte aligned; contents on
+ *          entry do not matter.
+ * Sizes as in engram_embed; about n * dim < 2^40 (the scratch size is 0 where
+ * they are refused). */
+size_t engram_embed_grad_scratch_size(int64_t n, int64_t rows, int32_t dim);
+engram_status engram_embed_grad(const void* dout, int32_t dout_f32, const int32_t* ids, int64_t n,
+                                int32_t streams, int64_t rows, int32_t dim, float scale,
+                                int32_t pad_id, int32_t accumulate, void* dtable,
+                                int32_t dtable_f32, void* scratch, size_t scratch_bytes,
+                                uint32_t* err, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

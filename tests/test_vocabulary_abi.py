@@ -1,0 +1,61 @@
+"""The calls at the vocabulary's two ends (lookup, its gradient, sampling)
+without a GPU: sizes and refusals.  Every call here fails its checks on the
+host, or has no work, and launches nothing."""
+import pytest
+import torch
+
+import gram_memory_layer_amd as ge
+
+FAKE = 1 << 20  # never dereferenced
+
+
+def test_embed_host_checks():
+    lib = ge.load()
+
+    def call(table=FAKE, t32=0, rows=100, dim=64, ids=FAKE, n=4, scale=1.0, streams=1, out=FAKE, o32=0):
+        return lib.engram_embed(table, t32, rows, dim, ids, n, scale, streams, out, o32, None, None)
+    assert call(table=None) == 1 and call(ids=None) == 1 and call(out=None) == 1
+    assert call(table=FAKE + 8) == 1 and call(out=FAKE + 4) == 1 and call(ids=FAKE + 2) == 1
+    assert call(t32=2) == 1 and call(o32=-1) == 1
+    assert call(rows=0) == 1 and call(n=-1) == 1 and call(n=1 << 31) == 1 and call(streams=0) == 1
+    assert call(scale=float("nan")) == 1 and call(scale=float("inf")) == 1
+    assert call(rows=1 << 31) == 2 and call(streams=9) == 2
+    for dim in (0, 4, 12, 32776):
+        assert call(dim=dim) == 2, dim
+    assert call(n=0) == 0 and call(n=0, table=None, ids=None, out=None) == 0
+
+
+def test_embed_grad_host_checks():
+    lib = ge.load()
+    size = ge.engram_embed_grad_scratch_size
+    assert size(0, 100, 64) == 0 and size(-1, 100, 64) == 0 and size(4, 0, 64) == 0 and size(4, 100, 12) == 0
+    assert 0 < size(4, 100, 64) <= size(4096, 100, 64) < size(4097, 100, 64)
+    assert size((1 << 31) - 1, 100, 32768) == 0  # more tiles than a launch takes
+
+    def call(dout=FAKE, d32=0, ids=FAKE, n=4, streams=1, rows=100, dim=64, scale=1.0, pad=-1, add=0, dt=FAKE,
+             t32=0, scratch=FAKE, nbytes=1 << 30):
+        return lib.engram_embed_grad(dout, d32, ids, n, streams, rows, dim, scale, pad, add, dt, t32, scratch,
+                                     nbytes, None, None)
+    assert call(dout=None) == 1 and call(ids=None) == 1 and call(dt=None) == 1
+    assert call(dout=FAKE + 8) == 1 and call(dt=FAKE + 4) == 1 and call(ids=FAKE + 2) == 1
+    assert call(d32=2) == 1 and call(t32=2) == 1 and call(add=2) == 1
+    assert call(n=-1) == 1 and call(rows=0) == 1 and call(streams=0) == 1
+    assert call(pad=-2) == 1 and call(pad=100) == 1
+    assert call(scale=float("nan")) == 1 and call(scale=-float("inf")) == 1
+    assert call(rows=1 << 31) == 2 and call(streams=9) == 2 and call(dim=12) == 2
+    assert call(n=(1 << 31) - 1, dim=32768) == 2
+    assert call(scratch=None) == 3 and call(scratch=FAKE + 128) == 3
+    assert call(nbytes=size(4, 100, 64) - 1) == 3
+    assert call(n=0, add=1) == 0 and call(n=0, add=0, dt=None) == 1
+
+
+def test_binding_refuses_what_is_not_on_the_device():
+    table, ids = torch.zeros(10, 16), torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        ge.engram_embed(table, ids)
+    with pytest.raises(TypeError):
+        ge.engram_embed(table.double(), ids)
+    with pytest.raises(TypeError):
+        ge.engram_embed([1.0], ids)
+    with pytest.raises(ValueError):
+        ge.engram_embed_grad(torch.zeros(4, 16), ids, 10)
