@@ -15,7 +15,8 @@ Functions carry the C names:
     engram_wkv_adapters, engram_wkv_adapters_scratch_size, engram_forward_adapted,
     engram_forward_adapted_workspace_size, engram_norm_quant, engram_beam_select,
     engram_beam_select_scratch_size, engram_beam_reorder,
-    engram_embed, engram_embed_grad, engram_embed_grad_scratch_size
+    engram_sample, engram_sample_scratch_size, engram_embed, engram_embed_grad,
+    engram_embed_grad_scratch_size
 plus ``Geometry`` / ``HashTables`` (the C structs), ``Adapters`` (the low-rank
 adapters of a layer's projection) and ``EngramLayer``, a holder for one layer's
 device tables, weights and workspace.
@@ -36,16 +37,17 @@ __all__ = [
     "Adapters", "engram_wkv_adapters", "engram_wkv_adapters_scratch_size",
     "engram_forward_adapted", "engram_forward_adapted_workspace_size", "engram_norm_quant",
     "engram_beam_select", "engram_beam_select_scratch_size", "engram_beam_reorder",
-    "engram_embed", "engram_embed_grad", "engram_embed_grad_scratch_size",
+    "engram_sample", "engram_sample_scratch_size", "engram_embed", "engram_embed_grad",
+    "engram_embed_grad_scratch_size",
     "ERRBIT_TOKEN", "ERRBIT_HASH", "ERRBIT_ROW", "ERRBIT_ADAPTER", "ERRBIT_LOGIT",
-    "ERRBIT_PARENT",
+    "ERRBIT_PARENT", "ERRBIT_SAMPLE",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libengram.so")
 
 ERRBIT_TOKEN, ERRBIT_HASH, ERRBIT_ROW = 0x1, 0x2, 0x4
-ERRBIT_ADAPTER, ERRBIT_LOGIT, ERRBIT_PARENT = 0x8, 0x10, 0x20
+ERRBIT_ADAPTER, ERRBIT_LOGIT, ERRBIT_PARENT, ERRBIT_SAMPLE = 0x8, 0x10, 0x20, 0x40
 _SCALE_FORMATS = {"e8m0_32": 0, "f32_128": 1, "f32_row": 2}
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported geometry",
            3: "workspace missing or too small", 4: "HIP runtime error",
@@ -166,6 +168,10 @@ def load():
     L.engram_beam_reorder.restype = C.c_int
     L.engram_beam_reorder.argtypes = [P, P, i32, P, i32, i32, P, P]
     f32 = C.c_float
+    L.engram_sample_scratch_size.restype = C.c_size_t
+    L.engram_sample_scratch_size.argtypes = [i32, i32]
+    L.engram_sample.restype = C.c_int
+    L.engram_sample.argtypes = [P, i32, i64, P, P, P, P, P, i32, i32, P, P, P, C.c_size_t, P, P]
     L.engram_embed.restype = C.c_int
     L.engram_embed.argtypes = [P, i32, i64, i32, P, i64, f32, i32, P, i32, P, P]
     L.engram_embed_grad_scratch_size.restype = C.c_size_t
@@ -867,6 +873,62 @@ def _float(t, name, shape=None, device=None):
         raise TypeError("%s must be torch.float32 or torch.bfloat16 (got %s)" % (name, kind))
     _dev(t, name, kind, shape, device)
     return 1 if kind is torch.float32 else 0
+
+
+def engram_sample_scratch_size(B: int, V: int) -> int:
+    return load().engram_sample_scratch_size(int(B), int(V))
+
+
+def engram_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None,
+                  logprobs=None, scratch=None, err=None):
+    """The next token of every row from given random numbers: logits bf16 or fp32
+    [B, V] (rows may be strided), u fp32 [B] in [0, 1), temperature fp32 [B] (0:
+    greedy), top_k int32 [B] (0: none), top_p fp32 [B] (1: none), min_p fp32 [B]
+    (0: none), each of the four or None -> (tokens int32 [B], logprobs fp32 [B]
+    of the token among those that the filters leave); -1 where there is none."""
+    L = load()
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    dev = logits.device
+    if not logits.is_cuda:
+        raise ValueError("logits must be a device tensor (got %s)" % dev)
+    f32 = logits.dtype is torch.float32
+    if not f32 and logits.dtype is not torch.bfloat16:
+        raise TypeError("logits must be torch.float32 or torch.bfloat16 (got %s)" % logits.dtype)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [B, V]")
+    shape, (B, V) = logits.shape[:1], logits.shape
+    stride = logits.stride()
+    ld = stride[0] if B > 1 else V
+    if (V > 1 and stride[1] != 1) or ld < V:
+        raise ValueError("logits must have contiguous rows")
+    _dev(u, "u", torch.float32, shape, dev)
+    if temperature is not None:
+        _dev(temperature, "temperature", torch.float32, shape, dev)
+    if top_k is not None:
+        _dev(top_k, "top_k", torch.int32, shape, dev)
+    if top_p is not None:
+        _dev(top_p, "top_p", torch.float32, shape, dev)
+    if min_p is not None:
+        _dev(min_p, "min_p", torch.float32, shape, dev)
+    if tokens is None:
+        tokens = torch.empty(shape, dtype=torch.int32, device=dev)
+    else:
+        _dev(tokens, "tokens", torch.int32, shape, dev)
+    if logprobs is None:
+        logprobs = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        _dev(logprobs, "logprobs", torch.float32, shape, dev)
+    if scratch is None:
+        scratch = torch.empty(max(engram_sample_scratch_size(B, V), 1), dtype=torch.uint8,
+                              device=dev)
+    _dev(scratch, "scratch", torch.uint8, None, dev)
+    if err is not None:
+        _dev(err, "err", torch.int32, (1,), dev)
+    _launch("engram_sample", L.engram_sample, dev, logits.data_ptr(), 1 if f32 else 0, ld,
+            u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), B, V,
+            tokens.data_ptr(), logprobs.data_ptr(), scratch.data_ptr(), scratch.numel(), _ptr(err))
+    return tokens, logprobs
 
 
 def engram_embed(table, ids, scale=1.0, streams=None, out=None, dtype=None, err=None):

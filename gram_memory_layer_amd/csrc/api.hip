@@ -671,4 +671,39 @@ engram_status engram_embed_grad(const void* dout, int32_t dout_f32, const int32_
                                               dtable_f32 != 0, scratch, err, (hipStream_t)stream));
 }
 
+// the sizes that sampling takes: 0, or the status that refuses them
+static engram_status sample_check(int32_t B, int32_t V) {
+    if (B < 0 || V < 1) return ENGRAM_ERR_INVALID_ARG;
+    if (B > 65535 || V > (1 << 22)) return ENGRAM_ERR_UNSUPPORTED;
+    return ENGRAM_OK;
+}
+
+size_t engram_sample_scratch_size(int32_t B, int32_t V) {
+    if (sample_check(B, V) != ENGRAM_OK || B == 0) return 0;
+    return engram::sample_scratch_bytes(B, V);
+}
+
+engram_status engram_sample(const void* logits, int32_t logits_f32, int64_t ld, const float* u,
+                            const float* temperature, const int32_t* top_k, const float* top_p,
+                            const float* min_p, int32_t B, int32_t V, int32_t* tokens,
+                            float* logprobs, void* scratch, size_t scratch_bytes, uint32_t* err,
+                            void* stream) {
+    const engram_status st = sample_check(B, V);
+    if (st != ENGRAM_OK) return st;
+    if (ld < V || ld >= ((int64_t)1 << 40) || (logits_f32 != 0 && logits_f32 != 1))
+        return ENGRAM_ERR_INVALID_ARG;
+    if (B == 0) return ENGRAM_OK;
+    if (!logits || !u || !tokens) return ENGRAM_ERR_INVALID_ARG;
+    if (((uintptr_t)logits & (logits_f32 ? 3u : 1u)) != 0 ||
+        (((uintptr_t)u | (uintptr_t)temperature | (uintptr_t)top_k | (uintptr_t)top_p |
+          (uintptr_t)min_p | (uintptr_t)tokens | (uintptr_t)logprobs) & 3u) != 0)
+        return ENGRAM_ERR_INVALID_ARG;
+    if (scratch == nullptr || scratch_bytes < engram_sample_scratch_size(B, V) ||
+        ((uintptr_t)scratch & 255u) != 0)
+        return ENGRAM_ERR_WORKSPACE;
+    return from_hip(engram::launch_sample(logits, logits_f32 != 0, ld, u, temperature, top_k,
+                                          top_p, min_p, B, V, tokens, logprobs, scratch, err,
+                                          (hipStream_t)stream));
+}
+
 }  // extern "C"

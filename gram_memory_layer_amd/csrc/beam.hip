@@ -9,19 +9,12 @@
 // The logits are read once.  Scores that lie next to each other decide which
 // tokens come out, so the sums of exponentials, their logarithm and the
 // scores are held in 64 bits.
-#include "internal.h"
+#include "logits.h"
 
 namespace engram {
 namespace {
 
 constexpr int kWaves = 4;  // waves of a workgroup that takes parts
-
-// LDS written by lanes of this wave is read by others of it afterwards (LDS
-// accesses of a wave are performed in order; this keeps the compiler to it)
-__device__ __forceinline__ void wave_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
 
 // exp(x) 2^-N in 64 bits, to 5e-11 relative, for -700 <= x - N ln 2 <= 1 and |x| <=
 // 5000, with `round` = 1.5 * 2^52 - N; a NaN stays one.  2^t = 2^n * 2^f with n the
@@ -163,55 +156,6 @@ __device__ __forceinline__ void wave_top(const double (&key)[E], const int32_t (
         last_i = bi;
     }
 }
-
-// A row of logits in 16-byte pieces.  It may start at any element: pieces are
-// laid out from the 16-byte boundary before it, and a piece that reaches out
-// of the row is read by elements (-inf outside).
-template <class T>
-struct Row {
-    static constexpr int VEC = 16 / sizeof(T);
-    const T* src;
-    int before;  // elements between the boundary and the row
-
-    __device__ explicit Row(const T* row)
-        : src(row), before((int)(((uintptr_t)row & 15) / sizeof(T))) {}
-    // the column of piece i's first element
-    __device__ int64_t column(int64_t i) const { return i * VEC - before; }
-    __device__ bool whole(int64_t i, int V) const {
-        return column(i) >= 0 && column(i) + VEC <= V;
-    }
-    // in two steps, so that several pieces can be on their way
-    __device__ uint4 fetch(int64_t i, int V) const {
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (whole(i, V)) raw = *reinterpret_cast<const uint4*>(src + column(i));
-        return raw;
-    }
-    __device__ void values(const uint4& raw, float (&x)[VEC]) const {
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            if constexpr (sizeof(T) == 4)
-                x[e] = __uint_as_float(w[e]);
-            else
-                x[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-        }
-    }
-    __device__ void unpack(const uint4& raw, int64_t i, int V, float (&x)[VEC]) const {
-        values(raw, x);
-        if (whole(i, V)) return;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int64_t c = column(i) + e;
-            x[e] = -INFINITY;
-            if (c >= 0 && c < V) {
-                if constexpr (sizeof(T) == 4)
-                    x[e] = src[c];
-                else
-                    x[e] = bf16_to_f32(src[c]);
-            }
-        }
-    }
-};
 
 // One wave a part: 64 lanes of E logits, E / VEC pieces of 64 lanes.  (512 rows of
 // 129,280: fp32 46-50 us, 5.3-5.8 TB/s, bound by memory; bf16 49 us, bound by the

@@ -221,6 +221,12 @@ hipError_t launch_embed_grad(const void* dout, bool dout_f32, const int32_t* ids
                              bool accumulate, void* dtable, bool dtable_f32, void* scratch,
                              uint32_t* err, hipStream_t s);
 
+size_t sample_scratch_bytes(int64_t B, int V);
+hipError_t launch_sample(const void* logits, bool f32, int64_t ld, const float* u,
+                         const float* temperature, const int32_t* top_k, const float* top_p,
+                         const float* min_p, int64_t B, int V, int32_t* tokens, float* logprobs,
+                         void* scratch, uint32_t* err, hipStream_t s);
+
 // engram_forward split at its workspace: every other argument check, and the
 // launches given a workspace of engram_forward_workspace_size bytes.
 engram_status forward_check(const engram_geometry* g, const engram_hash_tables* t,

@@ -48,6 +48,7 @@ typedef enum engram_status {
 #define ENGRAM_ERRBIT_ADAPTER 0x8u  /* an adapter id outside [-1, n) (used as none) */
 #define ENGRAM_ERRBIT_LOGIT  0x10u  /* a NaN or +infinity in a live beam's logits or scores */
 #define ENGRAM_ERRBIT_PARENT 0x20u  /* a parent outside [0, W) (its row is left as it was) */
+#define ENGRAM_ERRBIT_SAMPLE 0x40u  /* a sampling parameter outside its range (no token) */
 
 /* Geometry of one Engram layer ([block] constructor: ModelArgs dim, hc_mult,
  * norm_eps; EngramLayout num_embeddings, head_dim, max_ngram_size, n_heads).
@@ -410,10 +411,44 @@ engram_status engram_beam_reorder(void* const* states, const int64_t* row_bytes,
                                   int32_t n_states, const int32_t* parents, int32_t B, int32_t W,
                                   uint32_t* err, void* stream);
 
-/* ---- The vocabulary's two ends: a token's row into the layer's streams, and
- * the rows' gradient.  As above, the pages do not describe these calls, and a
+/* ---- The vocabulary's two ends: the next token by sampling, a token's row into
+ * the layer's streams, and the rows' gradient.  As above, the pages do not describe these calls, and a
  * scratch argument may be reused by the next call on the same stream and by
  * captured graphs that are replayed one after the other. */
+
+/* The next token of every row of logits from a given random number.  With x the
+ * row and
+ *   w(v) = exp((x(v) - max x) / temperature),
+ * in the order of falling x, equal ones by rising v,
+ *   top_k  the first top_k stay;
+ *   top_p  of these, one stays if the w of those before it sum to less than top_p
+ *          times the sum of the w of these (the first one always);
+ *   min_p  of these, one stays if w >= min_p (w of the largest is 1),
+ * token is the first v of those that stay, v rising, whose sum of w up to and with
+ * v exceeds u times the sum of all that stay; logprob = log(w(token) / that sum).
+ * Weights and sums in 64 bits (each weight to 2e-12 of itself); a w below 2^-999
+ * is none.
+ *   logits bf16 (logits_f32 = 0) or fp32, B rows of V, ld >= V elements apart;
+ *          rows may start at any element; a logit of -infinity never stays.
+ *   u      fp32 [B], in [0, 1).
+ *   temperature fp32 [B], >= 0 and finite, or NULL (1 for all); 0: the first
+ *          largest logit is the token, its logprob 0.
+ *   top_k  int32 [B] or NULL; 0 and less, or V and more: no such filter.
+ *   top_p  fp32 [B], in [0, 1], or NULL; 1: none.
+ *   min_p  fp32 [B], in [0, 1], or NULL; 0: none.
+ *   tokens int32 [B] out (to feed engram_hash and engram_embed); logprobs fp32 [B]
+ *          out, or NULL.
+ * A row whose logits are all -infinity has token -1 and logprob -infinity; so has
+ * one with a NaN or +infinity among its logits (ENGRAM_ERRBIT_LOGIT), or with a
+ * parameter outside the ranges above, a NaN one too (ENGRAM_ERRBIT_SAMPLE).
+ * 1 <= V <= 2^22, B <= 65535.  scratch: engram_sample_scratch_size bytes, 256-byte
+ * aligned; contents on entry do not matter. */
+size_t engram_sample_scratch_size(int32_t B, int32_t V);
+engram_status engram_sample(const void* logits, int32_t logits_f32, int64_t ld, const float* u,
+                            const float* temperature, const int32_t* top_k, const float* top_p,
+                            const float* min_p, int32_t B, int32_t V, int32_t* tokens,
+                            float* logprobs, void* scratch, size_t scratch_bytes, uint32_t* err,
+                            void* stream);
 
 /* Embedding rows with a scale, copied to every stream:
  *   out[i][s] = scale * table[ids[i]],  s < streams,

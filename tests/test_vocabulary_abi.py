@@ -59,3 +59,28 @@ def test_binding_refuses_what_is_not_on_the_device():
         ge.engram_embed([1.0], ids)
     with pytest.raises(ValueError):
         ge.engram_embed_grad(torch.zeros(4, 16), ids, 10)
+
+
+def test_sample_host_checks():
+    lib = ge.load()
+    size = ge.engram_sample_scratch_size
+    assert size(2, 1000) > 0 and size(0, 1000) == 0 and size(2, 0) == 0 and size(2, (1 << 22) + 1) == 0
+
+    def call(logits=FAKE, f32=1, ld=1000, u=FAKE, t=None, k=None, p=None, m=None, B=2, V=1000, tok=FAKE, lp=None,
+             scratch=FAKE, nbytes=1 << 40):
+        return lib.engram_sample(logits, f32, ld, u, t, k, p, m, B, V, tok, lp, scratch, nbytes, None, None)
+    assert call(logits=None) == 1 and call(u=None) == 1 and call(tok=None) == 1
+    assert call(logits=FAKE + 2) == 1 and call(f32=0, logits=FAKE + 1) == 1
+    for name in ("u", "t", "k", "p", "m", "tok", "lp"):
+        assert call(**{name: FAKE + 2}) == 1, name
+    assert call(f32=2) == 1 and call(ld=999) == 1 and call(B=-1) == 1 and call(V=0) == 1
+    assert call(V=(1 << 22) + 1, ld=1 << 23) == 2 and call(B=65536) == 2
+    assert call(scratch=None) == 3 and call(nbytes=64) == 3 and call(scratch=FAKE + 128) == 3
+    assert call(B=0) == 0
+
+
+def test_sampling_binding_refuses_what_is_not_on_the_device():
+    with pytest.raises(ValueError):
+        ge.engram_sample(torch.zeros(4, 16), torch.zeros(4))
+    with pytest.raises(TypeError):
+        ge.engram_sample([1.0], torch.zeros(4))
