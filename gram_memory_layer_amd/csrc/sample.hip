@@ -15,12 +15,21 @@
 namespace engram {
 namespace {
 
-constexpr int kPartThreads = 256;
-constexpr int kEach = 32;                       // logits a thread of a part
-constexpr int kPart = kPartThreads * kEach;     // logits a part
-constexpr int kRowThreads = 1024;
+constexpr int kEach = 32;                     // logits a thread of a part
+constexpr int kPart = 64 * kEach;             // logits a wave: a part
+constexpr int kBlockWaves = 4;
+constexpr int kBlock = kBlockWaves * kPart;   // logits a workgroup
+constexpr int kBuckets = 512;                 // of 1/32 of exp's argument, from a block's largest logit down;
+constexpr int kRest = kBuckets - 1;           // the last one takes all below, too
+constexpr int kCopies = 4;                    // of the buckets in LDS: lanes that meet in one wait for each other
+constexpr int kGroup = 16;                    // lanes whose largest logit is kept
+constexpr int kRowThreads = 512;
 constexpr int kRowWaves = kRowThreads / 64;
-constexpr int kBins = 1024;
+constexpr int kBinBits = 9, kBins = 1 << kBinBits;  // a thread each
+constexpr int kList = 4096;                   // candidates in LDS,
+constexpr int kSome = 64, kRanked = 256;       // that are ranked by counting, by a wave or all
+constexpr int kHits = 4 * kRowThreads;        // groups of a row looked at together
+constexpr int kMostBlocks = 256;              // of a row whose buckets are joined
 
 // exp(d / T) for d <= 0, by c = log2(e) / T: 2^n * 2^f, f in [-1/2, 1/2], 2^f by a
 // polynomial of degree eight with the least relative error (1.1e-12, by Remez'
@@ -28,10 +37,10 @@ constexpr int kBins = 1024;
 constexpr double kLog2e = 1.4426950408889634074;
 constexpr double kRound = 6755399441055744.0;  // 1.5 * 2^52: adding it rounds to a whole number
 constexpr double kNoWeight = 0x1p-999;
+// (for d * c >= -1000)
 __device__ __forceinline__ double weight(double d, double c) {
-    const double t = fmax(d * c, -1000.0);
-    const double r = t + kRound;
-    const double f = t - (r - kRound);
+    const double r = __builtin_fma(d, c, kRound);
+    const double f = __builtin_fma(d, c, -(r - kRound));
     double p = 1.3344183691340562e-06;
     p = __builtin_fma(p, f, 1.531420923292218e-05);
     p = __builtin_fma(p, f, 0.00015403098285512635);
@@ -65,10 +74,12 @@ struct Request {
 // A row's own values, checked
 struct Want {
     double c;      // log2(e) / temperature; 0: greedy
+    double least;  // the difference of logits that weighs 2^-1000
+    float s;       // buckets a unit of the logits
     double p, m, u;
     int k;         // 0: no top-k
     bool bad;
-    __device__ Want(const Request& q, int64_t row, int V) {
+    __device__ __forceinline__ Want(const Request& q, int64_t row, int V) {
         const float t = q.temperature ? q.temperature[row] : 1.0f;
         const float pp = q.top_p ? q.top_p[row] : 1.0f;
         const float mm = q.min_p ? q.min_p[row] : 0.0f;
@@ -77,137 +88,289 @@ struct Want {
         bad = !(t >= 0.0f && t < INFINITY) || !(pp >= 0.0f && pp <= 1.0f) ||
               !(mm >= 0.0f && mm <= 1.0f) || !(uu >= 0.0f && uu < 1.0f);
         c = t > 0.0f ? kLog2e / (double)t : 0.0;
+        least = -1000.0 / c;
+        s = 32.0f / t;
         p = pp;
         m = mm;
         u = uu;
         k = kk > 0 && kk < V ? kk : 0;
     }
-    __device__ bool greedy() const { return c == 0.0; }
-    __device__ bool filtered() const { return k > 0 || p < 1.0 || m > 0.0; }
+    __device__ __forceinline__ bool greedy() const { return c == 0.0; }
+    __device__ __forceinline__ bool filtered() const { return !greedy() && (k > 0 || p < 1.0 || m > 0.0); }
     // whether the weights of the whole row are summed
-    __device__ bool whole_sum() const { return !greedy() && k == 0 && (p < 1.0 || m == 0.0); }
+    __device__ __forceinline__ bool whole_sum() const { return !greedy() && k == 0 && (p < 1.0 || m == 0.0); }
+    __device__ __forceinline__ double weigh(float x, float top) const {
+        return weight(fmax((double)x - (double)top, least), c);
+    }
+    // A whole number that does not fall as x rises.  (s may be infinite: then
+    // zero goes with the negative ones.)
+    __device__ __forceinline__ int bucket(float x) const {
+        return (int)floorf(fminf(fmaxf(x * s, -0x1p29f), 0x1p29f));
+    }
 };
 
-// One workgroup a part of a row: its largest logit (NaN: a NaN or +infinity is in
-// it) and, where the row needs it, the sum of its weights relative to that.
+// What the blocks leave for the row
+struct Found {
+    float* tops;       // [parts] a part's largest logit; NaN: a NaN or +infinity is in it
+    double* sums;      // [parts] its weights' sum, relative to its largest logit (rows with a
+                       // filter: to the block's; where no sum is needed, the number of
+                       // logits above -infinity)
+    float* groups;     // [blocks * kBlock / (kGroup * VEC)] the largest of a group
+    double* buckets;   // [blocks][kBuckets] the sum of weights in the bucket, relative to the block's
+                       // largest logit, where the row's sum is needed, otherwise the number of logits
+    int blocks;
+};
+
+// x of another lane, by a data-parallel move (0 where that gives none)
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ uint32_t moved(uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, true);
+}
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ double moved(double x) {
+    return __hiloint2double((int)moved<CTRL, ROWS>((uint32_t)__double2hiint(x)),
+                            (int)moved<CTRL, ROWS>((uint32_t)__double2loint(x)));
+}
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ uint64_t moved(uint64_t x) {
+    return (uint64_t)moved<CTRL, ROWS>((uint32_t)(x >> 32)) << 32 | moved<CTRL, ROWS>((uint32_t)x);
+}
+// the sum of x up to and with each lane of the wave: shifts within rows of 16 lanes,
+// then the rows' last lanes on to the rows behind them
+template <class X>
+__device__ __forceinline__ X sum_upto(X x) {
+    x += moved<0x111>(x);
+    x += moved<0x112>(x);
+    x += moved<0x114>(x);
+    x += moved<0x118>(x);
+    x += moved<0x142, 0xA>(x);
+    x += moved<0x143, 0xC>(x);
+    return x;
+}
+__device__ __forceinline__ double last_lane(double x) {
+    return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(x), 63),
+                            __builtin_amdgcn_readlane(__double2loint(x), 63));
+}
+__device__ __forceinline__ uint64_t last_lane(uint64_t x) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), 63) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+// the largest of 16 lanes, in all of them
+__device__ __forceinline__ float largest_of_16(float x) {
+    x = fmaxf(x, __uint_as_float(moved<0x128>(__float_as_uint(x))));  // (rotations: no lane goes without)
+    x = fmaxf(x, __uint_as_float(moved<0x124>(__float_as_uint(x))));
+    x = fmaxf(x, __uint_as_float(moved<0x122>(__float_as_uint(x))));
+    return fmaxf(x, __uint_as_float(moved<0x121>(__float_as_uint(x))));
+}
+
+// One wave a part, four of them a block.  Rows without a filter need a part's largest
+// logit and its sum of weights; rows with one also how much weight, or where that is
+// not asked for how many logits, lie in each bucket.
 template <class T>
-__global__ void __launch_bounds__(kPartThreads) sample_part_kernel(
-    const T* __restrict__ logits, int64_t ld, const Request q, int V, int parts,
-    float* __restrict__ tops, double* __restrict__ sums) {
-    constexpr int VEC = Row<T>::VEC, NL = kEach / VEC, NW = kPartThreads / 64;
-    __shared__ float wave_top[NW];
-    __shared__ double wave_sum[NW];
-    __shared__ int wave_bad[NW];
+__global__ void __launch_bounds__(64 * kBlockWaves) sample_part_kernel(
+    const T* __restrict__ logits, int64_t ld, const Request q, int V, const Found out) {
+    constexpr int VEC = Row<T>::VEC, NL = kEach / VEC, NT = 64 * kBlockWaves;
+    __shared__ unsigned long long bucket[kBuckets * kCopies];
+    uint32_t* const number = reinterpret_cast<uint32_t*>(bucket);
+    __shared__ float wave_top[kBlockWaves];
     const int64_t row = blockIdx.y;
-    const int part = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t block = row * out.blocks + blockIdx.x;
+    const int part = blockIdx.x * kBlockWaves + wave;
     const Row<T> r(logits + row * ld);
-    const int64_t first = (int64_t)part * NL * kPartThreads + tid;
-    uint4 raw[NL];
+    const int64_t from = (int64_t)part * NL * 64;
+    const bool inside = r.column(from) >= 0 && r.column(from + NL * 64) <= V;
+    float v[NL][VEC];
+    {
+        uint4 raw[NL];
+        if (inside) {
+            const uint4* p = reinterpret_cast<const uint4*>(r.src + r.column(from + lane));
 #pragma unroll
-    for (int i = 0; i < NL; ++i) raw[i] = r.fetch(first + i * kPartThreads, V);
+            for (int i = 0; i < NL; ++i) raw[i] = p[64 * i];
+#pragma unroll
+            for (int i = 0; i < NL; ++i) r.values(raw[i], v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) raw[i] = r.fetch(from + lane + 64 * i, V);
+#pragma unroll
+            for (int i = 0; i < NL; ++i) r.unpack(raw[i], from + lane + 64 * i, V, v[i]);
+        }
+    }
     const Want want(q, row, V);
-    float v[NL][VEC], top = -INFINITY;
+    float own[NL], top = -INFINITY, low = INFINITY;
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-        r.unpack(raw[i], first + i * kPartThreads, V, v[i]);
+        own[i] = v[i][0];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             bad |= !(v[i][e] < INFINITY);
-            top = fmaxf(top, v[i][e]);
+            own[i] = fmaxf(own[i], v[i][e]);
+            low = fminf(low, v[i][e]);
         }
+        top = fmaxf(top, own[i]);
     }
     for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
     bad = __any(bad);
-    if (lane == 0) {
-        wave_top[wave] = top;
-        wave_bad[wave] = bad;
-    }
-    __syncthreads();
+    if (lane == 0)
+        out.tops[row * out.blocks * kBlockWaves + part] = bad ? __uint_as_float(0x7FC00000u) : top;
+    const bool filtered = want.filtered();
+    if (filtered) {
+        for (int b = tid; b < kBuckets * kCopies; b += NT) bucket[b] = 0;
+        if (lane == 0) wave_top[wave] = top;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        top = fmaxf(top, wave_top[w]);
-        bad |= wave_bad[w] != 0;
+        for (int w = 0; w < kBlockWaves; ++w) top = fmaxf(top, wave_top[w]);
     }
-    if (tid == 0) tops[row * parts + part] = bad ? __uint_as_float(0x7FC00000u) : top;
-    if (!want.whole_sum() || bad || top == -INFINITY) return;
+    if (top == -INFINITY) return;  // (the whole block, where it has a barrier ahead)
     double s = 0.0;
+    if (!filtered) {
+        if (!want.whole_sum() || bad) return;
+        if (__all(((double)low - (double)top) >= want.least)) {
 #pragma unroll
-    for (int i = 0; i < NL; ++i)
+            for (int i = 0; i < NL; ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s += weight((double)v[i][e] - (double)top, want.c);
-    for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
-    if (lane == 0) wave_sum[wave] = s;
-    __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < NW; ++w) s += wave_sum[w];
-        sums[row * parts + part] = s;
+                for (int e = 0; e < VEC; ++e) s += weight((double)v[i][e] - (double)top, want.c);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) s += want.weigh(v[i][e], top);
+        }
+    } else {
+        const int most = want.bucket(top), copy = lane & (kCopies - 1);
+        const bool weights = want.whole_sum();
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const float g = largest_of_16(own[i]);
+            if ((lane & (kGroup - 1)) == 0)
+                out.groups[row * out.blocks * (NT * NL / kGroup) + (from + lane + 64 * i) / kGroup] = g;
+        }
+        if (weights) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float x = v[i][e];
+                    const double w = want.weigh(x, top);
+                    s += w;
+                    // whole numbers of 2^-48, in any order: 2^13 of them at most
+                    if (x > -INFINITY)
+                        atomicAdd(&bucket[min(most - want.bucket(x), kRest) * kCopies + copy],
+                                  (unsigned long long)(__double_as_longlong(w + 16.0) -
+                                                       __double_as_longlong(16.0)));
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float x = v[i][e];
+                    if (x > -INFINITY) {
+                        s += 1.0;
+                        atomicAdd(&number[min(most - want.bucket(x), kRest) * kCopies + copy], 1u);
+                    }
+                }
+        }
+        __syncthreads();
+        for (int b = tid; b < kBuckets; b += NT) {
+            uint64_t all = 0;
+#pragma unroll
+            for (int j = 0; j < kCopies; ++j)
+                all += weights ? bucket[b * kCopies + j] : number[b * kCopies + j];
+            out.buckets[block * kBuckets + b] = (double)all * (weights ? 0x1p-48 : 1.0);
+        }
     }
+    s = last_lane(sum_upto(s));
+    if (lane == 0) out.sums[row * out.blocks * kBlockWaves + part] = s;
 }
 
 // What the threads of a row's workgroup exchange
 struct Shared {
     double sum[kRowWaves];
-    uint64_t whole[kRowWaves];
+    uint64_t whole[2][kRowWaves];
     uint32_t count[kBins];
     uint64_t mass[kBins];
-    int first, last;
-    double below;
-    int32_t token;
-    double token_weight;
+    int first, last, hits, listed, at[kRowWaves];
+    bool none;
+    uint64_t above[3];
+    double found[3];
+    double factor[kMostBlocks], blocks[kMostBlocks];
+    int offset[kMostBlocks];
+    float list_x[kList];
+    int list_i[kList];
+    __align__(8) int hit[kHits];
 };
 
 // sum over the workgroup, and this thread's share of it: what lies before it
 __device__ __forceinline__ double scan(double own, Shared& sh, double* total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double upto = own;
-    for (int o = 1; o < 64; o <<= 1) {
-        const double y = __shfl_up(upto, o, 64);
-        if (lane >= o) upto += y;
-    }
+    const double upto = sum_upto(own);
     __syncthreads();
     if (lane == 63) sh.sum[wave] = upto;
     __syncthreads();
     double before = 0.0, all = 0.0;
+#pragma unroll
     for (int w = 0; w < kRowWaves; ++w) {
-        if (w < wave) before += sh.sum[w];
-        all += sh.sum[w];
+        const double x = sh.sum[w];
+        if (w < wave) before += x;
+        all += x;
     }
     *total = all;
-    const double prev = __shfl_up(upto, 1, 64);
-    return before + (lane ? prev : 0.0);
+    return before + moved<0x138>(upto);  // (the lane before; 0 for the first)
 }
-__device__ __forceinline__ uint64_t scan(uint64_t own, Shared& sh) {
+// two at once: what lies before this thread's n and m
+__device__ __forceinline__ void scan(uint64_t& n, uint64_t& m, Shared& sh) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint64_t upto = own;
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint64_t y = __shfl_up(upto, o, 64);
-        if (lane >= o) upto += y;
+    const uint64_t upto_n = sum_upto(n), upto_m = sum_upto(m);
+    if (lane == 63) {
+        sh.whole[0][wave] = upto_n;
+        sh.whole[1][wave] = upto_m;
     }
     __syncthreads();
-    if (lane == 63) sh.whole[wave] = upto;
+    n = upto_n - n;
+    m = upto_m - m;
+#pragma unroll
+    for (int w = 0; w < kRowWaves - 1; ++w) {
+        const uint64_t a = sh.whole[0][w], b = sh.whole[1][w];
+        n += w < wave ? a : 0;
+        m += w < wave ? b : 0;
+    }
+}
+__device__ __forceinline__ uint64_t total_of(uint64_t own, Shared& sh) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    own = sum_upto(own);
     __syncthreads();
-    uint64_t before = upto - own;
-    for (int w = 0; w < wave; ++w) before += sh.whole[w];
-    return before;
+    if (lane == 63) sh.whole[0][wave] = own;
+    __syncthreads();
+    uint64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < kRowWaves; ++w) all += sh.whole[0][w];
+    return all;
 }
 
 // the lowest thread for which `is` holds, kRowThreads if none; all threads call
 __device__ __forceinline__ int lowest(bool is, Shared& sh) {
+    const uint64_t set = __ballot(is);
     __syncthreads();
-    if (threadIdx.x == 0) sh.first = kRowThreads;
+    if ((threadIdx.x & 63) == 0) sh.at[threadIdx.x >> 6] = set ? (int)threadIdx.x + __builtin_ctzll(set) : kRowThreads;
     __syncthreads();
-    if (is) atomicMin(&sh.first, (int)threadIdx.x);
-    __syncthreads();
-    return sh.first;
+    int first = kRowThreads;
+#pragma unroll
+    for (int w = 0; w < kRowWaves; ++w) first = min(first, sh.at[w]);
+    return first;
 }
+// the highest one, -1 if none
 __device__ __forceinline__ int highest(bool is, Shared& sh) {
+    const uint64_t set = __ballot(is);
     __syncthreads();
-    if (threadIdx.x == 0) sh.last = -1;
+    if ((threadIdx.x & 63) == 0) sh.at[threadIdx.x >> 6] = set ? (int)threadIdx.x + 63 - __builtin_clzll(set) : -1;
     __syncthreads();
-    if (is) atomicMax(&sh.last, (int)threadIdx.x);
-    __syncthreads();
-    return sh.last;
+    int last = -1;
+#pragma unroll
+    for (int w = 0; w < kRowWaves; ++w) last = max(last, sh.at[w]);
+    return last;
 }
 
 // The thread whose share of the sums holds `target`: the first whose end lies behind
@@ -221,34 +384,120 @@ __device__ __forceinline__ int holder(double before, double own, double target, 
 // its index at most idx.
 struct Cut {
     uint32_t key = 0;
-    int idx = 0x7FFFFFFF;
-    __device__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= idx); }
+    uint32_t idx = 0xFFFFFFFFu;
+    __device__ bool keeps(float x, int i) const {
+        const uint32_t k = key_of(x);
+        return k > key || (k == key && (uint32_t)i <= idx);
+    }
 };
 
-// A row, its weights, and passes over it by the workgroup
-template <class T>
-struct Whole {
-    static constexpr int VEC = Row<T>::VEC;
-    const Row<T> r;
-    const int V;
-    const double c;
+// Logits and their weights in whole numbers of 2^-scale, so that they add up to the same in any
+// order.  Each: each(f) calls f(logit, index) for its logits above -infinity, spread over
+// the workgroup's threads.
+template <class Each>
+struct Narrow {
+    const Each& each;
+    const Want& want;
     const float top;
-    const int pieces;
-    __device__ Whole(const T* row, int V_, double c_, float top_)
-        : r(row), V(V_), c(c_), top(top_), pieces((r.before + V_ + VEC - 1) / VEC) {}
-    __device__ double weight_of(float x) const { return weight((double)x - (double)top, c); }
+    const double magic, unit;  // 2^(52 - scale), 2^-scale
+    Shared& sh;
 
-    // f(x, index) for all logits but those at -infinity, pieces in turn
-    template <class F>
-    __device__ __forceinline__ void every(F f) const {
-        for (int i = threadIdx.x; i < pieces; i += kRowThreads) some(i, f);
+    __device__ __forceinline__ uint64_t units(float x) const {
+        return (uint64_t)(__double_as_longlong(want.weigh(x, top) + magic) - __double_as_longlong(magic));
     }
-    // the same with a run of neighbouring pieces for each thread
-    template <class F>
-    __device__ __forceinline__ void in_order(F f) const {
-        const int each = (pieces + kRowThreads - 1) / kRowThreads;
-        const int from = threadIdx.x * each, to = min(from + each, pieces);
-        for (int i = from; i < to; ++i) some(i, f);
+    // The first place (of those in [lo, hi], what place(logit, index) is; ~0: no candidate) up
+    // to which reached(number, weight) holds of the candidates; passes over them narrow it
+    // down by a factor of kBins each.  False where it is never reached.  n, m: what
+    // lies before the place, ties: the candidates at it.
+    template <class Place, class Reached>
+    __device__ __forceinline__ bool find(uint32_t& lo, uint32_t hi, bool weights, Place place, Reached reached,
+                         uint64_t& n, uint64_t& m, uint64_t& ties) const {
+        const int tid = threadIdx.x;
+        n = m = 0;
+        while (true) {
+            const int shift = lo < hi ? max(0, 32 - kBinBits - __builtin_clz(hi - lo)) : 0;
+            __syncthreads();
+            sh.count[tid] = 0;
+            sh.mass[tid] = 0;
+            if (tid == 0) sh.none = true;
+            __syncthreads();
+            each([&](float x, int i) {
+                const uint32_t at = place(x, i);
+                if (at < lo || at > hi) return;
+                atomicAdd(&sh.count[(at - lo) >> shift], 1u);
+                if (weights)
+                    atomicAdd((unsigned long long*)&sh.mass[(at - lo) >> shift], (unsigned long long)units(x));
+            });
+            __syncthreads();
+            const uint64_t own_n = sh.count[tid], own_m = sh.mass[tid];
+            uint64_t before_n = own_n, before_m = own_m;
+            scan(before_n, before_m, sh);
+            // (whole numbers: one thread's share is the first that reaches)
+            if (own_n > 0 && reached(n + before_n + own_n, m + before_m + own_m) &&
+                !(before_n > 0 && reached(n + before_n, m + before_m))) {
+                sh.above[0] = n + before_n;
+                sh.above[1] = m + before_m;
+                sh.above[2] = own_n;
+                sh.first = tid;
+                sh.none = false;
+            }
+            __syncthreads();
+            if (sh.none) return false;
+            const int at = sh.first;
+            n = sh.above[0];
+            m = sh.above[1];
+            ties = sh.above[2];
+            lo += (uint32_t)at << shift;
+            if (shift == 0) return true;
+            hi = min(hi, lo + ((1u << shift) - 1));
+        }
+    }
+    // The cut that keeps the first k of those that `in` keeps (k > 0), or those before
+    // which less than target (in units) lies.
+    __device__ __forceinline__ Cut cut(const Cut in, int k, double target, int V) const {
+        uint32_t at = ~key_of(top), idx = 0;
+        uint64_t n, m, ties;
+        if (!find(at, ~max(in.key, kLeastKey), k == 0,
+                  [&](float x, int i) { return in.keeps(x, i) ? ~key_of(x) : ~0u; },
+                  [&](uint64_t a, uint64_t b) { return k ? a >= (uint64_t)k : (double)b >= target; },
+                  n, m, ties))
+            return in;  // all of them do not reach it
+        Cut out;
+        out.key = ~at;
+        out.idx = in.key == out.key ? in.idx : ~0u;
+        // how many of the equal ones at the cut stay, and the last of these
+        double stay = (double)k - (double)n;
+        if (k == 0) stay = ceil((target - (double)m) / (want.weigh(value_of(out.key), top) / unit));
+        const uint64_t r = stay < 1.0 ? 1 : stay > 0x1p31 ? (uint64_t)1 << 31 : (uint64_t)stay;
+        if (r < ties && find(idx, (uint32_t)V - 1, false,
+                             [&](float x, int i) {
+                                 return key_of(x) == out.key && in.keeps(x, i) ? (uint32_t)i : ~0u;
+                             },
+                             [&](uint64_t a, uint64_t) { return a >= r; }, n, m, ties))
+            out.idx = idx;
+        return out;
+    }
+};
+template <class Each>
+__device__ __forceinline__ Narrow<Each> narrow(const Each& each, const Want& want, float top, int scale, Shared& sh) {
+    return Narrow<Each>{each, want, top, ldexp(1.0, 52 - scale), ldexp(1.0, -scale), sh};
+}
+
+// One workgroup a row.
+template <class T>
+struct Sampler {
+    static constexpr int VEC = Row<T>::VEC, NL = kEach / VEC, kPieces = kBlock / VEC;
+    const Row<T> r;
+    const int V, pieces;
+    const Want& want;
+    const float top;
+    Shared& sh;
+    int32_t* token;
+    float* logprob;  // or null
+
+    __device__ __forceinline__ void emit(int i, double lp) const {
+        *token = i;
+        if (logprob) *logprob = (float)lp;
     }
     template <class F>
     __device__ __forceinline__ void some(int i, F f) const {
@@ -258,223 +507,534 @@ struct Whole {
         for (int e = 0; e < VEC; ++e)
             if (x[e] > -INFINITY) f(x[e], (int)r.column(i) + e);
     }
+    // f for the row's logits but those at -infinity, pieces in turn
+    template <class F>
+    __device__ __forceinline__ void every(F f) const {
+        constexpr int AT = 4;
+        for (int i0 = threadIdx.x; i0 < pieces; i0 += AT * kRowThreads) {
+            uint4 raw[AT];
+#pragma unroll
+            for (int j = 0; j < AT; ++j) raw[j] = r.fetch(i0 + j * kRowThreads, V);
+#pragma unroll
+            for (int j = 0; j < AT; ++j) {
+                float x[VEC];
+                r.unpack(raw[j], i0 + j * kRowThreads, V, x);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (x[e] > -INFINITY) f(x[e], (int)r.column(i0 + j * kRowThreads) + e);
+            }
+        }
+    }
+    // f for those of pieces from .. to, a run of neighbouring ones for each thread
+    template <class F>
+    __device__ __forceinline__ void in_order(int from, int to, F f) const {
+        const int each = (to - from + kRowThreads - 1) / kRowThreads;
+        const int begin = from + threadIdx.x * each, end = min(begin + each, to);
+        for (int i = begin; i < end; ++i) some(i, f);
+    }
 
-    // The cut that keeps the first k elements of `in`, or (k = 0) those whose
-    // predecessors weigh less than target.  Passes over the row narrow the keys
-    // down by a factor of kBins each; weights add up as whole numbers of 2^-scale, in
-    // any order.
-    __device__ Cut cut(const Cut in, int k, double target, Shared& sh) const {
-        const int scale = min(50, 62 - (32 - __builtin_clz(V)));
-        const double magic = ldexp(1.0, 52 - scale), unit = ldexp(1.0, -scale);
-        uint32_t lo = max(in.key, kLeastKey), hi = key_of(top);
-        uint64_t above = 0, mass = 0;
-        const int tid = threadIdx.x;
-        while (lo < hi) {
-            const int shift = max(0, 22 - __builtin_clz(hi - lo));
-            const uint32_t bins = ((hi - lo) >> shift) + 1;
-            __syncthreads();
-            sh.count[tid] = 0;
-            sh.mass[tid] = 0;
-            __syncthreads();
-            every([&](float x, int i) {
-                const uint32_t key = key_of(x);
-                if (key < lo || key > hi || !in.keeps(key, i)) return;
-                const uint32_t at = bins - 1 - ((key - lo) >> shift);  // the largest first
-                atomicAdd(&sh.count[at], 1u);
-                if (k == 0) {
-                    const double w = weight_of(x) + magic;
-                    atomicAdd((unsigned long long*)&sh.mass[at],
-                              (unsigned long long)(__double_as_longlong(w) - __double_as_longlong(magic)));
-                }
+    // The token among the logits of pieces from .. to that stay: the first whose sum
+    // exceeds target; the sum of all is total (0: of these).
+    template <class Stays>
+    __device__ __forceinline__ void pick(int from, int to, double target, double total, Stays stays) const {
+        double own = 0.0, here;
+        in_order(from, to, [&](float x, int i) {
+            const double w = want.weigh(x, top);
+            if (w > kNoWeight && stays(x, i, w)) own += w;
+        });
+        const double before = scan(own, sh, &here);
+        if (total == 0.0) {
+            total = here;
+            target *= here;
+        }
+        if ((int)threadIdx.x != holder(before, own, target, sh)) return;
+        double sum = before, w_token = 0.0;
+        int at = -1;
+        bool done = false;
+        in_order(from, to, [&](float x, int i) {
+            const double w = want.weigh(x, top);
+            if (done || !(w > kNoWeight) || !stays(x, i, w)) return;
+            sum += w;
+            at = i;
+            w_token = w;
+            done = sum > target;
+        });
+        emit(at, log(w_token / total));
+    }
+
+    // the first of the largest: its part, then its place
+    __device__ __forceinline__ void greedy(const float* tops, int parts) const {
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            sh.first = parts;
+            sh.last = V;
+        }
+        __syncthreads();
+        for (int p = threadIdx.x; p < parts; p += kRowThreads)
+            if (tops[p] == top) atomicMin(&sh.first, p);
+        __syncthreads();
+        const int from = sh.first * (NL * 64);
+        for (int i = from + threadIdx.x; i < min(from + NL * 64, pieces); i += kRowThreads)
+            some(i, [&](float x, int at) {
+                if (x == top) atomicMin(&sh.last, at);
             });
+        __syncthreads();
+        if (threadIdx.x == 0) emit(sh.last, 0.0);
+    }
+
+    // No filter: the part that holds the number, then the logit.
+    __device__ __forceinline__ void all(const float* tops, const double* sums, int parts) const {
+        const int each = (parts + kRowThreads - 1) / kRowThreads;
+        const int from = threadIdx.x * each, to = min(from + each, parts);
+        auto sum_of = [&](int p) {
+            const double w = want.weigh(tops[p], top);
+            return w > kNoWeight ? sums[p] * w : 0.0;
+        };
+        double own = 0.0, total;
+        for (int p = from; p < to; ++p) own += sum_of(p);
+        const double before = scan(own, sh, &total), target = want.u * total;
+        const int t = holder(before, own, target, sh);
+        if ((int)threadIdx.x == t) {
+            double sum = before;
+            int part = from;
+            for (int p = from; p < to; ++p) {
+                const double x = sum_of(p);
+                if (!(x > 0.0)) continue;
+                sh.found[0] = sum;
+                part = p;
+                sum += x;
+                if (sum > target) break;
+            }
+            sh.hits = part;
+        }
+        __syncthreads();
+        const int begin = sh.hits * (NL * 64);
+        pick(begin, min(begin + NL * 64, pieces), target - sh.found[0], total,
+             [](float, int, double) { return true; });
+    }
+
+    // Any filters on any row, by passes over it.
+    __device__ __forceinline__ void by_passes(double total) const {
+        auto each = [&](auto f) { every(f); };
+        const auto row = narrow(each, want, top, min(50, 30 + __builtin_clz(V)), sh);
+        Cut keep;
+        if (want.k) keep = row.cut(keep, want.k, 0.0, V);
+        if (want.p < 1.0) {
+            if (want.k) {
+                double own = 0.0;
+                in_order(0, pieces, [&](float x, int i) {
+                    if (keep.keeps(x, i)) own += want.weigh(x, top);
+                });
+                scan(own, sh, &total);
+            }
+            keep = row.cut(keep, 0, want.p * total / row.unit, V);
+        }
+        pick(0, pieces, want.u, 0.0,
+             [&](float x, int i, double w) { return keep.keeps(x, i) && w >= want.m; });
+    }
+
+    // Up to 64 candidates, the first of the order, in LDS: one wave, a candidate a lane.
+    // (total: the sum of all weights of the row, where there is no top-k)
+    __device__ __forceinline__ void few(int n, double total) const {
+        const int lane = threadIdx.x;
+        if (lane >= 64) return;
+        const float x = lane < n ? sh.list_x[lane] : -INFINITY;
+        const int idx = lane < n ? sh.list_i[lane] : 0x7FFFFFFF;
+        const uint32_t key = key_of(x);
+        const double w = lane < n ? want.weigh(x, top) : 0.0;
+        int rank = 0, place = 0;  // in the order, by the index
+        for (int l = 0; l < n; ++l) {
+            const uint32_t k = __builtin_amdgcn_readlane(key, l);
+            const int i = __builtin_amdgcn_readlane(idx, l);
+            rank += (k > key || (k == key && i < idx)) ? 1 : 0;
+            place += i < idx ? 1 : 0;
+        }
+        double* by = reinterpret_cast<double*>(sh.mass);
+        int* at = reinterpret_cast<int*>(sh.count);
+        if (lane < n) by[rank] = w;
+        wave_fence();
+        const int most = want.k > 0 && want.k < n ? want.k : n;
+        const double sorted = lane < most ? by[lane] : 0.0;
+        wave_fence();
+        double upto = sorted;
+        for (int o = 1; o < 64; o <<= 1) {
+            const double y = __shfl_up(upto, o, 64);
+            if (lane >= o) upto += y;
+        }
+        if (want.k > 0) total = __shfl(upto, 63, 64);
+        const double before = __shfl_up(upto, 1, 64);
+        const bool stays = lane < most && (lane == 0 || ((want.p == 1.0 || before < want.p * total) &&
+                                                         sorted >= want.m && sorted > kNoWeight));
+        const int kept = __builtin_popcountll(__ballot(stays));  // the first ones
+        if (lane < n) {
+            by[place] = rank < kept ? w : 0.0;
+            at[place] = idx;
+        }
+        wave_fence();
+        const double own = lane < n ? by[lane] : 0.0;
+        upto = own;
+        for (int o = 1; o < 64; o <<= 1) {
+            const double y = __shfl_up(upto, o, 64);
+            if (lane >= o) upto += y;
+        }
+        const double sum = __shfl(upto, 63, 64), target = want.u * sum;
+        const uint64_t behind = __ballot(own > 0.0 && upto > target), any = __ballot(own > 0.0);
+        const int chosen = behind ? __builtin_ctzll(behind) : 63 - __builtin_clzll(any);
+        if (lane == chosen) emit(at[lane], log(own / sum));
+    }
+
+    // Up to kRanked of them: two threads a candidate count those before it in the order
+    // and by the index.
+    __device__ __forceinline__ void ranked(int n, double total) const {
+        static_assert(2 * kRanked <= kRowThreads && kRanked <= kHits, "");
+        const int tid = threadIdx.x, j = tid >> 1;
+        const bool there = j < n;
+        const float x = there ? sh.list_x[j] : 0.0f;
+        const int idx = there ? sh.list_i[j] : 0;
+        const uint32_t key = key_of(x);
+        const double w = want.weigh(x, top);
+        uint2* all = reinterpret_cast<uint2*>(sh.hit);
+        if (there && !(tid & 1)) all[j] = make_uint2(key, (uint32_t)idx);
+        __syncthreads();
+        int rank = 0, place = 0;
+#pragma unroll 8
+        for (int l = tid & 1; l < n; l += 2) {
+            const uint2 o = all[l];
+            const bool less = (int)o.y < idx;
+            rank += (o.x > key || (o.x == key && less)) ? 1 : 0;
+            place += less ? 1 : 0;
+        }
+        rank += __shfl_xor(rank, 1, 64);
+        place += __shfl_xor(place, 1, 64);
+        const bool writes = there && !(tid & 1);
+        double* by = reinterpret_cast<double*>(sh.mass);
+        int* at = reinterpret_cast<int*>(sh.count);
+        if (writes) by[rank] = w;
+        __syncthreads();
+        const int most = want.k > 0 && want.k < n ? want.k : n;
+        const double sorted = tid < most ? by[tid] : 0.0;
+        double sum;
+        const double before = scan(sorted, sh, &sum);
+        if (want.k > 0) total = sum;
+        const int kept = __syncthreads_count(
+            tid < most && (tid == 0 || ((want.p == 1.0 || before < want.p * total) && sorted >= want.m &&
+                                        sorted > kNoWeight)));
+        if (writes) {
+            by[place] = rank < kept ? w : 0.0;
+            at[place] = idx;
+        }
+        __syncthreads();
+        const double own = tid < n ? by[tid] : 0.0;
+        const double upto = scan(own, sh, &sum);
+        if (tid == holder(upto, own, want.u * sum, sh)) emit(at[tid], log(own / sum));
+    }
+
+    // The candidates in LDS are the first of the order, and all that stay is among them.
+    __device__ __forceinline__ void from_list(int n, double total) const {
+        auto each = [&](auto f) {
+            for (int j = threadIdx.x; j < n; j += kRowThreads) f(sh.list_x[j], sh.list_i[j]);
+        };
+        const auto list = narrow(each, want, top, 50, sh);
+        Cut keep;
+        auto sum_of = [&](auto stays) {
+            uint64_t own = 0;
+            each([&](float x, int i) { own += stays(x, i) ? list.units(x) : 0; });
+            return (double)total_of(own, sh);
+        };
+        if (want.k) {
+            keep = list.cut(keep, want.k, 0.0, V);
+            total = want.p < 1.0 ? sum_of([&](float x, int i) { return keep.keeps(x, i); }) : 0.0;
+        } else {
+            total /= list.unit;
+        }
+        if (want.p < 1.0) keep = list.cut(keep, 0, want.p * total, V);
+        auto stays = [&](float x, int i) {
+            const double w = want.weigh(x, top);
+            return keep.keeps(x, i) && w >= want.m && w > kNoWeight;
+        };
+        const double sum = sum_of(stays), target = want.u * sum;
+        uint32_t idx = 0;
+        uint64_t a, b, ties;
+        // (a number of 0 takes the first one, however little it weighs)
+        list.find(idx, (uint32_t)V - 1, true,
+                  [&](float x, int i) { return stays(x, i) ? (uint32_t)i : ~0u; },
+                  [&](uint64_t, uint64_t m) { return target == 0.0 || (double)m > target; }, a, b, ties);
+        each([&](float x, int i) {
+            if ((uint32_t)i == idx) emit(i, log(want.weigh(x, top) / (sum * list.unit)));
+        });
+    }
+
+    // The logits of buckets first .. last into the list; how many there are.
+    __device__ __forceinline__ int gather(const float* groups, int n_groups, int most, int first, int last) const {
+        const int tid = threadIdx.x, lane = tid & (kGroup - 1);
+        if (tid == 0) sh.listed = 0;
+        for (int g0 = 0; g0 < n_groups; g0 += kHits) {
             __syncthreads();
-            const uint64_t own_n = sh.count[tid], own_m = sh.mass[tid];
-            const uint64_t n = above + scan(own_n, sh), m = mass + scan(own_m, sh);
-            const int at = lowest(k ? n + own_n >= (uint64_t)k : (double)(m + own_m) * unit >= target, sh);
-            if (at == kRowThreads) return in;  // all of them do not reach it
-            __syncthreads();
-            if (tid == at) {
-                sh.whole[0] = n;
-                sh.whole[1] = m;
+            if (tid == 0) sh.hits = 0;
+            float x[kHits / kRowThreads];
+#pragma unroll
+            for (int j = 0; j < kHits / kRowThreads; ++j) {
+                const int g = g0 + j * kRowThreads + tid;
+                x[j] = g < n_groups ? groups[g] : -INFINITY;
             }
             __syncthreads();
-            above = sh.whole[0];
-            mass = sh.whole[1];
-            lo += (bins - 1 - (uint32_t)at) << shift;
-            hi = min(hi, lo + ((1u << shift) - 1));
-        }
-        // how many of the equal ones at the cut stay, and the last of these
-        double stay = (double)k - (double)above;
-        if (k == 0) {
-            const double w = weight_of(value_of(lo));
-            stay = ceil((target - (double)mass * unit) / w);
-        }
-        const uint64_t r = stay < 1.0 ? 1 : stay > 0x1p31 ? (uint64_t)1 << 31 : (uint64_t)stay;
-        uint64_t ties = 0;
-        in_order([&](float x, int i) { ties += key_of(x) == lo && in.keeps(lo, i); });
-        const uint64_t before = scan(ties, sh);
-        Cut out;
-        out.key = lo;
-        const int at = lowest(before < r && before + ties >= r, sh);
-        if (at == kRowThreads) {  // all of them
-            out.idx = in.key == lo ? in.idx : 0x7FFFFFFF;
-            return out;
+#pragma unroll
+            for (int j = 0; j < kHits / kRowThreads; ++j)
+                if (x[j] > -INFINITY && min(most - want.bucket(x[j]), kRest) <= last)
+                    sh.hit[atomicAdd(&sh.hits, 1)] = g0 + j * kRowThreads + tid;
+            __syncthreads();
+            const int hits = sh.hits;
+            constexpr int AT = 8, HOP = kRowThreads / kGroup;
+            for (int h0 = tid / kGroup; h0 < hits; h0 += AT * HOP) {
+                uint4 raw[AT];
+                int piece[AT];
+#pragma unroll
+                for (int j = 0; j < AT; ++j) {
+                    const int h = h0 + j * HOP;
+                    piece[j] = h < hits ? sh.hit[h] * kGroup + lane : -1;
+                    raw[j] = make_uint4(0, 0, 0, 0);
+                    if (piece[j] >= 0) raw[j] = r.fetch(piece[j], V);
+                }
+#pragma unroll
+                for (int j = 0; j < AT; ++j) {
+                    if (piece[j] < 0) continue;
+                    float v[VEC];
+                    r.unpack(raw[j], piece[j], V, v);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const int b = min(most - want.bucket(v[e]), kRest);
+                        if (v[e] > -INFINITY && b >= first && b <= last) {
+                            const int at = atomicAdd(&sh.listed, 1);
+                            if (at < kList) {
+                                sh.list_x[at] = v[e];
+                                sh.list_i[at] = (int)r.column(piece[j]) + e;
+                            }
+                        }
+                    }
+                }
+            }
         }
         __syncthreads();
-        if (tid == at) {
-            uint64_t seen = before;
-            in_order([&](float x, int i) {
-                if (key_of(x) == lo && in.keeps(lo, i) && ++seen == r) sh.last = i;
-            });
+        return sh.listed;
+    }
+
+    // Filters: the blocks' buckets joined say in which bucket the order is cut.  False
+    // where they do not, or it holds too many logits; total: the sum of the row's
+    // weights, where top-p asks for it, or the number of its logits.
+    __device__ __forceinline__ bool by_buckets(const float* tops, const double* sums, const float* groups,
+                                               const double* buckets, int blocks, double& total) const {
+        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+        const bool weights = want.whole_sum();
+        double own = 0.0;
+        total = 0.0;
+        if (blocks > kMostBlocks) {
+            if (weights) {
+                double own = 0.0;
+                for (int g = tid; g < blocks; g += kRowThreads) {
+                    const float4 t = reinterpret_cast<const float4*>(tops)[g];
+                    const float x = fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w));
+                    if (!(x > -INFINITY)) continue;
+                    double s = 0.0;
+                    for (int w = 0; w < kBlockWaves; ++w) s += sums[g * kBlockWaves + w];
+                    own += s * want.weigh(x, top);
+                }
+                scan(own, sh, &total);
+            }
+            return false;
+        }
+        const int most = want.bucket(top);
+        if (tid < blocks) {
+            const float4 t = reinterpret_cast<const float4*>(tops)[tid];
+            const float x = fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w));
+            const bool live = x > -INFINITY;
+            const double factor = live ? want.weigh(x, top) : 0.0;
+            sh.offset[tid] = live ? min(most - want.bucket(x), kBuckets) : kBuckets + 1;
+            sh.factor[tid] = weights ? factor : 1.0;
+            if (live) {
+                for (int w = 0; w < kBlockWaves; ++w) own += sums[tid * kBlockWaves + w];
+                if (weights) own *= factor;
+            }
+        }
+        scan(own, sh, &total);  // (and the barriers for offset and factor)
+        static_assert(kBuckets == kRowThreads && kBins == kRowThreads && kMostBlocks <= kBins, "");
+        // a thread a bucket; the row's last one takes what is left (of weights: nothing
+        // is cut there)
+        double in = 0.0, all;
+        for (int g0 = 0; g0 < blocks; g0 += 16) {
+            double x[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {  // (on their way at once)
+                const int g = min(g0 + j, blocks - 1), i = max(tid - sh.offset[g], 0);
+                x[j] = buckets[g * kBuckets + i];
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int g = min(g0 + j, blocks - 1);
+                if (g0 + j < blocks && tid >= sh.offset[g]) in += x[j] * sh.factor[g];
+            }
+        }
+        if (tid == kRest) in = 0.0;
+        const double before = scan(in, sh, &all);
+        if (tid == kRest) in = weights ? 0.0 : total - all;
+        // the bucket that holds the cut
+        int last = kRest;
+        if (want.k || want.p < 1.0)
+            last = min(last, lowest(in > 0.0 && before + in >= (want.k ? (double)want.k : want.p * total), sh));
+        if (want.m > 0.0 && !(want.k && want.p < 1.0)) {  // (the sum of top-k's has to be whole)
+            // below this no weight reaches m (a bucket more for the roundings)
+            const float edge = (float)((double)top + log2(want.m) / want.c);
+            const int bound = most - want.bucket(edge - fabsf(edge) * 0x1p-20f) + 1;
+            last = min(last, max(bound, 0));
+        }
+        // how many logits there are up to it, and in it: where weights were summed at most
+        // as many as if each had its bucket's least
+        double n = in;
+        if (weights) n = tid == kRest ? 2.0 * kList : in * exp2f((float)(tid + 1) * (1.4427f / 32.0f)) + 1.0;
+        const double n_before = weights ? scan(n, sh, &all) : before;
+        __syncthreads();
+        if (tid == last) {
+            sh.found[0] = before;
+            sh.found[1] = n_before;
+            sh.found[2] = n;
         }
         __syncthreads();
-        out.idx = sh.last;
-        return out;
+        const double above = sh.found[0], n_above = sh.found[1], here = sh.found[2];
+        const int n_groups = blocks * (kPieces / kGroup);
+        if (n_above + here <= kList) {
+            const int listed = gather(groups, n_groups, most, 0, last);
+            if (listed > kList) return false;
+            if (listed <= kSome)
+                few(listed, total);
+            else if (listed <= kRanked)
+                ranked(listed, total);
+            else
+                from_list(listed, total);
+            return true;
+        }
+        if (want.k || want.m > 0.0 || here > kList || last == kRest) return false;
+        // Top-p alone, with many before the cut: the bucket's logits say where it lies,
+        // the blocks' buckets which block holds the number.
+        const int listed = gather(groups, n_groups, most, last, last);
+        if (listed > kList) return false;
+        auto each = [&](auto f) {
+            for (int j = tid; j < listed; j += kRowThreads) f(sh.list_x[j], sh.list_i[j]);
+        };
+        const auto list = narrow(each, want, top, 50, sh);
+        const Cut keep = list.cut(Cut(), 0, (want.p * total - above) / list.unit, V);
+        __syncthreads();
+        sh.mass[tid] = 0;
+        __syncthreads();
+        each([&](float x, int i) {
+            if (keep.keeps(x, i))
+                atomicAdd((unsigned long long*)&sh.mass[(i + r.before) / kBlock], (unsigned long long)list.units(x));
+        });
+        for (int g = wave; g < blocks; g += kRowWaves) {
+            double s = 0.0;
+#pragma unroll
+            for (int j = 0; j < kBuckets / 64; ++j) {
+                const int i = lane + 64 * j;
+                if (i + sh.offset[g] < last) s += buckets[g * kBuckets + i];
+            }
+            for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
+            if (lane == 0) sh.blocks[g] = s * sh.factor[g];
+        }
+        __syncthreads();
+        own = tid < blocks ? sh.blocks[tid] + (double)sh.mass[tid] * list.unit : 0.0;
+        double stay;
+        const double at = scan(own, sh, &stay), target = want.u * stay;
+        const int block = holder(at, own, target, sh);
+        if (tid == block) sh.found[0] = at;
+        __syncthreads();
+        pick(block * kPieces, min((block + 1) * kPieces, pieces), target - sh.found[0], stay,
+             [&](float x, int i, double) {
+                 const int q = most - want.bucket(x);
+                 return q < last || (q == last && keep.keeps(x, i));
+             });
+        return true;
     }
 };
 
-// One workgroup a row.
 template <class T>
 __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(
-    const T* __restrict__ logits, int64_t ld, const Request q, int V, int parts,
-    const float* __restrict__ tops, const double* __restrict__ sums, int32_t* __restrict__ tokens,
-    float* __restrict__ logprobs, uint32_t* __restrict__ err) {
-    constexpr int VEC = Row<T>::VEC;
+    const T* __restrict__ logits, int64_t ld, const Request q, int V, const Found in,
+    int32_t* __restrict__ tokens, float* __restrict__ logprobs, uint32_t* __restrict__ err) {
     __shared__ Shared sh;
     const int64_t row = blockIdx.x;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, parts = in.blocks * kBlockWaves;
+    const float* tops = in.tops + row * parts;
+    float top = -INFINITY;
+    bool nan = false;
+    for (int p = tid; p < parts; p += kRowThreads) {
+        const float t = tops[p];
+        nan |= t != t;
+        top = fmaxf(top, t);
+    }
     const Want want(q, row, V);
-    auto emit = [&](int token, double logprob) {
-        tokens[row] = token;
-        if (logprobs) logprobs[row] = (float)logprob;
-    };
-    // (a part a thread: parts <= kRowThreads)
-    const float own_top = tid < parts ? tops[row * parts + tid] : -INFINITY;
-    float top = own_top;
     for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-    const bool nan = __syncthreads_or(own_top != own_top);
     if ((tid & 63) == 0) sh.sum[tid >> 6] = top;
-    __syncthreads();
+    nan = __syncthreads_or(nan);
     for (int w = 0; w < kRowWaves; ++w) top = fmaxf(top, (float)sh.sum[w]);
+    const Row<T> r(logits + row * ld);
+    const Sampler<T> s{r, V, (r.before + V + Row<T>::VEC - 1) / Row<T>::VEC, want, top, sh,
+                       tokens + row, logprobs ? logprobs + row : nullptr};
     if (want.bad || nan || top == -INFINITY) {
         if (tid == 0) {
-            emit(-1, -INFINITY);
+            s.emit(-1, -INFINITY);
             if (err && (want.bad || nan))
                 atomicOr(err, (want.bad ? ENGRAM_ERRBIT_SAMPLE : 0) | (nan ? ENGRAM_ERRBIT_LOGIT : 0));
         }
         return;
     }
-    const Whole<T> x(logits + row * ld, V, want.c, top);
-    if (want.greedy()) {
-        // the first part with the largest logit, and its first place there
-        const int part = lowest(own_top == top, sh);
-        __syncthreads();
-        if (tid == 0) sh.last = V;
-        __syncthreads();
-        constexpr int pieces = kPart / VEC;
-        for (int i = part * pieces + tid; i < min((part + 1) * pieces, x.pieces); i += kRowThreads)
-            x.some(i, [&](float v, int at) {
-                if (v == top) atomicMin(&sh.last, at);
-            });
-        __syncthreads();
-        if (tid == 0) emit(sh.last, 0.0);
-        return;
-    }
-    double own = 0.0, total = 0.0, before = 0.0;
-    if (want.whole_sum()) {
-        const double w = weight((double)own_top - (double)top, want.c);
-        if (w > kNoWeight) own = sums[row * parts + tid] * w;
-        before = scan(own, sh, &total);
-    }
-    // f(thread's run of pieces): the pick among the run's elements that stay
-    auto pick = [&](double target, double at, auto stays, auto run) {
-        double sum = at;
-        int token = -1;
-        double w_token = 0.0;
-        bool done = false;
-        run([&](float v, int i) {
-            const double w = x.weight_of(v);
-            if (done || !(w > kNoWeight) || !stays(v, i, w)) return;
-            sum += w;
-            token = i;
-            w_token = w;
-            done = sum > target;
-        });
-        emit(token, log(w_token / total));
-    };
-    if (!want.filtered()) {
-        // the part that holds the number, then the piece
-        double target = want.u * total;
-        const int part = holder(before, own, target, sh);
-        __syncthreads();
-        if (tid == part) sh.below = before;
-        __syncthreads();
-        target -= sh.below;
-        constexpr int pieces = kPart / VEC, each = (pieces + kRowThreads - 1) / kRowThreads;
-        const int from = part * pieces + tid * each, to = min(from + each, x.pieces);
-        auto run = [&](auto f) {
-            for (int i = from; i < to; ++i) x.some(i, f);
-        };
-        own = 0.0;
-        run([&](float v, int) {
-            const double w = x.weight_of(v);
-            own += w > kNoWeight ? w : 0.0;
-        });
-        double here;
-        before = scan(own, sh, &here);
-        if (tid == holder(before, own, target, sh))
-            pick(target, before, [](float, int, double) { return true; }, run);
-        return;
-    }
-    Cut keep;
-    if (want.k) {
-        keep = x.cut(keep, want.k, 0.0, sh);
-        if (want.p < 1.0) {
-            own = 0.0;
-            x.in_order([&](float v, int i) {
-                if (keep.keeps(key_of(v), i)) own += x.weight_of(v);
-            });
-            scan(own, sh, &total);
-        }
-    }
-    if (want.p < 1.0) keep = x.cut(keep, 0, want.p * total, sh);
-    auto stays = [&](float v, int i, double w) { return keep.keeps(key_of(v), i) && w >= want.m; };
-    own = 0.0;
-    x.in_order([&](float v, int i) {
-        const double w = x.weight_of(v);
-        if (w > kNoWeight && stays(v, i, w)) own += w;
-    });
-    before = scan(own, sh, &total);
-    const double target = want.u * total;
-    if (tid == holder(before, own, target, sh))
-        pick(target, before, stays, [&](auto f) { x.in_order(f); });
+    const double* sums = in.sums + row * parts;
+    if (want.greedy()) return s.greedy(tops, parts);
+    if (!want.filtered()) return s.all(tops, sums, parts);
+    const int64_t blocks = row * in.blocks;
+    double total;
+    if (!s.by_buckets(tops, sums, in.groups + blocks * (kBlock / Row<T>::VEC / kGroup),
+                      in.buckets + blocks * kBuckets, in.blocks, total))
+        s.by_passes(total);
 }
 
-int parts_of(int V) { return (int)(((int64_t)V + 7 + kPart - 1) / kPart); }
+int blocks_of(int V) { return (int)(((int64_t)V + 7 + kBlock - 1) / kBlock); }
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+size_t layout(int64_t B, int V, void* base, Found* f) {
+    const size_t blocks = (size_t)B * blocks_of(V);
+    char* at = (char*)base;
+    auto take = [&](size_t bytes) {
+        char* here = at;
+        at += up256(bytes);
+        return here;
+    };
+    f->blocks = blocks_of(V);
+    f->sums = (double*)take(blocks * kBlockWaves * sizeof(double));
+    f->buckets = (double*)take(blocks * kBuckets * sizeof(double));
+    f->tops = (float*)take(blocks * kBlockWaves * sizeof(float));
+    f->groups = (float*)take(blocks * (kBlock / Row<float>::VEC / kGroup) * sizeof(float));
+    return (size_t)(at - (char*)base);
+}
 
 template <class T>
 hipError_t run_sample(const void* logits, int64_t ld, const Request& q, int64_t B, int V,
                       int32_t* tokens, float* logprobs, void* scratch, uint32_t* err,
                       hipStream_t s) {
-    const int parts = parts_of(V);
-    double* sums = (double*)scratch;
-    float* tops = (float*)((char*)scratch + up256((size_t)B * parts * sizeof(double)));
-    sample_part_kernel<T><<<dim3(parts, (uint32_t)B), dim3(kPartThreads), 0, s>>>(
-        (const T*)logits, ld, q, V, parts, tops, sums);
+    Found f;
+    layout(B, V, scratch, &f);
+    sample_part_kernel<T><<<dim3(f.blocks, (uint32_t)B), dim3(64 * kBlockWaves), 0, s>>>(
+        (const T*)logits, ld, q, V, f);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     sample_row_kernel<T><<<dim3((uint32_t)B), dim3(kRowThreads), 0, s>>>(
-        (const T*)logits, ld, q, V, parts, tops, sums, tokens, logprobs, err);
+        (const T*)logits, ld, q, V, f, tokens, logprobs, err);
     return hipGetLastError();
 }
 
 }  // namespace
 
 size_t sample_scratch_bytes(int64_t B, int V) {
-    const size_t n = (size_t)B * parts_of(V);
-    return up256(n * sizeof(double)) + up256(n * sizeof(float));
+    Found f;
+    return layout(B, V, nullptr, &f);
 }
 
 hipError_t launch_sample(const void* logits, bool f32, int64_t ld, const float* u,
