@@ -166,11 +166,11 @@ __device__ __forceinline__ float largest_of_16(float x) {
 // One wave a part, four of them a block.  Rows without a filter need a part's largest
 // logit and its sum of weights; rows with one also how much weight, or where that is
 // not asked for how many logits, lie in each bucket.
-template <class T>
+template <class T, bool FILTERS>
 __global__ void __launch_bounds__(64 * kBlockWaves) sample_part_kernel(
     const T* __restrict__ logits, int64_t ld, const Request q, int V, const Found out) {
     constexpr int VEC = Row<T>::VEC, NL = kEach / VEC, NT = 64 * kBlockWaves;
-    __shared__ unsigned long long bucket[kBuckets * kCopies];
+    __shared__ unsigned long long bucket[FILTERS ? kBuckets * kCopies : 1];
     uint32_t* const number = reinterpret_cast<uint32_t*>(bucket);
     __shared__ float wave_top[kBlockWaves];
     const int64_t row = blockIdx.y;
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(64 * kBlockWaves) sample_part_kernel(
     bad = __any(bad);
     if (lane == 0)
         out.tops[row * out.blocks * kBlockWaves + part] = bad ? __uint_as_float(0x7FC00000u) : top;
-    const bool filtered = want.filtered();
+    const bool filtered = FILTERS && want.filtered();
     if (filtered) {
         for (int b = tid; b < kBuckets * kCopies; b += NT) bucket[b] = 0;
         if (lane == 0) wave_top[wave] = top;
@@ -298,8 +298,7 @@ struct Shared {
     double found[3];
     double factor[kMostBlocks], blocks[kMostBlocks];
     int offset[kMostBlocks];
-    float list_x[kList];
-    int list_i[kList];
+    int list[kList];
     __align__(8) int hit[kHits];
 };
 
@@ -391,20 +390,17 @@ struct Cut {
     }
 };
 
-// Logits and their weights in whole numbers of 2^-scale, so that they add up to the same in any
-// order.  Each: each(f) calls f(logit, index) for its logits above -infinity, spread over
-// the workgroup's threads.
+// Logits and their weights in whole numbers of 2^-scale, so that they add up to the same
+// in any order.  Each: each(f) calls f(logit, index, units) for its logits above -infinity,
+// spread over the workgroup's threads; units() are the weight.
 template <class Each>
 struct Narrow {
     const Each& each;
     const Want& want;
     const float top;
-    const double magic, unit;  // 2^(52 - scale), 2^-scale
+    const double unit;  // 2^-scale
     Shared& sh;
 
-    __device__ __forceinline__ uint64_t units(float x) const {
-        return (uint64_t)(__double_as_longlong(want.weigh(x, top) + magic) - __double_as_longlong(magic));
-    }
     // The first place (of those in [lo, hi], what place(logit, index) is; ~0: no candidate) up
     // to which reached(number, weight) holds of the candidates; passes over them narrow it
     // down by a factor of kBins each.  False where it is never reached.  n, m: what
@@ -421,12 +417,12 @@ struct Narrow {
             sh.mass[tid] = 0;
             if (tid == 0) sh.none = true;
             __syncthreads();
-            each([&](float x, int i) {
+            each([&](float x, int i, auto units) {
                 const uint32_t at = place(x, i);
                 if (at < lo || at > hi) return;
                 atomicAdd(&sh.count[(at - lo) >> shift], 1u);
                 if (weights)
-                    atomicAdd((unsigned long long*)&sh.mass[(at - lo) >> shift], (unsigned long long)units(x));
+                    atomicAdd((unsigned long long*)&sh.mass[(at - lo) >> shift], (unsigned long long)units());
             });
             __syncthreads();
             const uint64_t own_n = sh.count[tid], own_m = sh.mass[tid];
@@ -479,8 +475,13 @@ struct Narrow {
     }
 };
 template <class Each>
-__device__ __forceinline__ Narrow<Each> narrow(const Each& each, const Want& want, float top, int scale, Shared& sh) {
-    return Narrow<Each>{each, want, top, ldexp(1.0, 52 - scale), ldexp(1.0, -scale), sh};
+__device__ __forceinline__ Narrow<Each> narrow(const Each& each, const Want& want, float top, int scale,
+                                               Shared& sh) {
+    return Narrow<Each>{each, want, top, ldexp(1.0, -scale), sh};
+}
+// a weight in whole numbers of 2^-scale, magic = 2^(52 - scale)
+__device__ __forceinline__ uint64_t units_of(double w, double magic) {
+    return (uint64_t)(__double_as_longlong(w + magic) - __double_as_longlong(magic));
 }
 
 // One workgroup a row.
@@ -525,33 +526,29 @@ struct Sampler {
             }
         }
     }
-    // f for those of pieces from .. to, a run of neighbouring ones for each thread
+    // the same, a run of neighbouring pieces for each thread
     template <class F>
-    __device__ __forceinline__ void in_order(int from, int to, F f) const {
-        const int each = (to - from + kRowThreads - 1) / kRowThreads;
-        const int begin = from + threadIdx.x * each, end = min(begin + each, to);
+    __device__ __forceinline__ void in_order(F f) const {
+        const int each = (pieces + kRowThreads - 1) / kRowThreads;
+        const int begin = threadIdx.x * each, end = min(begin + each, pieces);
         for (int i = begin; i < end; ++i) some(i, f);
     }
 
-    // The token among the logits of pieces from .. to that stay: the first whose sum
-    // exceeds target; the sum of all is total (0: of these).
+    // The token among the row's logits that stay: the first whose sum exceeds u times the
+    // sum of all.
     template <class Stays>
-    __device__ __forceinline__ void pick(int from, int to, double target, double total, Stays stays) const {
-        double own = 0.0, here;
-        in_order(from, to, [&](float x, int i) {
+    __device__ __forceinline__ void pick(Stays stays) const {
+        double own = 0.0, total;
+        in_order([&](float x, int i) {
             const double w = want.weigh(x, top);
             if (w > kNoWeight && stays(x, i, w)) own += w;
         });
-        const double before = scan(own, sh, &here);
-        if (total == 0.0) {
-            total = here;
-            target *= here;
-        }
+        const double before = scan(own, sh, &total), target = want.u * total;
         if ((int)threadIdx.x != holder(before, own, target, sh)) return;
         double sum = before, w_token = 0.0;
         int at = -1;
         bool done = false;
-        in_order(from, to, [&](float x, int i) {
+        in_order([&](float x, int i) {
             const double w = want.weigh(x, top);
             if (done || !(w > kNoWeight) || !stays(x, i, w)) return;
             sum += w;
@@ -559,6 +556,46 @@ struct Sampler {
             w_token = w;
             done = sum > target;
         });
+        emit(at, log(w_token / total));
+    }
+    // The token among the logits of pieces from .. to, at most a block of them, held in
+    // registers: the first of those that stay whose sum exceeds target.
+    template <class Stays>
+    __device__ __forceinline__ void pick_near(int from, int to, double target, double total, Stays stays) const {
+        constexpr int E = kPieces / kRowThreads;
+        const int each = (to - from + kRowThreads - 1) / kRowThreads, begin = from + threadIdx.x * each;
+        uint4 raw[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) raw[j] = r.fetch(j < each && begin + j < to ? begin + j : pieces, V);
+        double w[E][VEC], own = 0.0, here;
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const bool in = j < each && begin + j < to;
+            float x[VEC];
+            r.unpack(raw[j], in ? begin + j : pieces, V, x);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                w[j][e] = want.weigh(x[e], top);
+                if (!(w[j][e] > kNoWeight && x[e] > -INFINITY && stays(x[e], (int)r.column(begin + j) + e)))
+                    w[j][e] = 0.0;
+                own += w[j][e];
+            }
+        }
+        const double before = scan(own, sh, &here);
+        if ((int)threadIdx.x != holder(before, own, target, sh)) return;
+        double sum = before, w_token = 0.0;
+        int at = -1;
+        bool done = false;
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                if (done || !(w[j][e] > 0.0)) continue;
+                sum += w[j][e];
+                at = (int)r.column(begin + j) + e;
+                w_token = w[j][e];
+                done = sum > target;
+            }
         emit(at, log(w_token / total));
     }
 
@@ -609,28 +646,31 @@ struct Sampler {
         }
         __syncthreads();
         const int begin = sh.hits * (NL * 64);
-        pick(begin, min(begin + NL * 64, pieces), target - sh.found[0], total,
-             [](float, int, double) { return true; });
+        pick_near(begin, min(begin + NL * 64, pieces), target - sh.found[0], total,
+                  [](float, int) { return true; });
     }
 
     // Any filters on any row, by passes over it.
     __device__ __forceinline__ void by_passes(double total) const {
-        auto each = [&](auto f) { every(f); };
-        const auto row = narrow(each, want, top, min(50, 30 + __builtin_clz(V)), sh);
+        const int scale = min(50, 30 + __builtin_clz(V));
+        const double magic = ldexp(1.0, 52 - scale);
+        auto each = [&](auto f) {
+            every([&](float x, int i) { f(x, i, [&] { return units_of(want.weigh(x, top), magic); }); });
+        };
+        const auto row = narrow(each, want, top, scale, sh);
         Cut keep;
         if (want.k) keep = row.cut(keep, want.k, 0.0, V);
         if (want.p < 1.0) {
             if (want.k) {
                 double own = 0.0;
-                in_order(0, pieces, [&](float x, int i) {
+                in_order([&](float x, int i) {
                     if (keep.keeps(x, i)) own += want.weigh(x, top);
                 });
                 scan(own, sh, &total);
             }
             keep = row.cut(keep, 0, want.p * total / row.unit, V);
         }
-        pick(0, pieces, want.u, 0.0,
-             [&](float x, int i, double w) { return keep.keeps(x, i) && w >= want.m; });
+        pick([&](float x, int i, double w) { return keep.keeps(x, i) && w >= want.m; });
     }
 
     // Up to 64 candidates, the first of the order, in LDS: one wave, a candidate a lane.
@@ -638,8 +678,8 @@ struct Sampler {
     __device__ __forceinline__ void few(int n, double total) const {
         const int lane = threadIdx.x;
         if (lane >= 64) return;
-        const float x = lane < n ? sh.list_x[lane] : -INFINITY;
-        const int idx = lane < n ? sh.list_i[lane] : 0x7FFFFFFF;
+        const int idx = lane < n ? sh.list[lane] : 0x7FFFFFFF;
+        const float x = lane < n ? value(idx) : -INFINITY;
         const uint32_t key = key_of(x);
         const double w = lane < n ? want.weigh(x, top) : 0.0;
         int rank = 0, place = 0;  // in the order, by the index
@@ -656,13 +696,9 @@ struct Sampler {
         const int most = want.k > 0 && want.k < n ? want.k : n;
         const double sorted = lane < most ? by[lane] : 0.0;
         wave_fence();
-        double upto = sorted;
-        for (int o = 1; o < 64; o <<= 1) {
-            const double y = __shfl_up(upto, o, 64);
-            if (lane >= o) upto += y;
-        }
-        if (want.k > 0) total = __shfl(upto, 63, 64);
-        const double before = __shfl_up(upto, 1, 64);
+        double upto = sum_upto(sorted);
+        if (want.k > 0) total = last_lane(upto);
+        const double before = moved<0x138>(upto);  // (the lane before's)
         const bool stays = lane < most && (lane == 0 || ((want.p == 1.0 || before < want.p * total) &&
                                                          sorted >= want.m && sorted > kNoWeight));
         const int kept = __builtin_popcountll(__ballot(stays));  // the first ones
@@ -672,12 +708,8 @@ struct Sampler {
         }
         wave_fence();
         const double own = lane < n ? by[lane] : 0.0;
-        upto = own;
-        for (int o = 1; o < 64; o <<= 1) {
-            const double y = __shfl_up(upto, o, 64);
-            if (lane >= o) upto += y;
-        }
-        const double sum = __shfl(upto, 63, 64), target = want.u * sum;
+        upto = sum_upto(own);
+        const double sum = last_lane(upto), target = want.u * sum;
         const uint64_t behind = __ballot(own > 0.0 && upto > target), any = __ballot(own > 0.0);
         const int chosen = behind ? __builtin_ctzll(behind) : 63 - __builtin_clzll(any);
         if (lane == chosen) emit(at[lane], log(own / sum));
@@ -689,8 +721,8 @@ struct Sampler {
         static_assert(2 * kRanked <= kRowThreads && kRanked <= kHits, "");
         const int tid = threadIdx.x, j = tid >> 1;
         const bool there = j < n;
-        const float x = there ? sh.list_x[j] : 0.0f;
-        const int idx = there ? sh.list_i[j] : 0;
+        const int idx = there ? sh.list[j] : 0;
+        const float x = value(idx);
         const uint32_t key = key_of(x);
         const double w = want.weigh(x, top);
         uint2* all = reinterpret_cast<uint2*>(sh.hit);
@@ -729,92 +761,94 @@ struct Sampler {
         if (tid == holder(upto, own, want.u * sum, sh)) emit(at[tid], log(own / sum));
     }
 
-    // The candidates in LDS are the first of the order, and all that stay is among them.
-    __device__ __forceinline__ void from_list(int n, double total) const {
-        auto each = [&](auto f) {
-            for (int j = threadIdx.x; j < n; j += kRowThreads) f(sh.list_x[j], sh.list_i[j]);
-        };
-        const auto list = narrow(each, want, top, 50, sh);
-        Cut keep;
-        auto sum_of = [&](auto stays) {
-            uint64_t own = 0;
-            each([&](float x, int i) { own += stays(x, i) ? list.units(x) : 0; });
-            return (double)total_of(own, sh);
-        };
-        if (want.k) {
-            keep = list.cut(keep, want.k, 0.0, V);
-            total = want.p < 1.0 ? sum_of([&](float x, int i) { return keep.keeps(x, i); }) : 0.0;
-        } else {
-            total /= list.unit;
+    // The least logit of bucket q or a higher one (q: at most the largest logit's): 64 lanes
+    // narrow its key down.
+    __device__ __forceinline__ float least_of(int q) const {
+        uint32_t lo = kLeastKey, hi = key_of(top);
+        const uint32_t lane = threadIdx.x & 63;
+        while (lo < hi) {
+            const uint32_t step = (hi - lo) / 64 + 1, at = min(lo + lane * step, hi);
+            const uint64_t yes = __ballot(want.bucket(value_of(at)) >= q);
+            const uint32_t first = yes ? __builtin_ctzll(yes) : 64;
+            hi = min(hi, lo + first * step);
+            lo = first ? min(lo + (first - 1) * step + 1, hi) : lo;
         }
-        if (want.p < 1.0) keep = list.cut(keep, 0, want.p * total, V);
-        auto stays = [&](float x, int i) {
-            const double w = want.weigh(x, top);
-            return keep.keeps(x, i) && w >= want.m && w > kNoWeight;
-        };
-        const double sum = sum_of(stays), target = want.u * sum;
-        uint32_t idx = 0;
-        uint64_t a, b, ties;
-        // (a number of 0 takes the first one, however little it weighs)
-        list.find(idx, (uint32_t)V - 1, true,
-                  [&](float x, int i) { return stays(x, i) ? (uint32_t)i : ~0u; },
-                  [&](uint64_t, uint64_t m) { return target == 0.0 || (double)m > target; }, a, b, ties);
-        each([&](float x, int i) {
-            if ((uint32_t)i == idx) emit(i, log(want.weigh(x, top) / (sum * list.unit)));
-        });
+        return value_of(hi);
     }
 
-    // The logits of buckets first .. last into the list; how many there are.
-    __device__ __forceinline__ int gather(const float* groups, int n_groups, int most, int first, int last) const {
+    __device__ __forceinline__ float value(int i) const {
+        if constexpr (sizeof(T) == 4)
+            return r.src[i];
+        else
+            return bf16_to_f32(r.src[i]);
+    }
+
+    // The places of the logits in [least, most) into the list; how many there are.
+    __device__ __forceinline__ int gather(const float* groups, int n_groups, float least, float most) const {
         const int tid = threadIdx.x, lane = tid & (kGroup - 1);
+        __syncthreads();
         if (tid == 0) sh.listed = 0;
         for (int g0 = 0; g0 < n_groups; g0 += kHits) {
-            __syncthreads();
-            if (tid == 0) sh.hits = 0;
             float x[kHits / kRowThreads];
 #pragma unroll
             for (int j = 0; j < kHits / kRowThreads; ++j) {
                 const int g = g0 + j * kRowThreads + tid;
                 x[j] = g < n_groups ? groups[g] : -INFINITY;
             }
+            if (tid == 0) sh.hits = 0;
             __syncthreads();
 #pragma unroll
             for (int j = 0; j < kHits / kRowThreads; ++j)
-                if (x[j] > -INFINITY && min(most - want.bucket(x[j]), kRest) <= last)
-                    sh.hit[atomicAdd(&sh.hits, 1)] = g0 + j * kRowThreads + tid;
+                if (x[j] >= least) sh.hit[atomicAdd(&sh.hits, 1)] = g0 + j * kRowThreads + tid;
             __syncthreads();
             const int hits = sh.hits;
-            constexpr int AT = 8, HOP = kRowThreads / kGroup;
-            for (int h0 = tid / kGroup; h0 < hits; h0 += AT * HOP) {
+            // 32 logits a lane at once, a bit each; where the row's ends or no group are a
+            // piece is all -infinity until its logits are looked at one by one
+            constexpr int AT = 32 / VEC, HOP = kRowThreads / kGroup;
+            constexpr uint32_t NONE = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+            for (int h0 = tid / kGroup; __any(h0 < hits); h0 += AT * HOP) {
                 uint4 raw[AT];
-                int piece[AT];
+                uint32_t found = 0, part = 0;
 #pragma unroll
                 for (int j = 0; j < AT; ++j) {
-                    const int h = h0 + j * HOP;
-                    piece[j] = h < hits ? sh.hit[h] * kGroup + lane : -1;
-                    raw[j] = make_uint4(0, 0, 0, 0);
-                    if (piece[j] >= 0) raw[j] = r.fetch(piece[j], V);
-                }
-#pragma unroll
-                for (int j = 0; j < AT; ++j) {
-                    if (piece[j] < 0) continue;
-                    float v[VEC];
-                    r.unpack(raw[j], piece[j], V, v);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const int b = min(most - want.bucket(v[e]), kRest);
-                        if (v[e] > -INFINITY && b >= first && b <= last) {
-                            const int at = atomicAdd(&sh.listed, 1);
-                            if (at < kList) {
-                                sh.list_x[at] = v[e];
-                                sh.list_i[at] = (int)r.column(piece[j]) + e;
-                            }
-                        }
+                    raw[j] = make_uint4(NONE, NONE, NONE, NONE);
+                    if (h0 + j * HOP < hits) {
+                        const int col = (sh.hit[h0 + j * HOP] * kGroup + lane) * VEC - r.before;
+                        if (col >= 0 && col <= V - VEC)
+                            raw[j] = *reinterpret_cast<const uint4*>(r.src + col);
+                        else
+                            part |= 1u << j;
                     }
                 }
+#pragma unroll
+                for (int j = 0; j < AT; ++j) {
+                    float v[VEC];
+                    r.values(raw[j], v);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        found |= v[e] >= least && v[e] < most ? 1u << (j * VEC + e) : 0u;
+                }
+                while (part) {
+                    const int j = __builtin_ctz(part), col = (sh.hit[h0 + j * HOP] * kGroup + lane) * VEC - r.before;
+                    part &= part - 1;
+                    for (int e = 0; e < VEC; ++e)
+                        if (col + e >= 0 && col + e < V && value(col + e) >= least && value(col + e) < most)
+                            found |= 1u << (j * VEC + e);
+                }
+                const uint32_t own = __builtin_popcount(found), upto = sum_upto(own);
+                const uint32_t all = __builtin_amdgcn_readlane(upto, 63);
+                if (all == 0) continue;
+                uint32_t at = 0;
+                if ((tid & 63) == 0) at = atomicAdd((uint32_t*)&sh.listed, all);
+                at = __builtin_amdgcn_readfirstlane(at) + upto - own;
+                for (; found; found &= found - 1, ++at) {
+                    const int bit = __builtin_ctz(found);
+                    if (at < kList)
+                        sh.list[at] = (sh.hit[h0 + bit / VEC * HOP] * kGroup + lane) * VEC - r.before + bit % VEC;
+                }
             }
+            __syncthreads();
         }
-        __syncthreads();
         return sh.listed;
     }
 
@@ -899,62 +933,104 @@ struct Sampler {
         }
         __syncthreads();
         const double above = sh.found[0], n_above = sh.found[1], here = sh.found[2];
-        const int n_groups = blocks * (kPieces / kGroup);
-        if (n_above + here <= kList) {
-            const int listed = gather(groups, n_groups, most, 0, last);
-            if (listed > kList) return false;
-            if (listed <= kSome)
-                few(listed, total);
-            else if (listed <= kRanked)
-                ranked(listed, total);
-            else
-                from_list(listed, total);
+        // The logits up to the cut's bucket, where the list holds them; with top-p alone those of
+        // the bucket, where the blocks' buckets say what lies before it.
+        const bool few_before = n_above + here <= kList;
+        if (!few_before && (want.k || want.m > 0.0 || here > kList || last == kRest)) return false;
+        const float least = last == kRest ? value_of(kLeastKey) : least_of(most - last);
+        const float over = few_before || last == 0 ? INFINITY : least_of(most - last + 1);
+        const int listed = gather(groups, blocks * (kPieces / kGroup), least, over);
+        if (listed > kList) return false;
+        if (few_before && listed <= kSome) {
+            few(listed, total);
             return true;
         }
-        if (want.k || want.m > 0.0 || here > kList || last == kRest) return false;
-        // Top-p alone, with many before the cut: the bucket's logits say where it lies,
-        // the blocks' buckets which block holds the number.
-        const int listed = gather(groups, n_groups, most, last, last);
-        if (listed > kList) return false;
+        if (few_before && listed <= kRanked) {
+            ranked(listed, total);
+            return true;
+        }
+        constexpr int E = kList / kRowThreads;
+        float x[E];
+        int idx[E];
+        uint64_t w[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            idx[j] = tid + j * kRowThreads < listed ? sh.list[tid + j * kRowThreads] : 0;
+            x[j] = value(idx[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < E; ++j) w[j] = units_of(want.weigh(x[j], top), 4.0);
         auto each = [&](auto f) {
-            for (int j = tid; j < listed; j += kRowThreads) f(sh.list_x[j], sh.list_i[j]);
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                if (tid + j * kRowThreads < listed) f(x[j], idx[j], [&] { return w[j]; });
         };
         const auto list = narrow(each, want, top, 50, sh);
-        const Cut keep = list.cut(Cut(), 0, (want.p * total - above) / list.unit, V);
+        auto sum_of = [&](auto stays) {
+            uint64_t sum = 0;
+            each([&](float v, int i, auto units) { sum += stays(v, i, units()) ? units() : 0; });
+            return (double)total_of(sum, sh);
+        };
+        Cut keep;
+        double target = (want.p * total - (few_before ? 0.0 : above)) / list.unit;
+        if (want.k) {
+            keep = list.cut(keep, want.k, 0.0, V);
+            if (want.p < 1.0) target = want.p * sum_of([&](float v, int i, uint64_t) { return keep.keeps(v, i); });
+        }
+        if (want.p < 1.0) keep = list.cut(keep, 0, target, V);
+        if (few_before) {
+            auto stays = [&](float v, int i) {
+                const double y = want.weigh(v, top);
+                return keep.keeps(v, i) && y >= want.m && y > kNoWeight;
+            };
+            const double sum = sum_of([&](float v, int i, uint64_t) { return stays(v, i); });
+            const double number = want.u * sum;
+            uint32_t first = 0;
+            uint64_t n_first, m_first, ties;
+            // (a number of 0 takes the first one, however little it weighs)
+            list.find(first, (uint32_t)V - 1, true,
+                      [&](float v, int i) { return stays(v, i) ? (uint32_t)i : ~0u; },
+                      [&](uint64_t, uint64_t b) { return number == 0.0 || (double)b > number; }, n_first,
+                      m_first, ties);
+            each([&](float v, int i, auto) {
+                if ((uint32_t)i == first) emit(i, log(want.weigh(v, top) / (sum * list.unit)));
+            });
+            return true;
+        }
+        // which block holds the number: its buckets before the cut's, and what stays of that
         __syncthreads();
         sh.mass[tid] = 0;
         __syncthreads();
-        each([&](float x, int i) {
-            if (keep.keeps(x, i))
-                atomicAdd((unsigned long long*)&sh.mass[(i + r.before) / kBlock], (unsigned long long)list.units(x));
+        each([&](float v, int i, auto units) {
+            if (keep.keeps(v, i))
+                atomicAdd((unsigned long long*)&sh.mass[(i + r.before) / kBlock], (unsigned long long)units());
         });
         for (int g = wave; g < blocks; g += kRowWaves) {
             double s = 0.0;
 #pragma unroll
             for (int j = 0; j < kBuckets / 64; ++j) {
                 const int i = lane + 64 * j;
-                if (i + sh.offset[g] < last) s += buckets[g * kBuckets + i];
+                const double y = buckets[g * kBuckets + i];
+                if (i + sh.offset[g] < last) s += y;
             }
-            for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
+            s = last_lane(sum_upto(s));
             if (lane == 0) sh.blocks[g] = s * sh.factor[g];
         }
         __syncthreads();
         own = tid < blocks ? sh.blocks[tid] + (double)sh.mass[tid] * list.unit : 0.0;
         double stay;
-        const double at = scan(own, sh, &stay), target = want.u * stay;
+        const double at = scan(own, sh, &stay);
+        target = want.u * stay;
         const int block = holder(at, own, target, sh);
         if (tid == block) sh.found[0] = at;
         __syncthreads();
-        pick(block * kPieces, min((block + 1) * kPieces, pieces), target - sh.found[0], stay,
-             [&](float x, int i, double) {
-                 const int q = most - want.bucket(x);
-                 return q < last || (q == last && keep.keeps(x, i));
-             });
+        pick_near(block * kPieces, min((block + 1) * kPieces, pieces), target - sh.found[0], stay,
+                  [&](float v, int i) { return v >= over || (v >= least && keep.keeps(v, i)); });
         return true;
     }
 };
 
-template <class T>
+template <class T, bool FILTERS>
 __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(
     const T* __restrict__ logits, int64_t ld, const Request q, int V, const Found in,
     int32_t* __restrict__ tokens, float* __restrict__ logprobs, uint32_t* __restrict__ err) {
@@ -987,12 +1063,14 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(
     }
     const double* sums = in.sums + row * parts;
     if (want.greedy()) return s.greedy(tops, parts);
-    if (!want.filtered()) return s.all(tops, sums, parts);
-    const int64_t blocks = row * in.blocks;
-    double total;
-    if (!s.by_buckets(tops, sums, in.groups + blocks * (kBlock / Row<T>::VEC / kGroup),
-                      in.buckets + blocks * kBuckets, in.blocks, total))
-        s.by_passes(total);
+    if (!FILTERS || !want.filtered()) return s.all(tops, sums, parts);
+    if constexpr (FILTERS) {
+        const int64_t blocks = row * in.blocks;
+        double total;
+        if (!s.by_buckets(tops, sums, in.groups + blocks * (kBlock / Row<T>::VEC / kGroup),
+                          in.buckets + blocks * kBuckets, in.blocks, total))
+            s.by_passes(total);
+    }
 }
 
 int blocks_of(int V) { return (int)(((int64_t)V + 7 + kBlock - 1) / kBlock); }
@@ -1021,12 +1099,15 @@ hipError_t run_sample(const void* logits, int64_t ld, const Request& q, int64_t 
                       hipStream_t s) {
     Found f;
     layout(B, V, scratch, &f);
-    sample_part_kernel<T><<<dim3(f.blocks, (uint32_t)B), dim3(64 * kBlockWaves), 0, s>>>(
-        (const T*)logits, ld, q, V, f);
+    // (without any filter kernels that hold fewer registers)
+    const bool filters = q.top_k || q.top_p || q.min_p;
+    auto part = filters ? sample_part_kernel<T, true> : sample_part_kernel<T, false>;
+    part<<<dim3(f.blocks, (uint32_t)B), dim3(64 * kBlockWaves), 0, s>>>((const T*)logits, ld, q, V, f);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    sample_row_kernel<T><<<dim3((uint32_t)B), dim3(kRowThreads), 0, s>>>(
-        (const T*)logits, ld, q, V, f, tokens, logprobs, err);
+    auto whole = filters ? sample_row_kernel<T, true> : sample_row_kernel<T, false>;
+    whole<<<dim3((uint32_t)B), dim3(kRowThreads), 0, s>>>((const T*)logits, ld, q, V, f, tokens,
+                                                        logprobs, err);
     return hipGetLastError();
 }
 
