@@ -19,14 +19,18 @@ constexpr int kEach = 32;                     // logits a thread of a part
 constexpr int kPart = 64 * kEach;             // logits a wave: a part
 constexpr int kBlockWaves = 4;
 constexpr int kBlock = kBlockWaves * kPart;   // logits a workgroup
-constexpr int kBuckets = 512;                 // of 1/32 of exp's argument, from a block's largest logit down;
+constexpr int kBuckets = 512;                 // of 1/24 of exp's argument (of 1/8 where logits are only
+                                              // counted), from a block's largest logit down;
 constexpr int kRest = kBuckets - 1;           // the last one takes all below, too
+constexpr int kXcds = 8;                      // workgroups go to these in turn: a row's all to one, so
+                                              // that its logits are in the cache of the last one's
 constexpr int kCopies = 4;                    // of the buckets in LDS: lanes that meet in one wait for each other
 constexpr int kGroup = 16;                    // lanes whose largest logit is kept
 constexpr int kRowThreads = 512;
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kBinBits = 9, kBins = 1 << kBinBits;  // a thread each
-constexpr int kList = 4096;                   // candidates in LDS,
+constexpr int kList = 8192;                   // candidates in LDS,
+constexpr int kManyBefore = 1024;
 constexpr int kSome = 64, kRanked = 256;       // that are ranked by counting, by a wave or all
 constexpr int kHits = 4 * kRowThreads;        // groups of a row looked at together
 constexpr int kMostBlocks = 256;              // of a row whose buckets are joined
@@ -42,6 +46,7 @@ __device__ __forceinline__ double weight(double d, double c) {
     const double r = __builtin_fma(d, c, kRound);
     const double f = __builtin_fma(d, c, -(r - kRound));
     double p = 1.3344183691340562e-06;
+    asm("" : "+v"(p));  // (in registers: an instruction takes one constant)
     p = __builtin_fma(p, f, 1.531420923292218e-05);
     p = __builtin_fma(p, f, 0.00015403098285512635);
     p = __builtin_fma(p, f, 0.0013333434157515403);
@@ -89,16 +94,16 @@ struct Want {
               !(mm >= 0.0f && mm <= 1.0f) || !(uu >= 0.0f && uu < 1.0f);
         c = t > 0.0f ? kLog2e / (double)t : 0.0;
         least = -1000.0 / c;
-        s = 32.0f / t;
         p = pp;
         m = mm;
         u = uu;
         k = kk > 0 && kk < V ? kk : 0;
+        s = (k ? 8.0f : 24.0f) / t;
     }
     __device__ __forceinline__ bool greedy() const { return c == 0.0; }
     __device__ __forceinline__ bool filtered() const { return !greedy() && (k > 0 || p < 1.0 || m > 0.0); }
-    // whether the weights of the whole row are summed
-    __device__ __forceinline__ bool whole_sum() const { return !greedy() && k == 0 && (p < 1.0 || m == 0.0); }
+    // whether the weights of the whole row are summed, or only logits counted
+    __device__ __forceinline__ bool whole_sum() const { return !greedy() && k == 0; }
     __device__ __forceinline__ double weigh(float x, float top) const {
         return weight(fmax((double)x - (double)top, least), c);
     }
@@ -162,22 +167,31 @@ __device__ __forceinline__ float largest_of_16(float x) {
     x = fmaxf(x, __uint_as_float(moved<0x122>(__float_as_uint(x))));
     return fmaxf(x, __uint_as_float(moved<0x121>(__float_as_uint(x))));
 }
+// of the wave, in all lanes
+__device__ __forceinline__ float largest(float x) {
+    x = largest_of_16(x);
+    const int u = __float_as_int(x);
+    return fmaxf(fmaxf(__int_as_float(__builtin_amdgcn_readlane(u, 0)), __int_as_float(__builtin_amdgcn_readlane(u, 16))),
+                 fmaxf(__int_as_float(__builtin_amdgcn_readlane(u, 32)), __int_as_float(__builtin_amdgcn_readlane(u, 48))));
+}
 
 // One wave a part, four of them a block.  Rows without a filter need a part's largest
 // logit and its sum of weights; rows with one also how much weight, or where that is
 // not asked for how many logits, lie in each bucket.
 template <class T, bool FILTERS>
 __global__ void __launch_bounds__(64 * kBlockWaves) sample_part_kernel(
-    const T* __restrict__ logits, int64_t ld, const Request q, int V, const Found out) {
+    const T* __restrict__ logits, int64_t ld, const Request q, int64_t rows, int V, const Found out) {
     constexpr int VEC = Row<T>::VEC, NL = kEach / VEC, NT = 64 * kBlockWaves;
     __shared__ unsigned long long bucket[FILTERS ? kBuckets * kCopies : 1];
     uint32_t* const number = reinterpret_cast<uint32_t*>(bucket);
     __shared__ float wave_top[kBlockWaves];
-    const int64_t row = blockIdx.y;
+    const uint32_t along = blockIdx.x / kXcds, at = along % out.blocks;
+    const int64_t row = (int64_t)(along / out.blocks) * kXcds + blockIdx.x % kXcds;
+    if (row >= rows) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t block = row * out.blocks + blockIdx.x;
-    const int part = blockIdx.x * kBlockWaves + wave;
+    const int64_t block = row * out.blocks + at;
+    const int part = at * kBlockWaves + wave;
     const Row<T> r(logits + row * ld);
     const int64_t from = (int64_t)part * NL * 64;
     const bool inside = r.column(from) >= 0 && r.column(from + NL * 64) <= V;
@@ -211,7 +225,7 @@ __global__ void __launch_bounds__(64 * kBlockWaves) sample_part_kernel(
         }
         top = fmaxf(top, own[i]);
     }
-    for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    top = largest(top);
     bad = __any(bad);
     if (lane == 0)
         out.tops[row * out.blocks * kBlockWaves + part] = bad ? __uint_as_float(0x7FC00000u) : top;
@@ -293,6 +307,7 @@ struct Shared {
     uint32_t count[kBins];
     uint64_t mass[kBins];
     int first, last, hits, listed, at[kRowWaves];
+    uint32_t range[2];
     bool none;
     uint64_t above[3];
     double found[3];
@@ -393,7 +408,8 @@ struct Cut {
 // Logits and their weights in whole numbers of 2^-scale, so that they add up to the same
 // in any order.  Each: each(f) calls f(logit, index, units) for its logits above -infinity,
 // spread over the workgroup's threads; units() are the weight.
-template <class Each>
+// RUNS: neighbours are often equal.
+template <bool RUNS, class Each>
 struct Narrow {
     const Each& each;
     const Want& want;
@@ -420,9 +436,25 @@ struct Narrow {
             each([&](float x, int i, auto units) {
                 const uint32_t at = place(x, i);
                 if (at < lo || at > hi) return;
-                atomicAdd(&sh.count[(at - lo) >> shift], 1u);
-                if (weights)
-                    atomicAdd((unsigned long long*)&sh.mass[(at - lo) >> shift], (unsigned long long)units());
+                const uint32_t bin = (at - lo) >> shift;
+                const uint64_t w = weights ? units() : 0;
+                if constexpr (RUNS) {  // equal logits, or near indices: the wave's together
+                    const uint64_t here = __ballot(1);
+                    const uint32_t one = __builtin_amdgcn_readfirstlane(bin);
+                    const uint64_t w_one = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(w >> 32)) << 32 |
+                                           (uint32_t)__builtin_amdgcn_readfirstlane((int)w);
+                    if (__ballot(bin == one && w == w_one) == here) {
+                        if ((uint32_t)__builtin_ctzll(here) == (tid & 63)) {
+                            const uint32_t number = __builtin_popcountll(here);
+                            atomicAdd(&sh.count[one], number);
+                            if (weights)
+                                atomicAdd((unsigned long long*)&sh.mass[one], (unsigned long long)(w_one * number));
+                        }
+                        return;
+                    }
+                }
+                atomicAdd(&sh.count[bin], 1u);
+                if (weights) atomicAdd((unsigned long long*)&sh.mass[bin], (unsigned long long)w);
             });
             __syncthreads();
             const uint64_t own_n = sh.count[tid], own_m = sh.mass[tid];
@@ -449,11 +481,11 @@ struct Narrow {
         }
     }
     // The cut that keeps the first k of those that `in` keeps (k > 0), or those before
-    // which less than target (in units) lies.
-    __device__ __forceinline__ Cut cut(const Cut in, int k, double target, int V) const {
-        uint32_t at = ~key_of(top), idx = 0;
+    // which less than target (in units) lies; all of them lie in [least, most].
+    __device__ __forceinline__ Cut cut(const Cut in, int k, double target, float most, float least, int V) const {
+        uint32_t at = ~key_of(most), idx = 0;
         uint64_t n, m, ties;
-        if (!find(at, ~max(in.key, kLeastKey), k == 0,
+        if (!find(at, ~max(in.key, key_of(least)), k == 0,
                   [&](float x, int i) { return in.keeps(x, i) ? ~key_of(x) : ~0u; },
                   [&](uint64_t a, uint64_t b) { return k ? a >= (uint64_t)k : (double)b >= target; },
                   n, m, ties))
@@ -474,10 +506,10 @@ struct Narrow {
         return out;
     }
 };
-template <class Each>
-__device__ __forceinline__ Narrow<Each> narrow(const Each& each, const Want& want, float top, int scale,
+template <bool RUNS, class Each>
+__device__ __forceinline__ Narrow<RUNS, Each> narrow(const Each& each, const Want& want, float top, int scale,
                                                Shared& sh) {
-    return Narrow<Each>{each, want, top, ldexp(1.0, -scale), sh};
+    return Narrow<RUNS, Each>{each, want, top, ldexp(1.0, -scale), sh};
 }
 // a weight in whole numbers of 2^-scale, magic = 2^(52 - scale)
 __device__ __forceinline__ uint64_t units_of(double w, double magic) {
@@ -495,6 +527,7 @@ struct Sampler {
     Shared& sh;
     int32_t* token;
     float* logprob;  // or null
+    float floor;     // the least logit that min-p lets stay
 
     __device__ __forceinline__ void emit(int i, double lp) const {
         *token = i;
@@ -541,7 +574,7 @@ struct Sampler {
         double own = 0.0, total;
         in_order([&](float x, int i) {
             const double w = want.weigh(x, top);
-            if (w > kNoWeight && stays(x, i, w)) own += w;
+            if (w > kNoWeight && stays(x, i)) own += w;
         });
         const double before = scan(own, sh, &total), target = want.u * total;
         if ((int)threadIdx.x != holder(before, own, target, sh)) return;
@@ -550,7 +583,7 @@ struct Sampler {
         bool done = false;
         in_order([&](float x, int i) {
             const double w = want.weigh(x, top);
-            if (done || !(w > kNoWeight) || !stays(x, i, w)) return;
+            if (done || !(w > kNoWeight) || !stays(x, i)) return;
             sum += w;
             at = i;
             w_token = w;
@@ -650,27 +683,51 @@ struct Sampler {
                   [](float, int) { return true; });
     }
 
-    // Any filters on any row, by passes over it.
-    __device__ __forceinline__ void by_passes(double total) const {
+    // Any filters on any row, by passes over it.  The first cut lies in [least, over), with
+    // `above` (logits for top-k, else weight) before these.
+    __device__ __forceinline__ void by_passes(double total, float least, float over, double above) const {
         const int scale = min(50, 30 + __builtin_clz(V));
         const double magic = ldexp(1.0, 52 - scale);
+        uint32_t lo = ~0u, hi = 0;
+        every([&](float x, int) {
+            if (x < least || x >= over) return;
+            lo = min(lo, key_of(x));
+            hi = max(hi, key_of(x));
+        });
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            sh.range[0] = ~0u;
+            sh.range[1] = 0;
+        }
+        __syncthreads();
+        atomicMin(&sh.range[0], lo);
+        atomicMax(&sh.range[1], hi);
+        __syncthreads();
+        least = value_of(sh.range[0]);
+        float most = value_of(sh.range[1]);
         auto each = [&](auto f) {
-            every([&](float x, int i) { f(x, i, [&] { return units_of(want.weigh(x, top), magic); }); });
+            every([&](float x, int i) {
+                if (x >= least && x <= most) f(x, i, [&] { return units_of(want.weigh(x, top), magic); });
+            });
         };
-        const auto row = narrow(each, want, top, scale, sh);
+        const auto row = narrow<true>(each, want, top, scale, sh);
         Cut keep;
-        if (want.k) keep = row.cut(keep, want.k, 0.0, V);
-        if (want.p < 1.0) {
-            if (want.k) {
+        for (int again = 0; again < 2; ++again) {  // top-k, then top-p
+            if (again ? want.p == 1.0 : want.k == 0) continue;
+            if (again && want.k) {
                 double own = 0.0;
                 in_order([&](float x, int i) {
                     if (keep.keeps(x, i)) own += want.weigh(x, top);
                 });
                 scan(own, sh, &total);
+                above = 0.0;
+                least = value_of(keep.key);
+                most = top;
             }
-            keep = row.cut(keep, 0, want.p * total / row.unit, V);
+            keep = row.cut(keep, again ? 0 : want.k - (int)above, again ? (want.p * total - above) / row.unit : 0.0,
+                           most, least, V);
         }
-        pick([&](float x, int i, double w) { return keep.keeps(x, i) && w >= want.m; });
+        pick([&](float x, int i) { return keep.keeps(x, i) && x >= floor; });
     }
 
     // Up to 64 candidates, the first of the order, in LDS: one wave, a candidate a lane.
@@ -678,16 +735,19 @@ struct Sampler {
     __device__ __forceinline__ void few(int n, double total) const {
         const int lane = threadIdx.x;
         if (lane >= 64) return;
-        const int idx = lane < n ? sh.list[lane] : 0x7FFFFFFF;
-        const float x = lane < n ? value(idx) : -INFINITY;
-        const uint32_t key = key_of(x);
-        const double w = lane < n ? want.weigh(x, top) : 0.0;
+        const int idx = lane < n ? sh.list[lane] : 0;
+        const uint32_t key = lane < n ? key_of(value(idx)) : 0;
+        const double w = lane < n ? want.weigh(value_of(key), top) : 0.0;
+        uint2* all = reinterpret_cast<uint2*>(sh.hit);
+        all[lane] = make_uint2(key, (uint32_t)idx);
+        wave_fence();
         int rank = 0, place = 0;  // in the order, by the index
+#pragma unroll 8
         for (int l = 0; l < n; ++l) {
-            const uint32_t k = __builtin_amdgcn_readlane(key, l);
-            const int i = __builtin_amdgcn_readlane(idx, l);
-            rank += (k > key || (k == key && i < idx)) ? 1 : 0;
-            place += i < idx ? 1 : 0;
+            const uint2 o = all[l];
+            const bool less = (int)o.y < idx;
+            rank += (o.x > key || (o.x == key && less)) ? 1 : 0;
+            place += less ? 1 : 0;
         }
         double* by = reinterpret_cast<double*>(sh.mass);
         int* at = reinterpret_cast<int*>(sh.count);
@@ -700,8 +760,10 @@ struct Sampler {
         if (want.k > 0) total = last_lane(upto);
         const double before = moved<0x138>(upto);  // (the lane before's)
         const bool stays = lane < most && (lane == 0 || ((want.p == 1.0 || before < want.p * total) &&
-                                                         sorted >= want.m && sorted > kNoWeight));
-        const int kept = __builtin_popcountll(__ballot(stays));  // the first ones
+                                                         sorted > kNoWeight));
+        // (the first ones, by each filter)
+        const int kept = min(__builtin_popcountll(__ballot(stays)),
+                             __builtin_popcountll(__ballot(lane < n && value_of(key) >= floor)));
         if (lane < n) {
             by[place] = rank < kept ? w : 0.0;
             at[place] = idx;
@@ -748,9 +810,10 @@ struct Sampler {
         double sum;
         const double before = scan(sorted, sh, &sum);
         if (want.k > 0) total = sum;
-        const int kept = __syncthreads_count(
-            tid < most && (tid == 0 || ((want.p == 1.0 || before < want.p * total) && sorted >= want.m &&
-                                        sorted > kNoWeight)));
+        const int kept = min(
+            __syncthreads_count(tid < most && (tid == 0 || ((want.p == 1.0 || before < want.p * total) &&
+                                                            sorted > kNoWeight))),
+            __syncthreads_count(writes && x >= floor));
         if (writes) {
             by[place] = rank < kept ? w : 0.0;
             at[place] = idx;
@@ -761,19 +824,23 @@ struct Sampler {
         if (tid == holder(upto, own, want.u * sum, sh)) emit(at[tid], log(own / sum));
     }
 
-    // The least logit of bucket q or a higher one (q: at most the largest logit's): 64 lanes
-    // narrow its key down.
-    __device__ __forceinline__ float least_of(int q) const {
+    // The least logit for which `is` holds (it does for the largest, and for those above one
+    // that it holds for): 64 lanes narrow its key down.
+    template <class Is>
+    __device__ __forceinline__ float least_such(Is is) const {
         uint32_t lo = kLeastKey, hi = key_of(top);
         const uint32_t lane = threadIdx.x & 63;
         while (lo < hi) {
             const uint32_t step = (hi - lo) / 64 + 1, at = min(lo + lane * step, hi);
-            const uint64_t yes = __ballot(want.bucket(value_of(at)) >= q);
+            const uint64_t yes = __ballot(is(value_of(at)));
             const uint32_t first = yes ? __builtin_ctzll(yes) : 64;
             hi = min(hi, lo + first * step);
             lo = first ? min(lo + (first - 1) * step + 1, hi) : lo;
         }
         return value_of(hi);
+    }
+    __device__ __forceinline__ float least_of(int q) const {
+        return least_such([&](float x) { return want.bucket(x) >= q; });
     }
 
     __device__ __forceinline__ float value(int i) const {
@@ -783,17 +850,87 @@ struct Sampler {
             return bf16_to_f32(r.src[i]);
     }
 
+    static constexpr int AT = 32 / VEC;  // pieces of 32 logits
+
+    // The wave's logits that are found, a bit each of a lane's 32, into the list;
+    // place_of(bit): where it is in the row.
+    template <class PlaceOf>
+    __device__ __forceinline__ void list(uint32_t found, PlaceOf place_of) const {
+        const uint32_t own = __builtin_popcount(found), upto = sum_upto(own);
+        const uint32_t all = __builtin_amdgcn_readlane(upto, 63);
+        if (all == 0) return;
+        uint32_t at = 0;
+        if ((threadIdx.x & 63) == 0) at = atomicAdd((uint32_t*)&sh.listed, all);
+        at = __builtin_amdgcn_readfirstlane(at) + upto - own;
+        for (; found; found &= found - 1, ++at)
+            if (at < kList) sh.list[at] = place_of(__builtin_ctz(found));
+    }
+    __device__ __forceinline__ uint32_t found_in(const uint4 (&raw)[AT], float least, float most) const {
+        uint32_t found = 0;
+#pragma unroll
+        for (int j = 0; j < AT; ++j) {
+            float v[VEC];
+            r.values(raw[j], v);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) found |= v[e] >= least && v[e] < most ? 1u << (j * VEC + e) : 0u;
+        }
+        return found;
+    }
+
     // The places of the logits in [least, most) into the list; how many there are.
-    __device__ __forceinline__ int gather(const float* groups, int n_groups, float least, float most) const {
+    // (tops: the first kHits groups')
+    __device__ __forceinline__ int gather(const float* groups, int n_groups,
+                                          const float (&tops)[kHits / kRowThreads], float least,
+                                          float most) const {
         const int tid = threadIdx.x, lane = tid & (kGroup - 1);
+        int many = 0;
+#pragma unroll
+        for (int j = 0; j < kHits / kRowThreads; ++j) many += tops[j] >= least ? 1 : 0;
         __syncthreads();
         if (tid == 0) sh.listed = 0;
+        many = __syncthreads_count(2 * many > kHits / kRowThreads);
+        if (2 * many > min(kRowThreads, n_groups)) {
+            // most groups have one: the row's pieces in turn, the next ones on their way;
+            // its ends, which are no whole pieces, first
+            const int begin = r.before ? 1 : 0, end = max((r.before + V) / VEC, begin);
+            if (tid < 2 * VEC) {
+                const int i = tid < VEC ? tid : end * VEC - r.before + tid - VEC;
+                if (i < (tid < VEC ? min(begin * VEC - r.before, V) : V) && value(i) >= least && value(i) < most) {
+                    const int at = atomicAdd(&sh.listed, 1);
+                    if (at < kList) sh.list[at] = i;
+                }
+            }
+            uint4 raw[AT], next[AT];
+            auto fetch = [&](int i0) {
+#pragma unroll
+                for (int j = 0; j < AT; ++j) {
+                    const int i = min(i0 + j * kRowThreads, end - 1);
+                    next[j] = *reinterpret_cast<const uint4*>(r.src + (i * VEC - r.before));
+                }
+            };
+            if (end > begin) {
+                fetch(begin + tid);
+                for (int i0 = begin + tid; __any(i0 < end); i0 += AT * kRowThreads) {
+#pragma unroll
+                    for (int j = 0; j < AT; ++j) raw[j] = next[j];
+                    fetch(i0 + AT * kRowThreads);
+                    uint32_t found = found_in(raw, least, most);
+                    const int there = i0 < end ? (end - i0 + kRowThreads - 1) / kRowThreads : 0;
+                    if (there < AT) found &= (1u << there * VEC) - 1;
+                    list(found, [&](int bit) {
+                        return (i0 + bit / VEC * kRowThreads) * VEC - r.before + bit % VEC;
+                    });
+                }
+            }
+            __syncthreads();
+            return sh.listed;
+        }
         for (int g0 = 0; g0 < n_groups; g0 += kHits) {
             float x[kHits / kRowThreads];
 #pragma unroll
             for (int j = 0; j < kHits / kRowThreads; ++j) {
                 const int g = g0 + j * kRowThreads + tid;
-                x[j] = g < n_groups ? groups[g] : -INFINITY;
+                x[j] = g0 == 0 ? tops[j] : g < n_groups ? groups[g] : -INFINITY;
             }
             if (tid == 0) sh.hits = 0;
             __syncthreads();
@@ -802,13 +939,13 @@ struct Sampler {
                 if (x[j] >= least) sh.hit[atomicAdd(&sh.hits, 1)] = g0 + j * kRowThreads + tid;
             __syncthreads();
             const int hits = sh.hits;
-            // 32 logits a lane at once, a bit each; where the row's ends or no group are a
-            // piece is all -infinity until its logits are looked at one by one
-            constexpr int AT = 32 / VEC, HOP = kRowThreads / kGroup;
+            // where the row's ends or no group are a piece is all -infinity until its
+            // logits are looked at one by one
+            constexpr int HOP = kRowThreads / kGroup;
             constexpr uint32_t NONE = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
             for (int h0 = tid / kGroup; __any(h0 < hits); h0 += AT * HOP) {
                 uint4 raw[AT];
-                uint32_t found = 0, part = 0;
+                uint32_t part = 0;
 #pragma unroll
                 for (int j = 0; j < AT; ++j) {
                     raw[j] = make_uint4(NONE, NONE, NONE, NONE);
@@ -820,14 +957,7 @@ struct Sampler {
                             part |= 1u << j;
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < AT; ++j) {
-                    float v[VEC];
-                    r.values(raw[j], v);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        found |= v[e] >= least && v[e] < most ? 1u << (j * VEC + e) : 0u;
-                }
+                uint32_t found = found_in(raw, least, most);
                 while (part) {
                     const int j = __builtin_ctz(part), col = (sh.hit[h0 + j * HOP] * kGroup + lane) * VEC - r.before;
                     part &= part - 1;
@@ -835,17 +965,9 @@ struct Sampler {
                         if (col + e >= 0 && col + e < V && value(col + e) >= least && value(col + e) < most)
                             found |= 1u << (j * VEC + e);
                 }
-                const uint32_t own = __builtin_popcount(found), upto = sum_upto(own);
-                const uint32_t all = __builtin_amdgcn_readlane(upto, 63);
-                if (all == 0) continue;
-                uint32_t at = 0;
-                if ((tid & 63) == 0) at = atomicAdd((uint32_t*)&sh.listed, all);
-                at = __builtin_amdgcn_readfirstlane(at) + upto - own;
-                for (; found; found &= found - 1, ++at) {
-                    const int bit = __builtin_ctz(found);
-                    if (at < kList)
-                        sh.list[at] = (sh.hit[h0 + bit / VEC * HOP] * kGroup + lane) * VEC - r.before + bit % VEC;
-                }
+                list(found, [&](int bit) {
+                    return (sh.hit[h0 + bit / VEC * HOP] * kGroup + lane) * VEC - r.before + bit % VEC;
+                });
             }
             __syncthreads();
         }
@@ -856,11 +978,14 @@ struct Sampler {
     // where they do not, or it holds too many logits; total: the sum of the row's
     // weights, where top-p asks for it, or the number of its logits.
     __device__ __forceinline__ bool by_buckets(const float* tops, const double* sums, const float* groups,
-                                               const double* buckets, int blocks, double& total) const {
+                                               const double* buckets, int blocks, double& total,
+                                               float& least, float& over, double& above) const {
         const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
         const bool weights = want.whole_sum();
         double own = 0.0;
-        total = 0.0;
+        total = above = 0.0;
+        least = value_of(kLeastKey);
+        over = INFINITY;
         if (blocks > kMostBlocks) {
             if (weights) {
                 double own = 0.0;
@@ -875,6 +1000,14 @@ struct Sampler {
                 scan(own, sh, &total);
             }
             return false;
+        }
+        // (on their way ahead)
+        const int n_groups = blocks * (kPieces / kGroup);
+        float group_tops[kHits / kRowThreads];
+#pragma unroll
+        for (int j = 0; j < kHits / kRowThreads; ++j) {
+            const int g = j * kRowThreads + tid;
+            group_tops[j] = g < n_groups ? groups[g] : -INFINITY;
         }
         const int most = want.bucket(top);
         if (tid < blocks) {
@@ -910,20 +1043,20 @@ struct Sampler {
         if (tid == kRest) in = 0.0;
         const double before = scan(in, sh, &all);
         if (tid == kRest) in = weights ? 0.0 : total - all;
-        // the bucket that holds the cut
+        // the bucket that holds the cut: top-k's or top-p's, or min-p's where that is higher
         int last = kRest;
         if (want.k || want.p < 1.0)
             last = min(last, lowest(in > 0.0 && before + in >= (want.k ? (double)want.k : want.p * total), sh));
+        bool cut_here = last < kRest;
         if (want.m > 0.0 && !(want.k && want.p < 1.0)) {  // (the sum of top-k's has to be whole)
-            // below this no weight reaches m (a bucket more for the roundings)
-            const float edge = (float)((double)top + log2(want.m) / want.c);
-            const int bound = most - want.bucket(edge - fabsf(edge) * 0x1p-20f) + 1;
-            last = min(last, max(bound, 0));
+            const int bound = most - want.bucket(floor);
+            cut_here &= last <= bound;
+            last = min(last, bound);
         }
         // how many logits there are up to it, and in it: where weights were summed at most
         // as many as if each had its bucket's least
         double n = in;
-        if (weights) n = tid == kRest ? 2.0 * kList : in * exp2f((float)(tid + 1) * (1.4427f / 32.0f)) + 1.0;
+        if (weights) n = tid == kRest ? 2.0 * kList : in * exp2f((float)(tid + 1) * (1.4427f / 24.0f)) + 1.0;
         const double n_before = weights ? scan(n, sh, &all) : before;
         __syncthreads();
         if (tid == last) {
@@ -932,14 +1065,25 @@ struct Sampler {
             sh.found[2] = n;
         }
         __syncthreads();
-        const double above = sh.found[0], n_above = sh.found[1], here = sh.found[2];
-        // The logits up to the cut's bucket, where the list holds them; with top-p alone those of
-        // the bucket, where the blocks' buckets say what lies before it.
-        const bool few_before = n_above + here <= kList;
-        if (!few_before && (want.k || want.m > 0.0 || here > kList || last == kRest)) return false;
-        const float least = last == kRest ? value_of(kLeastKey) : least_of(most - last);
-        const float over = few_before || last == 0 ? INFINITY : least_of(most - last + 1);
-        const int listed = gather(groups, blocks * (kPieces / kGroup), least, over);
+        const double n_above = sh.found[1], here = sh.found[2];
+        // The logits up to the cut's bucket, where the list holds them; without top-k those of
+        // the bucket, as the blocks' buckets say what lies before it.
+        // (a long list takes longer than one bucket's and a block)
+        const bool few_before = n_above + here <= (weights && last < kRest && here <= kList ? kManyBefore : kList);
+        if (last < kRest) least = least_of(most - last);
+        if (!few_before) {
+            if (last == kRest) return false;
+            if (last > 0) over = least_of(most - last + 1);
+            above = sh.found[0];
+            if (want.k || here > kList) {
+                if (cut_here) return false;
+                least = value_of(kLeastKey);
+                over = INFINITY;
+                above = 0.0;
+                return false;
+            }
+        }
+        const int listed = gather(groups, n_groups, group_tops, least, over);
         if (listed > kList) return false;
         if (few_before && listed <= kSome) {
             few(listed, total);
@@ -965,23 +1109,22 @@ struct Sampler {
             for (int j = 0; j < E; ++j)
                 if (tid + j * kRowThreads < listed) f(x[j], idx[j], [&] { return w[j]; });
         };
-        const auto list = narrow(each, want, top, 50, sh);
+        const auto list = narrow<false>(each, want, top, 50, sh);
         auto sum_of = [&](auto stays) {
             uint64_t sum = 0;
             each([&](float v, int i, auto units) { sum += stays(v, i, units()) ? units() : 0; });
             return (double)total_of(sum, sh);
         };
         Cut keep;
-        double target = (want.p * total - (few_before ? 0.0 : above)) / list.unit;
+        double target = (want.p * total - above) / list.unit;
         if (want.k) {
-            keep = list.cut(keep, want.k, 0.0, V);
+            keep = list.cut(keep, want.k, 0.0, top, least, V);
             if (want.p < 1.0) target = want.p * sum_of([&](float v, int i, uint64_t) { return keep.keeps(v, i); });
         }
-        if (want.p < 1.0) keep = list.cut(keep, 0, target, V);
+        if (want.p < 1.0 && (few_before || cut_here)) keep = list.cut(keep, 0, target, fminf(over, top), least, V);
         if (few_before) {
             auto stays = [&](float v, int i) {
-                const double y = want.weigh(v, top);
-                return keep.keeps(v, i) && y >= want.m && y > kNoWeight;
+                return keep.keeps(v, i) && v >= floor && want.weigh(v, top) > kNoWeight;
             };
             const double sum = sum_of([&](float v, int i, uint64_t) { return stays(v, i); });
             const double number = want.u * sum;
@@ -1002,7 +1145,7 @@ struct Sampler {
         sh.mass[tid] = 0;
         __syncthreads();
         each([&](float v, int i, auto units) {
-            if (keep.keeps(v, i))
+            if (v >= floor && keep.keeps(v, i))
                 atomicAdd((unsigned long long*)&sh.mass[(i + r.before) / kBlock], (unsigned long long)units());
         });
         for (int g = wave; g < blocks; g += kRowWaves) {
@@ -1025,7 +1168,7 @@ struct Sampler {
         if (tid == block) sh.found[0] = at;
         __syncthreads();
         pick_near(block * kPieces, min((block + 1) * kPieces, pieces), target - sh.found[0], stay,
-                  [&](float v, int i) { return v >= over || (v >= least && keep.keeps(v, i)); });
+                  [&](float v, int i) { return v >= over || (v >= least && v >= floor && keep.keeps(v, i)); });
         return true;
     }
 };
@@ -1046,13 +1189,13 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(
         top = fmaxf(top, t);
     }
     const Want want(q, row, V);
-    for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    top = largest(top);
     if ((tid & 63) == 0) sh.sum[tid >> 6] = top;
     nan = __syncthreads_or(nan);
     for (int w = 0; w < kRowWaves; ++w) top = fmaxf(top, (float)sh.sum[w]);
     const Row<T> r(logits + row * ld);
-    const Sampler<T> s{r, V, (r.before + V + Row<T>::VEC - 1) / Row<T>::VEC, want, top, sh,
-                       tokens + row, logprobs ? logprobs + row : nullptr};
+    Sampler<T> s{r, V, (r.before + V + Row<T>::VEC - 1) / Row<T>::VEC, want, top, sh,
+                       tokens + row, logprobs ? logprobs + row : nullptr, value_of(kLeastKey)};
     if (want.bad || nan || top == -INFINITY) {
         if (tid == 0) {
             s.emit(-1, -INFINITY);
@@ -1065,11 +1208,13 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(
     if (want.greedy()) return s.greedy(tops, parts);
     if (!FILTERS || !want.filtered()) return s.all(tops, sums, parts);
     if constexpr (FILTERS) {
+        if (want.m > 0.0) s.floor = s.least_such([&](float x) { return want.weigh(x, top) >= want.m; });
         const int64_t blocks = row * in.blocks;
-        double total;
+        double total, above;
+        float least, over;  // where the cut lies
         if (!s.by_buckets(tops, sums, in.groups + blocks * (kBlock / Row<T>::VEC / kGroup),
-                          in.buckets + blocks * kBuckets, in.blocks, total))
-            s.by_passes(total);
+                          in.buckets + blocks * kBuckets, in.blocks, total, least, over, above))
+            s.by_passes(total, least, over, above);
     }
 }
 
@@ -1102,7 +1247,8 @@ hipError_t run_sample(const void* logits, int64_t ld, const Request& q, int64_t 
     // (without any filter kernels that hold fewer registers)
     const bool filters = q.top_k || q.top_p || q.min_p;
     auto part = filters ? sample_part_kernel<T, true> : sample_part_kernel<T, false>;
-    part<<<dim3(f.blocks, (uint32_t)B), dim3(64 * kBlockWaves), 0, s>>>((const T*)logits, ld, q, V, f);
+    part<<<dim3((uint32_t)((B + kXcds - 1) / kXcds * kXcds * f.blocks)), dim3(64 * kBlockWaves), 0, s>>>(
+        (const T*)logits, ld, q, B, V, f);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     auto whole = filters ? sample_row_kernel<T, true> : sample_row_kernel<T, false>;
