@@ -130,7 +130,8 @@ constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kEach = kChunk / kSortThreads;
 constexpr int kMaxDigit = 11;
 constexpr int kMaxBins = 1 << kMaxDigit;
-constexpr int kFewChunks = 64;      // up to here each workgroup sums the counts before its own
+constexpr int kFewChunks = 62;      // up to here each workgroup sums the counts before its own (a thread
+                                    // at most 31 of them, in 16 bits)
 
 struct __attribute__((aligned(8))) Pair {
     uint32_t key, pos;
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(
     if (!totals) {
         __syncthreads();
         const int groups = bins / 8, hop = kSortThreads / groups, g = tid % groups;
-        uint32_t earlier[8] = {0, 0, 0, 0, 0, 0, 0, 0}, all[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        u32x4 earlier = {0, 0, 0, 0}, all = {0, 0, 0, 0};  // two digits a word
         for (int c0 = tid / groups; c0 < chunks; c0 += 16 * hop) {
             u32x4 x[16];
 #pragma unroll
@@ -384,18 +385,17 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(
                 if (c < chunks) x[j] = reinterpret_cast<const u32x4*>(counts)[c * groups + g];
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t y = x[j][e / 2] >> (e & 1 ? 16 : 0) & 0xFFFFu;
-                    all[e] += y;
-                    earlier[e] += c0 + j * hop < chunk ? y : 0;
-                }
+            for (int j = 0; j < 16; ++j) {
+                all += x[j];
+                if (c0 + j * hop < chunk) earlier += x[j];
+            }
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            atomicAdd(&place[g * 8 + e], all[e]);
-            atomicAdd(&count[g * 8 + e], earlier[e]);
+            const uint32_t x = all[e / 2] >> (e & 1 ? 16 : 0) & 0xFFFFu;
+            const uint32_t y = earlier[e / 2] >> (e & 1 ? 16 : 0) & 0xFFFFu;
+            if (x) atomicAdd(&place[g * 8 + e], x);
+            if (y) atomicAdd(&count[g * 8 + e], y);
         }
         __syncthreads();
     }
@@ -444,7 +444,7 @@ struct SumArgs {
     const D* dout;
     W* dtable;
     float* part;         // [tiles][2][dim]
-    uint32_t* owners;    // the number of listed tiles, then the tiles
+    uint32_t* owners;    // the number of listed tiles, (nothing,) then each and its last key
     uint32_t rows;
     uint32_t tiles;
     int dim, streams, tile;
@@ -548,7 +548,11 @@ __device__ __forceinline__ void sum_tile(const SumArgs<D, W>& a) {
     const uint32_t at_end = a.pair[start + a.tile - 1].key;
     if (at_end == a.rows || a.pair[start + a.tile].key != at_end) return;
     put_part(a.part + ((int64_t)t * 2 + (begun ? 1 : 0)) * a.dim + c, sum);
-    if (begun && c == 0) a.owners[1 + atomicAdd(a.owners, 1u)] = t;
+    if (begun && c == 0) {
+        const uint32_t at = atomicAdd(a.owners, 1u);
+        a.owners[2 + 2 * at] = t;
+        a.owners[3 + 2 * at] = at_end;
+    }
 }
 
 // the first place in pair[lo, hi) whose key is at least k
@@ -573,9 +577,8 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const SumArgs<D, W> a) {
     const int lane = threadIdx.x & 63, quarter = lane >> 4;
     const uint32_t wave = blockIdx.x * 4 + (threadIdx.x >> 6);
     for (uint32_t w = wave; w < total; w += gridDim.x * 4) {
-        const uint32_t at = w / blocks, t = a.owners[1 + at];
+        const uint32_t at = w / blocks, t = a.owners[2 + 2 * at], key = a.owners[3 + 2 * at];
         const int c = (int)(w - at * blocks) * 64 + (lane & 15) * 4;
-        const uint32_t key = a.pair[(int64_t)(t + 1) * a.tile - 1].key;
         // the last tile that begins with the row: 64 at a time
         uint32_t lo = t + 1, hi = a.tiles;  // lo does; hi does not, or is none
         while (lo + 1 < hi) {
@@ -590,7 +593,7 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const SumArgs<D, W> a) {
         f32x4 sum = {0, 0, 0, 0};
         if (c < a.dim) {
             if (quarter == 0) sum = *reinterpret_cast<const f32x4*>(a.part + ((int64_t)t * 2 + 1) * a.dim + c);
-#pragma unroll 8
+#pragma unroll 16
             for (int64_t q = from; q < to; ++q) {
                 const f32x4 x = *reinterpret_cast<const f32x4*>(a.part + (t + q) * 2 * a.dim + c);
 #pragma unroll
@@ -806,7 +809,7 @@ GradScratch grad_layout(int64_t n, int64_t rows, int dim) {
     g.counts = take(radix ? ((size_t)g.chunks << g.digit_bits) * 2 : 0);
     g.before = take(g.chunks > kFewChunks ? ((size_t)g.chunks << g.digit_bits) * 4 : 0);
     g.totals = take(g.chunks > kFewChunks ? ((size_t)4 << g.digit_bits) : 0);
-    g.owners = take((size_t)(room + 1) * 4);
+    g.owners = take((size_t)(room + 1) * 8);
     g.part = take((size_t)room * 2 * dim * sizeof(float));
     g.bytes = at;
     return g;
