@@ -221,8 +221,9 @@ __device__ __forceinline__ uint32_t key_of(int32_t id, int64_t rows, int32_t pad
 }
 
 // Zeros over a whole gradient, by workgroups beside the first sorting kernel's: 16 bytes a
-// thread, so that all that are running write next to each other (2.65 GB: 390 us, 6.8
-// TB/s; runs of 64 KiB a workgroup 480, with the nontemporal hint 520).
+// thread, so that all that are running write next to each other, and small workgroups for
+// large ones (2.65 GB: 256 threads 385 us, 6.9 TB/s, 1024 threads 425; runs of 64 KiB
+// a workgroup 480, with the nontemporal hint 520).
 struct Fill {
     u32x4* to;        // null: none
     int64_t units;    // of 16 bytes
@@ -251,35 +252,36 @@ struct SortArgs {
 // counted by a wave, the keys of all in LDS.  (A radix sort of 4096 in one
 // workgroup took 16 us.)
 constexpr int kRankMost = 8192;
-constexpr int kRankThreads = 1024;
-__global__ void __launch_bounds__(kRankThreads) sort_rank_kernel(const SortArgs a,
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) sort_rank_kernel(const SortArgs a,
                                                                  const Fill zeros) {
-    if (blockIdx.x >= zeros.first) return fill<kRankThreads>(zeros);
+    if (blockIdx.x >= zeros.first) return fill<THREADS>(zeros);
+    constexpr int EACH = 4096 / THREADS;
     __shared__ u32x4 keys[kRankMost / 4];
     uint32_t* key = reinterpret_cast<uint32_t*>(keys);
     const int tid = threadIdx.x, lane = tid & 63, n = (int)a.n, fours = (n + 3) / 4;
     bool bad = false;
-    for (int i0 = tid; i0 < fours * 4; i0 += kRankThreads * 4) {
-        int32_t id[4];  // (all on their way at once)
+    for (int i0 = tid; i0 < fours * 4; i0 += THREADS * EACH) {
+        int32_t id[EACH];  // (all on their way at once)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i = i0 + kRankThreads * j;
+        for (int j = 0; j < EACH; ++j) {
+            const int i = i0 + THREADS * j;
             id[j] = i < n ? a.ids[i] : 0;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i = i0 + kRankThreads * j;
+        for (int j = 0; j < EACH; ++j) {
+            const int i = i0 + THREADS * j;
             if (i < fours * 4) key[i] = i < n ? key_of(id[j], a.rows, a.pad_id, &bad) : ~0u;
         }
     }
     if (blockIdx.x == 0) {
         if (bad && a.err) atomicOr(a.err, ENGRAM_ERRBIT_ROW);
         if (tid == 0) *a.owners = 0;
-        for (int i = n + tid; i < (int)a.padded; i += kRankThreads)
+        for (int i = n + tid; i < (int)a.padded; i += THREADS)
             a.pair[i] = Pair{(uint32_t)a.rows, 0};
     }
     __syncthreads();
-    const int i = __builtin_amdgcn_readfirstlane(blockIdx.x * (kRankThreads / 64) + (tid >> 6));
+    const int i = __builtin_amdgcn_readfirstlane(blockIdx.x * (THREADS / 64) + (tid >> 6));
     if (i >= n) return;
     const uint32_t own = key[i];
     int before = 0;
@@ -676,6 +678,7 @@ __global__ void __launch_bounds__(THREADS) fill_kernel(const Fill zeros) {
 // Up to 64 positions: one kernel.  A workgroup takes a run of rows, zeros and sums, or,
 // where only rows that ids name are written (each = 0), 256 (row, eight columns) pairs.
 constexpr int kFewMost = 64;
+constexpr int64_t kMuchBytes = 256 << 20;  // zeros by small workgroups
 constexpr int64_t kFewBytes = 32 << 20;  // a gradient that one launch fills and sums
 template <class D, class W>
 __global__ void __launch_bounds__(256) grad_few_kernel(
@@ -836,6 +839,7 @@ hipError_t run_grad(const void* dout, const int32_t* ids, int64_t n, int streams
         *grid = first + (uint32_t)(blocks < launch ? blocks : launch);
         return f;
     };
+    const bool much = over && units * 16 > kMuchBytes;
     const bool named_only = accumulate || over;  // the sums' kernel writes no zeros
     uint32_t grid = 0;
     hipError_t e = hipSuccess;
@@ -862,9 +866,12 @@ hipError_t run_grad(const void* dout, const int32_t* ids, int64_t n, int streams
     int now = 0;
     SortArgs a{ids, n, g.padded, rows, pad_id, pair[0], owners, err};
     if (n <= kRankMost) {
-        constexpr int per = kRankThreads / 64;
-        const Fill f = zeros((uint32_t)((n + per - 1) / per), kRankThreads, &grid);
-        sort_rank_kernel<<<dim3(grid), dim3(kRankThreads), 0, s>>>(a, f);
+        const int threads = much ? 256 : 1024, per = threads / 64;
+        const Fill f = zeros((uint32_t)((n + per - 1) / per), threads, &grid);
+        if (much)
+            sort_rank_kernel<256><<<dim3(grid), dim3(256), 0, s>>>(a, f);
+        else
+            sort_rank_kernel<1024><<<dim3(grid), dim3(1024), 0, s>>>(a, f);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     } else {
         uint16_t* counts = (uint16_t*)(base + g.counts);
@@ -875,7 +882,14 @@ hipError_t run_grad(const void* dout, const int32_t* ids, int64_t n, int streams
             const int d = g.bits - shift < g.digit_bits ? g.bits - shift : g.digit_bits;
             const int last = shift + d >= g.bits;
             Fill f{nullptr, 0, (uint32_t)g.chunks, 0};
-            if (shift == 0) {
+            if (shift == 0 && much) {
+                f = zeros(0, 256, &grid);
+                fill_kernel<256><<<dim3(grid), dim3(256), 0, s>>>(f);
+                if ((e = hipGetLastError()) != hipSuccess) return e;
+                f = Fill{nullptr, 0, (uint32_t)g.chunks, 0};
+                grid = (uint32_t)g.chunks;
+                sort_count_kernel<true><<<chunks, threads, 0, s>>>(a, nullptr, shift, d, counts, f);
+            } else if (shift == 0) {
                 f = zeros((uint32_t)g.chunks, kSortThreads, &grid);
                 sort_count_kernel<true><<<dim3(grid), threads, 0, s>>>(a, nullptr, shift, d, counts, f);
             } else {

@@ -140,6 +140,22 @@ def test_gradient(ge, n, rows, dim, streams, dk, tk):
             assert torch.equal(again, dt)  # the same bits on every run
 
 
+@pytest.mark.parametrize("n", [65, 300, 8192, 8193])
+def test_large_gradients_are_zero_between_the_rows(ge, n):
+    dev = torch.device("cuda:0")
+    rows, dim = 70_001, 1024  # 287 MB
+    say("embed grad large", n)
+    g = gen(dev, n)
+    ids = torch.randint(0, rows, (n,), generator=g, device=dev, dtype=torch.int32)
+    ids[n // 2:] = ids[0]
+    dout = torch.randn(n, dim, generator=g, device=dev)
+    dt, edges = guarded((rows, dim), torch.float32, dev)
+    dt.fill_(float("nan"))
+    ge.engram_embed_grad(dout, ids, rows, dtable=dt)
+    check_grad(dt, dout, ids, rows, 1.0)
+    assert all((e == 7).all() for e in edges)
+
+
 @pytest.mark.parametrize("n", [50, 5000])
 def test_gradient_pads_bad_ids_and_shapes(ge, n):
     dev = torch.device("cuda:0")
