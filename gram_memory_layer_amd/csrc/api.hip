@@ -616,6 +616,12 @@ engram_status engram_beam_reorder(void* const* states, const int64_t* row_bytes,
 
 // ---------------------------------------------------------------- the vocabulary's two ends
 
+// whether out, which a call writes, reaches into what it reads at `in`
+static bool overlap(const void* out, int64_t out_bytes, const void* in, int64_t in_bytes) {
+    const char *a = (const char*)out, *b = (const char*)in;
+    return a < b + in_bytes && b < a + out_bytes;
+}
+
 // the sizes of a lookup and its gradient: 0, or the status that refuses them
 static engram_status embed_check(int64_t rows, int32_t dim, int64_t n, int32_t streams) {
     if (rows < 1 || n < 0 || n >= kMaxTokens || streams < 1) return ENGRAM_ERR_INVALID_ARG;
@@ -634,6 +640,10 @@ engram_status engram_embed(const void* table, int32_t table_f32, int64_t rows, i
     if (n == 0) return ENGRAM_OK;
     if (!table || !ids || !out) return ENGRAM_ERR_INVALID_ARG;
     if (!aligned16(table) || !aligned16(out) || ((uintptr_t)ids & 3u) != 0)
+        return ENGRAM_ERR_INVALID_ARG;
+    const int64_t out_bytes = n * streams * dim * (out_f32 ? 4 : 2);
+    if (overlap(out, out_bytes, table, rows * dim * (table_f32 ? 4 : 2)) ||
+        overlap(out, out_bytes, ids, n * 4))
         return ENGRAM_ERR_INVALID_ARG;
     return from_hip(engram::launch_embed(table, table_f32 != 0, rows, dim, ids, n, scale, streams,
                                          out, out_f32 != 0, err, (hipStream_t)stream));
@@ -665,6 +675,10 @@ engram_status engram_embed_grad(const void* dout, int32_t dout_f32, const int32_
         if (scratch == nullptr || scratch_bytes < engram_embed_grad_scratch_size(n, rows, dim) ||
             ((uintptr_t)scratch & 255u) != 0)
             return ENGRAM_ERR_WORKSPACE;
+        const int64_t bytes = rows * dim * (dtable_f32 ? 4 : 2);
+        if (overlap(dtable, bytes, dout, n * streams * dim * (dout_f32 ? 4 : 2)) ||
+            overlap(dtable, bytes, ids, n * 4))
+            return ENGRAM_ERR_INVALID_ARG;
     }
     return from_hip(engram::launch_embed_grad(dout, dout_f32 != 0, ids, n, streams, rows, dim,
                                               scale, pad_id, accumulate != 0, dtable,
@@ -674,7 +688,7 @@ engram_status engram_embed_grad(const void* dout, int32_t dout_f32, const int32_
 // the sizes that sampling takes: 0, or the status that refuses them
 static engram_status sample_check(int32_t B, int32_t V) {
     if (B < 0 || V < 1) return ENGRAM_ERR_INVALID_ARG;
-    if (B > 65535 || V > (1 << 22)) return ENGRAM_ERR_UNSUPPORTED;
+    if (B > 65535 || V > (1 << 22) || !engram::sample_supported(B, V)) return ENGRAM_ERR_UNSUPPORTED;
     return ENGRAM_OK;
 }
 
@@ -701,6 +715,16 @@ engram_status engram_sample(const void* logits, int32_t logits_f32, int64_t ld, 
     if (scratch == nullptr || scratch_bytes < engram_sample_scratch_size(B, V) ||
         ((uintptr_t)scratch & 255u) != 0)
         return ENGRAM_ERR_WORKSPACE;
+    const int64_t bytes = (int64_t)B * 4;  // rows are read while others' tokens are written
+    for (const void* out : {(const void*)tokens, (const void*)logprobs}) {
+        if (out == nullptr) continue;
+        for (const void* in : {(const void*)u, (const void*)temperature, (const void*)top_k,
+                               (const void*)top_p, (const void*)min_p})
+            if (in != nullptr && overlap(out, bytes, in, bytes)) return ENGRAM_ERR_INVALID_ARG;
+        if (overlap(out, bytes, logits, ((B - 1) * ld + V) * (logits_f32 ? 4 : 2)))
+            return ENGRAM_ERR_INVALID_ARG;
+    }
+    if (logprobs && overlap(logprobs, bytes, tokens, bytes)) return ENGRAM_ERR_INVALID_ARG;
     return from_hip(engram::launch_sample(logits, logits_f32 != 0, ld, u, temperature, top_k,
                                           top_p, min_p, B, V, tokens, logprobs, scratch, err,
                                           (hipStream_t)stream));

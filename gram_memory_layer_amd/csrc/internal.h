@@ -221,6 +221,8 @@ hipError_t launch_embed_grad(const void* dout, bool dout_f32, const int32_t* ids
                              bool accumulate, void* dtable, bool dtable_f32, void* scratch,
                              uint32_t* err, hipStream_t s);
 
+// (the parts' threads have to fit a launch)
+bool sample_supported(int64_t B, int V);
 size_t sample_scratch_bytes(int64_t B, int V);
 hipError_t launch_sample(const void* logits, bool f32, int64_t ld, const float* u,
                          const float* temperature, const int32_t* top_k, const float* top_p,

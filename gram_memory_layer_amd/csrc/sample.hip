@@ -488,8 +488,12 @@ struct Narrow {
         if (!find(at, ~max(in.key, key_of(least)), k == 0,
                   [&](float x, int i) { return in.keeps(x, i) ? ~key_of(x) : ~0u; },
                   [&](uint64_t a, uint64_t b) { return k ? a >= (uint64_t)k : (double)b >= target; },
-                  n, m, ties))
-            return in;  // all of them do not reach it
+                  n, m, ties)) {
+            // all of them do not reach it (by a rounding, or there are fewer)
+            Cut all = in;
+            if (key_of(least) > in.key) all.key = key_of(least), all.idx = ~0u;
+            return all;
+        }
         Cut out;
         out.key = ~at;
         out.idx = in.key == out.key ? in.idx : ~0u;
@@ -1258,6 +1262,10 @@ hipError_t run_sample(const void* logits, int64_t ld, const Request& q, int64_t 
 }
 
 }  // namespace
+
+bool sample_supported(int64_t B, int V) {
+    return (B + kXcds - 1) / kXcds * kXcds * blocks_of(V) * (64 * kBlockWaves) < ((int64_t)1 << 32);
+}
 
 size_t sample_scratch_bytes(int64_t B, int V) {
     Found f;

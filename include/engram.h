@@ -412,9 +412,10 @@ engram_status engram_beam_reorder(void* const* states, const int64_t* row_bytes,
                                   uint32_t* err, void* stream);
 
 /* ---- The vocabulary's two ends: the next token by sampling, a token's row into
- * the layer's streams, and the rows' gradient.  As above, the pages do not describe these calls, and a
- * scratch argument may be reused by the next call on the same stream and by
- * captured graphs that are replayed one after the other. */
+ * the layer's streams, and the rows' gradient.  As above, the pages do not describe
+ * these calls, and a scratch argument may be reused by the next call on the same
+ * stream and by captured graphs that are replayed one after the other.  Outputs
+ * that overlap what a call reads are refused (ENGRAM_ERR_INVALID_ARG). */
 
 /* The next token of every row of logits from a given random number.  With x the
  * row and
@@ -437,12 +438,13 @@ engram_status engram_beam_reorder(void* const* states, const int64_t* row_bytes,
  *   top_p  fp32 [B], in [0, 1], or NULL; 1: none.
  *   min_p  fp32 [B], in [0, 1], or NULL; 0: none.
  *   tokens int32 [B] out (to feed engram_hash and engram_embed); logprobs fp32 [B]
- *          out, or NULL.
+ *          out, or NULL; not overlapping the others.
  * A row whose logits are all -infinity has token -1 and logprob -infinity; so has
  * one with a NaN or +infinity among its logits (ENGRAM_ERRBIT_LOGIT), or with a
  * parameter outside the ranges above, a NaN one too (ENGRAM_ERRBIT_SAMPLE).
- * 1 <= V <= 2^22, B <= 65535.  scratch: engram_sample_scratch_size bytes, 256-byte
- * aligned; contents on entry do not matter. */
+ * 1 <= V <= 2^22, B <= 65535, about B * V < 2^37.  scratch:
+ * engram_sample_scratch_size bytes (0 where sizes are refused), 256-byte aligned;
+ * contents on entry do not matter. */
 size_t engram_sample_scratch_size(int32_t B, int32_t V);
 engram_status engram_sample(const void* logits, int32_t logits_f32, int64_t ld, const float* u,
                             const float* temperature, const int32_t* top_k, const float* top_p,

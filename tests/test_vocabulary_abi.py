@@ -75,6 +75,7 @@ def test_sample_host_checks():
         assert call(**{name: FAKE + 2}) == 1, name
     assert call(f32=2) == 1 and call(ld=999) == 1 and call(B=-1) == 1 and call(V=0) == 1
     assert call(V=(1 << 22) + 1, ld=1 << 23) == 2 and call(B=65536) == 2
+    assert call(B=65535, V=1 << 22, ld=1 << 22) == 2 and size(65535, 1 << 22) == 0  # more threads than a launch's
     assert call(scratch=None) == 3 and call(nbytes=64) == 3 and call(scratch=FAKE + 128) == 3
     assert call(B=0) == 0
 
@@ -84,3 +85,32 @@ def test_sampling_binding_refuses_what_is_not_on_the_device():
         ge.engram_sample(torch.zeros(4, 16), torch.zeros(4))
     with pytest.raises(TypeError):
         ge.engram_sample([1.0], torch.zeros(4))
+
+
+def test_outputs_that_overlap_inputs_are_refused():
+    lib = ge.load()
+    at = [(i + 1) << 32 for i in range(9)]  # far apart: refused for the one overlap that each call has
+    table, ids, scratch = at[0], at[1], at[2]
+
+    def embed(out, o32=0, streams=2):  # out: 4 * 2 * 64 values; the table 100 * 64 of bf16
+        return lib.engram_embed(table, 0, 100, 64, ids, 4, 1.0, streams, out, o32, None, None)
+    assert embed(table) == 1 and embed(table + 100 * 128 - 16) == 1 and embed(table - 1024 + 16) == 1
+    assert embed(table - 2048 + 16, o32=1) == 1 and embed(ids) == 1
+
+    def grad(dt, n=4, t32=0):
+        return lib.engram_embed_grad(table, 0, ids, n, 2, 100, 64, 1.0, -1, 0, dt, t32, scratch, 1 << 30, None, None)
+    assert grad(table) == 1 and grad(table + 4 * 256 - 16) == 1 and grad(table - 100 * 128 + 16) == 1
+    assert grad(table - 100 * 256 + 16, t32=1) == 1 and grad(ids) == 1
+
+    names = ("u", "t", "k", "p", "m", "tok", "lp")
+    places = dict(zip(names, at[2:]))
+
+    def sample(**where):
+        p = {**places, **where}
+        return lib.engram_sample(at[0], 0, 1000, p["u"], p["t"], p["k"], p["p"], p["m"], 3, 900, p["tok"], p["lp"],
+                                 at[1], 1 << 30, None, None)
+    for out in ("tok", "lp"):
+        for name in names:
+            if name != out:
+                assert sample(**{out: places[name] + 8}) == 1 and sample(**{out: places[name] - 8}) == 1, (out, name)
+        assert sample(**{out: at[0] + 2 * 2900 - 4}) == 1 and sample(**{out: at[0] - 8}) == 1, out
