@@ -244,7 +244,7 @@ struct SortArgs {
     int64_t rows;
     int32_t pad_id;
     Pair* pair;              // [padded] out, sorted; keys behind the n-th are `rows`
-    uint32_t* owners;        // a counter that a later kernel uses: set to 0
+    uint32_t* owners;        // two counters that a later kernel uses: set to 0
     uint32_t* err;
 };
 
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(THREADS) sort_rank_kernel(const SortArgs a,
     }
     if (blockIdx.x == 0) {
         if (bad && a.err) atomicOr(a.err, ENGRAM_ERRBIT_ROW);
-        if (tid == 0) *a.owners = 0;
+        if (tid < 2) a.owners[tid] = 0;
         for (int i = n + tid; i < (int)a.padded; i += THREADS)
             a.pair[i] = Pair{(uint32_t)a.rows, 0};
     }
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs
     }
     if (FIRST) {
         if (bad && a.err) atomicOr(a.err, ENGRAM_ERRBIT_ROW);
-        if (blockIdx.x == 0 && tid == 0) *a.owners = 0;
+        if (blockIdx.x == 0 && tid < 2) a.owners[tid] = 0;
     }
     __syncthreads();
     for (int b = tid; b < bins; b += kSortThreads)
@@ -439,6 +439,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(
 // parts up in order.
 constexpr int kBatch = 4;      // positions whose rows are on their way at once,
 constexpr int kBatchOne = 8;   // with one stream
+constexpr int kJoined = 16;    // and parts
+// tiles that a row reaches into behind its first: that many take the joining kernel's
+// workgroups (3, 5, 9: 98,304 positions of 64 columns 48.3, 49.1, 50.5 us; 32,768 of 2056 by
+// frequency 96.6, 95.7, 95.3)
+constexpr int kMany = 3;
 
 template <class D, class W>
 struct SumArgs {
@@ -446,7 +451,8 @@ struct SumArgs {
     const D* dout;
     W* dtable;
     float* part;         // [tiles][2][dim]
-    uint32_t* owners;    // the number of listed tiles, (nothing,) then each and its last key
+    uint32_t* owners;    // the listed tiles' numbers, of few parts and of many, then each and
+                         // its last key: those of few from the front, of many from the end
     uint32_t rows;
     uint32_t tiles;
     int dim, streams, tile;
@@ -551,7 +557,9 @@ __device__ __forceinline__ void sum_tile(const SumArgs<D, W>& a) {
     if (at_end == a.rows || a.pair[start + a.tile].key != at_end) return;
     put_part(a.part + ((int64_t)t * 2 + (begun ? 1 : 0)) * a.dim + c, sum);
     if (begun && c == 0) {
-        const uint32_t at = atomicAdd(a.owners, 1u);
+        const bool many = t + kMany < a.tiles && a.pair[start + (int64_t)kMany * a.tile].key == at_end;
+        uint32_t at = atomicAdd(a.owners + (many ? 1 : 0), 1u);
+        if (many) at = a.tiles - 1 - at;
         a.owners[2 + 2 * at] = t;
         a.owners[3 + 2 * at] = at_end;
     }
@@ -570,54 +578,103 @@ __device__ __forceinline__ int64_t first_at_least(const Pair* pair, int64_t lo, 
     return lo;
 }
 
-// The rows that reach over tiles, a wave 64 columns of one: 16 lanes four columns
-// each, the wave's four quarters an equal share of the parts, joined in order.
+// the last tile that begins with the row that tile t ends with, 64 looked at together
+template <class D, class W>
+__device__ __forceinline__ uint32_t last_tile(const SumArgs<D, W>& a, uint32_t t, uint32_t key) {
+    const uint32_t lane = threadIdx.x & 63;
+    uint32_t lo = t + 1, hi = a.tiles;  // lo does; hi does not, or is none
+    while (lo + 1 < hi) {
+        const uint32_t step = (hi - lo + 63) / 64, q = lo + lane * step;
+        const bool in = q < hi && a.pair[(int64_t)q * a.tile].key == key;
+        const uint32_t yes = (uint32_t)__builtin_popcountll(__ballot(in));
+        hi = lo + yes * step < hi ? lo + yes * step : hi;
+        lo += (yes - 1) * step;
+    }
+    return lo;
+}
+
+// Four columns of share i of n of a row's parts: that of tile t, where it begins, then one
+// of each tile behind it.
+template <class D, class W>
+__device__ __forceinline__ f32x4 sum_parts(const SumArgs<D, W>& a, uint32_t t, uint32_t last, int c,
+                                           int i, int n) {
+    const int64_t parts = last - t, each = (parts + n - 1) / n;  // behind the first one
+    const int64_t from = 1 + i * each, to = min(from + each, parts + 1);
+    f32x4 sum = {0, 0, 0, 0};
+    if (c >= a.dim) return sum;
+    if (i == 0) sum = *reinterpret_cast<const f32x4*>(a.part + ((int64_t)t * 2 + 1) * a.dim + c);
+    for (int64_t q0 = from; q0 < to; q0 += kJoined) {
+        f32x4 x[kJoined];  // (on their way at once; behind the share's last one that one again)
+#pragma unroll
+        for (int j = 0; j < kJoined; ++j)
+            x[j] = *reinterpret_cast<const f32x4*>(a.part + (t + min(q0 + j, to - 1)) * 2 * a.dim + c);
+#pragma unroll
+        for (int j = 0; j < kJoined; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] = q0 + j < to ? sum[e] + x[j][e] : sum[e];
+    }
+    return sum;
+}
+
+// Four columns of a row that reaches over tiles, by its parts' sum.
+template <class D, class W>
+__device__ __forceinline__ void put_four(const SumArgs<D, W>& a, uint32_t key, int c, const f32x4& sum) {
+    W* to = a.dtable + (int64_t)key * a.dim + c;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(W) == 4)
+            to[e] = a.accumulate ? __builtin_fmaf(a.scale, sum[e], to[e]) : a.scale * sum[e];
+        else
+            to[e] = (W)f32_to_bf16(a.accumulate ? __builtin_fmaf(a.scale, sum[e], bf16_to_f32(to[e]))
+                                                : a.scale * sum[e]);
+    }
+}
+
+// The rows that reach over tiles.  One of many parts takes a workgroup for 64 columns, 16
+// lanes four each of a sixteenth of the parts, the shares joined in order; of the others a
+// thread takes four columns.
 template <class D, class W>
 __global__ void __launch_bounds__(256) grad_join_kernel(const SumArgs<D, W> a) {
-    const uint32_t blocks = (uint32_t)(a.dim + 63) / 64;
-    const uint32_t total = a.owners[0] * blocks;
-    const int lane = threadIdx.x & 63, quarter = lane >> 4;
-    const uint32_t wave = blockIdx.x * 4 + (threadIdx.x >> 6);
-    for (uint32_t w = wave; w < total; w += gridDim.x * 4) {
-        const uint32_t at = w / blocks, t = a.owners[2 + 2 * at], key = a.owners[3 + 2 * at];
-        const int c = (int)(w - at * blocks) * 64 + (lane & 15) * 4;
-        // the last tile that begins with the row: 64 at a time
-        uint32_t lo = t + 1, hi = a.tiles;  // lo does; hi does not, or is none
-        while (lo + 1 < hi) {
-            const uint32_t step = (hi - lo + 63) / 64, q = lo + lane * step;
-            const bool in = q < hi && a.pair[(int64_t)q * a.tile].key == key;
-            const uint32_t yes = (uint32_t)__builtin_popcountll(__ballot(in));
-            hi = lo + yes * step < hi ? lo + yes * step : hi;
-            lo += (yes - 1) * step;
-        }
-        const int64_t parts = lo - t, each = (parts + 3) / 4;  // behind the first one
-        const int64_t from = 1 + quarter * each, to = min(from + each, parts + 1);
-        f32x4 sum = {0, 0, 0, 0};
-        if (c < a.dim) {
-            if (quarter == 0) sum = *reinterpret_cast<const f32x4*>(a.part + ((int64_t)t * 2 + 1) * a.dim + c);
-#pragma unroll 16
-            for (int64_t q = from; q < to; ++q) {
-                const f32x4 x = *reinterpret_cast<const f32x4*>(a.part + (t + q) * 2 * a.dim + c);
+    __shared__ f32x4 shares[16][16];
+    const uint32_t blocks = (uint32_t)(a.dim + 63) / 64, many = a.owners[1] * blocks;
+    const int tid = threadIdx.x;
+    for (uint32_t w = blockIdx.x; w < many; w += gridDim.x) {
+        const uint32_t at = a.tiles - 1 - w / blocks, t = a.owners[2 + 2 * at], key = a.owners[3 + 2 * at];
+        const int c = (int)(w % blocks) * 64 + (tid & 15) * 4;
+        shares[tid >> 4][tid & 15] = sum_parts(a, t, last_tile(a, t, key), c, tid >> 4, 16);
+        __syncthreads();
+        if (tid < 16 && c < a.dim) {
+            f32x4 sum = shares[0][tid];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) {
+                const f32x4 x = shares[i][tid];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sum[e] += x[e];
             }
+            put_four(a, key, c, sum);
         }
+        __syncthreads();
+    }
+    const uint32_t per_row = (uint32_t)a.dim / 4;
+    const uint64_t few = (uint64_t)a.owners[0] * per_row;
+    for (uint64_t i = (uint64_t)blockIdx.x * 256 + tid; i < few; i += (uint64_t)gridDim.x * 256) {
+        const uint32_t at = (uint32_t)(i / per_row), t = a.owners[2 + 2 * at], key = a.owners[3 + 2 * at];
+        const int c = (int)(i - (uint64_t)at * per_row) * 4;
+        bool goes_on[kMany];  // the row reaches into the j-th tile behind its first
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {  // ((0 + 1) + (2 + 3))
-            sum[e] += __shfl_down(sum[e], 16, 64);
-            sum[e] += __shfl_down(sum[e], 32, 64);
-        }
-        if (quarter == 0 && c < a.dim) {
-            W* to_row = a.dtable + (int64_t)key * a.dim + c;
+        for (int j = 1; j < kMany; ++j)
+            goes_on[j] = t + j < a.tiles && a.pair[(int64_t)(t + j) * a.tile].key == key;
+        f32x4 sum = *reinterpret_cast<const f32x4*>(a.part + ((int64_t)t * 2 + 1) * a.dim + c);
+        f32x4 x[kMany];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (sizeof(W) == 4)
-                    to_row[e] = a.accumulate ? __builtin_fmaf(a.scale, sum[e], to_row[e]) : a.scale * sum[e];
-                else
-                    to_row[e] = (W)f32_to_bf16(a.accumulate ? __builtin_fmaf(a.scale, sum[e], bf16_to_f32(to_row[e]))
-                                                            : a.scale * sum[e]);
-            }
-        }
+        for (int j = 1; j < kMany; ++j)
+            if (goes_on[j]) x[j] = *reinterpret_cast<const f32x4*>(a.part + (int64_t)(t + j) * 2 * a.dim + c);
+#pragma unroll
+        for (int j = 1; j < kMany; ++j)
+            if (goes_on[j])
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] += x[j][e];
+        put_four(a, key, c, sum);
     }
 }
 
@@ -935,8 +992,8 @@ hipError_t run_grad(const void* dout, const int32_t* ids, int64_t n, int streams
         sum_blocks = 0;
     }
     if (g.tiles > 1) {
-        const int64_t items = (g.tiles - 1) * ((dim + 63) / 64);  // at most: a wave each
-        grad_join_kernel<D, W><<<dim3((uint32_t)std::min<int64_t>((items + 3) / 4, 2048)), dim3(256), 0, s>>>(b);
+        const int64_t items = (g.tiles - 1) * (dim / 4);  // at most: a thread each
+        grad_join_kernel<D, W><<<dim3((uint32_t)std::min<int64_t>((items + 255) / 256, 2048)), dim3(256), 0, s>>>(b);
         e = hipGetLastError();
     }
     return e;

@@ -261,6 +261,27 @@ def test_many_positions(ge):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("n", [62 * 2048, 62 * 2048 + 1, 8193, 5000])
+def test_rows_named_by_most_positions(ge, n):
+    """Whole numbers, summed exactly in any order: one row that every position, or most, names
+    (counts that fill a sort's words; rows of one part to thousands), between rows named once."""
+    dev = torch.device("cuda:0")
+    g = gen(dev, n)
+    for rows, dim in ((1, 72), (2, 8), (6, 8), (9, 64), (30, 8), (100, 136), (1000, 8), (40000, 64)):
+        say(f"{n} positions of {rows} rows of {dim}")
+        hot = rows // 2
+        for share in (0.0, 0.02, 0.5):  # of positions that name another row
+            ids = torch.where(torch.rand(n, generator=g, device=dev) < share,
+                              torch.randint(0, rows, (n,), generator=g, device=dev), hot).int()
+            dout = torch.randint(-3, 9, (n, dim), generator=g, device=dev).float()
+            dt = ge.engram_embed_grad(dout, ids, rows)
+            rest = ids != hot
+            want = torch.zeros(rows, dim, dtype=torch.float64, device=dev)
+            want.index_add_(0, ids[rest].long(), dout[rest].double())
+            want[hot] = dout[~rest].double().sum(0)
+            assert torch.equal(dt.double(), want), (rows, share)
+
+
 def test_streams_of_work_and_graphs(ge):
     dev = torch.device("cuda:0")
     say("embed in a graph")
