@@ -25,14 +25,14 @@ constexpr int kRest = kBuckets - 1;           // the last one takes all below, t
 constexpr int kXcds = 8;                      // workgroups go to these in turn: a row's all to one, so
                                               // that its logits are in the cache of the last one's
 constexpr int kCopies = 4;                    // of the buckets in LDS: lanes that meet in one wait for each other
-constexpr int kGroup = 16;                    // lanes whose largest logit is kept
+constexpr int kGroup = 4;                     // lanes whose largest logit is kept
 constexpr int kRowThreads = 512;
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kBinBits = 9, kBins = 1 << kBinBits;  // a thread each
 constexpr int kList = 8192;                   // candidates in LDS,
 constexpr int kManyBefore = 1024;
 constexpr int kSome = 64, kRanked = 256;       // that are ranked by counting, by a wave or all
-constexpr int kHits = 4 * kRowThreads;        // groups of a row looked at together
+constexpr int kHits = 16 * kRowThreads;       // groups of a row looked at together
 constexpr int kMostBlocks = 256;              // of a row whose buckets are joined
 
 // exp(d / T) for d <= 0, by c = log2(e) / T: 2^n * 2^f, f in [-1/2, 1/2], 2^f by a
@@ -160,7 +160,11 @@ __device__ __forceinline__ uint64_t last_lane(uint64_t x) {
     return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), 63) << 32 |
            (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
 }
-// the largest of 16 lanes, in all of them
+// the largest of four lanes, and of 16, in all of them
+__device__ __forceinline__ float largest_of_4(float x) {
+    x = fmaxf(x, __uint_as_float(moved<0xB1>(__float_as_uint(x))));
+    return fmaxf(x, __uint_as_float(moved<0x4E>(__float_as_uint(x))));
+}
 __device__ __forceinline__ float largest_of_16(float x) {
     x = fmaxf(x, __uint_as_float(moved<0x128>(__float_as_uint(x))));  // (rotations: no lane goes without)
     x = fmaxf(x, __uint_as_float(moved<0x124>(__float_as_uint(x))));
@@ -257,7 +261,7 @@ __global__ void __launch_bounds__(64 * kBlockWaves) sample_part_kernel(
         const bool weights = want.whole_sum();
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            const float g = largest_of_16(own[i]);
+            const float g = largest_of_4(own[i]);
             if ((lane & (kGroup - 1)) == 0)
                 out.groups[row * out.blocks * (NT * NL / kGroup) + (from + lane + 64 * i) / kGroup] = g;
         }
@@ -314,7 +318,7 @@ struct Shared {
     double factor[kMostBlocks], blocks[kMostBlocks];
     int offset[kMostBlocks];
     int list[kList];
-    __align__(8) int hit[kHits];
+    __align__(8) uint16_t hit[kHits];
 };
 
 // sum over the workgroup, and this thread's share of it: what lies before it
@@ -784,7 +788,7 @@ struct Sampler {
     // Up to kRanked of them: two threads a candidate count those before it in the order
     // and by the index.
     __device__ __forceinline__ void ranked(int n, double total) const {
-        static_assert(2 * kRanked <= kRowThreads && kRanked <= kHits, "");
+        static_assert(2 * kRanked <= kRowThreads && kRanked * sizeof(uint2) <= sizeof(sh.hit), "");
         const int tid = threadIdx.x, j = tid >> 1;
         const bool there = j < n;
         const int idx = there ? sh.list[j] : 0;
@@ -869,80 +873,98 @@ struct Sampler {
         for (; found; found &= found - 1, ++at)
             if (at < kList) sh.list[at] = place_of(__builtin_ctz(found));
     }
-    __device__ __forceinline__ uint32_t found_in(const uint4 (&raw)[AT], float least, float most) const {
+    // the logits above low and not above high, a bit each: a difference's sign (four
+    // instructions a logit; two comparisons, joined, and a bit take ten issue slots)
+    __device__ __forceinline__ uint32_t found_in(const uint4 (&raw)[AT], float low, float high) const {
         uint32_t found = 0;
 #pragma unroll
-        for (int j = 0; j < AT; ++j) {
+        for (int j = AT - 1; j >= 0; --j) {
             float v[VEC];
             r.values(raw[j], v);
+            if (low == -INFINITY) {  // (a difference would be none)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) found |= v[e] >= least && v[e] < most ? 1u << (j * VEC + e) : 0u;
+                for (int e = 0; e < VEC; ++e) found |= v[e] > low && v[e] <= high ? 1u << (j * VEC + e) : 0u;
+            } else {
+#pragma unroll
+                for (int e = VEC - 1; e >= 0; --e)
+                    found = __builtin_amdgcn_alignbit(
+                        found, __float_as_uint(low - v[e]) ^ __float_as_uint(high - v[e]), 31);
+            }
         }
         return found;
     }
+    // the next logit below x, which is above -infinity
+    __device__ __forceinline__ float below(float x) const {
+        const float y = value_of(key_of(x) - 1);
+        return y == 0.0f && !(x > 0.0f) ? -0x1p-149f : y;  // (below both zeros)
+    }
 
-    // The places of the logits in [least, most) into the list; how many there are.
+    // The places of the logits in [least, most) into the list, the row's pieces in turn, the
+    // next ones on their way; its ends, which are no whole pieces, first.
+    __device__ __forceinline__ int in_turn(float least, float most) const {
+        const int tid = threadIdx.x;
+        const int begin = r.before ? 1 : 0, end = max((r.before + V) / VEC, begin);
+        if (tid < 2 * VEC) {
+            const int i = tid < VEC ? tid : end * VEC - r.before + tid - VEC;
+            if (i < (tid < VEC ? min(begin * VEC - r.before, V) : V) && value(i) >= least && value(i) < most) {
+                const int at = atomicAdd(&sh.listed, 1);
+                if (at < kList) sh.list[at] = i;
+            }
+        }
+        const float low = below(least), high = below(most);
+        uint4 raw[AT], next[AT];
+        auto fetch = [&](int i0) {
+#pragma unroll
+            for (int j = 0; j < AT; ++j) {
+                const int i = min(i0 + j * kRowThreads, end - 1);
+                next[j] = *reinterpret_cast<const uint4*>(r.src + (i * VEC - r.before));
+            }
+        };
+        if (end > begin) {
+            fetch(begin + tid);
+            for (int i0 = begin + tid; __any(i0 < end); i0 += AT * kRowThreads) {
+#pragma unroll
+                for (int j = 0; j < AT; ++j) raw[j] = next[j];
+                fetch(i0 + AT * kRowThreads);
+                uint32_t found = found_in(raw, low, high);
+                const int there = i0 < end ? (end - i0 + kRowThreads - 1) / kRowThreads : 0;
+                if (there < AT) found &= (1u << there * VEC) - 1;
+                list(found, [&](int bit) {
+                    return (i0 + bit / VEC * kRowThreads) * VEC - r.before + bit % VEC;
+                });
+            }
+        }
+        __syncthreads();
+        return sh.listed;
+    }
+
+    // The same by the groups whose largest logit is one, where these are not most.
     // (tops: the first kHits groups')
     __device__ __forceinline__ int gather(const float* groups, int n_groups,
                                           const float (&tops)[kHits / kRowThreads], float least,
                                           float most) const {
         const int tid = threadIdx.x, lane = tid & (kGroup - 1);
-        int many = 0;
-#pragma unroll
-        for (int j = 0; j < kHits / kRowThreads; ++j) many += tops[j] >= least ? 1 : 0;
+        const float low = below(least), high = below(most);
         __syncthreads();
-        if (tid == 0) sh.listed = 0;
-        many = __syncthreads_count(2 * many > kHits / kRowThreads);
-        if (2 * many > min(kRowThreads, n_groups)) {
-            // most groups have one: the row's pieces in turn, the next ones on their way;
-            // its ends, which are no whole pieces, first
-            const int begin = r.before ? 1 : 0, end = max((r.before + V) / VEC, begin);
-            if (tid < 2 * VEC) {
-                const int i = tid < VEC ? tid : end * VEC - r.before + tid - VEC;
-                if (i < (tid < VEC ? min(begin * VEC - r.before, V) : V) && value(i) >= least && value(i) < most) {
-                    const int at = atomicAdd(&sh.listed, 1);
-                    if (at < kList) sh.list[at] = i;
-                }
-            }
-            uint4 raw[AT], next[AT];
-            auto fetch = [&](int i0) {
-#pragma unroll
-                for (int j = 0; j < AT; ++j) {
-                    const int i = min(i0 + j * kRowThreads, end - 1);
-                    next[j] = *reinterpret_cast<const uint4*>(r.src + (i * VEC - r.before));
-                }
-            };
-            if (end > begin) {
-                fetch(begin + tid);
-                for (int i0 = begin + tid; __any(i0 < end); i0 += AT * kRowThreads) {
-#pragma unroll
-                    for (int j = 0; j < AT; ++j) raw[j] = next[j];
-                    fetch(i0 + AT * kRowThreads);
-                    uint32_t found = found_in(raw, least, most);
-                    const int there = i0 < end ? (end - i0 + kRowThreads - 1) / kRowThreads : 0;
-                    if (there < AT) found &= (1u << there * VEC) - 1;
-                    list(found, [&](int bit) {
-                        return (i0 + bit / VEC * kRowThreads) * VEC - r.before + bit % VEC;
-                    });
-                }
-            }
-            __syncthreads();
-            return sh.listed;
-        }
+        if (tid == 0) sh.listed = sh.hits = 0;
+        __syncthreads();
         for (int g0 = 0; g0 < n_groups; g0 += kHits) {
-            float x[kHits / kRowThreads];
+            uint32_t hit = 0;
 #pragma unroll
             for (int j = 0; j < kHits / kRowThreads; ++j) {
                 const int g = g0 + j * kRowThreads + tid;
-                x[j] = g0 == 0 ? tops[j] : g < n_groups ? groups[g] : -INFINITY;
+                const float x = g0 == 0 ? tops[j] : g < n_groups ? groups[g] : -INFINITY;
+                hit |= x >= least ? 1u << j : 0u;
             }
-            if (tid == 0) sh.hits = 0;
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < kHits / kRowThreads; ++j)
-                if (x[j] >= least) sh.hit[atomicAdd(&sh.hits, 1)] = g0 + j * kRowThreads + tid;
+            const uint32_t own = __builtin_popcount(hit), upto = sum_upto(own);
+            uint32_t at = 0;
+            if ((tid & 63) == 63) at = atomicAdd((uint32_t*)&sh.hits, upto);
+            at = __builtin_amdgcn_readlane(at, 63) + upto - own;
+            for (; hit; hit &= hit - 1, ++at)
+                sh.hit[at] = (uint16_t)(__builtin_ctz(hit) * kRowThreads + tid);
             __syncthreads();
             const int hits = sh.hits;
+            if (g0 == 0 && 2 * hits > min(n_groups, kHits)) return in_turn(least, most);
             // where the row's ends or no group are a piece is all -infinity until its
             // logits are looked at one by one
             constexpr int HOP = kRowThreads / kGroup;
@@ -954,26 +976,31 @@ struct Sampler {
                 for (int j = 0; j < AT; ++j) {
                     raw[j] = make_uint4(NONE, NONE, NONE, NONE);
                     if (h0 + j * HOP < hits) {
-                        const int col = (sh.hit[h0 + j * HOP] * kGroup + lane) * VEC - r.before;
+                        const int col = ((g0 + sh.hit[h0 + j * HOP]) * kGroup + lane) * VEC - r.before;
                         if (col >= 0 && col <= V - VEC)
                             raw[j] = *reinterpret_cast<const uint4*>(r.src + col);
                         else
                             part |= 1u << j;
                     }
                 }
-                uint32_t found = found_in(raw, least, most);
+                uint32_t found = found_in(raw, low, high);
                 while (part) {
-                    const int j = __builtin_ctz(part), col = (sh.hit[h0 + j * HOP] * kGroup + lane) * VEC - r.before;
+                    const int j = __builtin_ctz(part);
+                    const int col = ((g0 + sh.hit[h0 + j * HOP]) * kGroup + lane) * VEC - r.before;
                     part &= part - 1;
                     for (int e = 0; e < VEC; ++e)
                         if (col + e >= 0 && col + e < V && value(col + e) >= least && value(col + e) < most)
                             found |= 1u << (j * VEC + e);
                 }
                 list(found, [&](int bit) {
-                    return (sh.hit[h0 + bit / VEC * HOP] * kGroup + lane) * VEC - r.before + bit % VEC;
+                    return ((g0 + sh.hit[h0 + bit / VEC * HOP]) * kGroup + lane) * VEC - r.before + bit % VEC;
                 });
             }
             __syncthreads();
+            if (g0 + kHits < n_groups) {
+                if (tid == 0) sh.hits = 0;
+                __syncthreads();
+            }
         }
         return sh.listed;
     }
