@@ -309,7 +309,7 @@ struct Shared {
     double sum[kRowWaves];
     uint64_t whole[2][kRowWaves];
     uint32_t count[kBins];
-    uint64_t mass[kBins];
+    uint64_t mass[kBins + 1];  // (a row's blocks are at most that many)
     int first, last, hits, listed, at[kRowWaves];
     uint32_t range[2];
     bool none;
@@ -567,64 +567,17 @@ struct Sampler {
             }
         }
     }
-    // the same, a run of neighbouring pieces for each thread
-    template <class F>
-    __device__ __forceinline__ void in_order(F f) const {
-        const int each = (pieces + kRowThreads - 1) / kRowThreads;
-        const int begin = threadIdx.x * each, end = min(begin + each, pieces);
-        for (int i = begin; i < end; ++i) some(i, f);
-    }
-
-    // The token among the row's logits that stay: the first whose sum exceeds u times the
-    // sum of all.
-    template <class Stays>
-    __device__ __forceinline__ void pick(Stays stays) const {
-        double own = 0.0, total;
-        in_order([&](float x, int i) {
-            const double w = want.weigh(x, top);
-            if (w > kNoWeight && stays(x, i)) own += w;
-        });
-        const double before = scan(own, sh, &total), target = want.u * total;
-        if ((int)threadIdx.x != holder(before, own, target, sh)) return;
-        double sum = before, w_token = 0.0;
-        int at = -1;
-        bool done = false;
-        in_order([&](float x, int i) {
-            const double w = want.weigh(x, top);
-            if (done || !(w > kNoWeight) || !stays(x, i)) return;
-            sum += w;
-            at = i;
-            w_token = w;
-            done = sum > target;
-        });
-        emit(at, log(w_token / total));
-    }
-    // The token among the logits of pieces from .. to, at most a block of them, held in
-    // registers: the first of those that stay whose sum exceeds target.
-    template <class Stays>
-    __device__ __forceinline__ void pick_near(int from, int to, double target, double total, Stays stays) const {
-        constexpr int E = kPieces / kRowThreads;
-        const int each = (to - from + kRowThreads - 1) / kRowThreads, begin = from + threadIdx.x * each;
-        uint4 raw[E];
+    // The token among logits whose weights w (0: does not stay) the threads hold, those of
+    // pieces from begin on: the first whose sum exceeds target.
+    template <int E>
+    __device__ __forceinline__ void choose(const double (&w)[E][VEC], int begin, double target, double total) const {
+        double own = 0.0, here;
 #pragma unroll
-        for (int j = 0; j < E; ++j) raw[j] = r.fetch(j < each && begin + j < to ? begin + j : pieces, V);
-        double w[E][VEC], own = 0.0, here;
+        for (int j = 0; j < E; ++j)
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const bool in = j < each && begin + j < to;
-            float x[VEC];
-            r.unpack(raw[j], in ? begin + j : pieces, V, x);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                w[j][e] = want.weigh(x[e], top);
-                if (!(w[j][e] > kNoWeight && x[e] > -INFINITY && stays(x[e], (int)r.column(begin + j) + e)))
-                    w[j][e] = 0.0;
-                own += w[j][e];
-            }
-        }
-        const double before = scan(own, sh, &here);
-        if ((int)threadIdx.x != holder(before, own, target, sh)) return;
-        double sum = before, w_token = 0.0;
+            for (int e = 0; e < VEC; ++e) own += w[j][e];
+        double sum = scan(own, sh, &here), w_token = 0.0;
+        if ((int)threadIdx.x != holder(sum, own, target, sh)) return;
         int at = -1;
         bool done = false;
 #pragma unroll
@@ -638,6 +591,158 @@ struct Sampler {
                 done = sum > target;
             }
         emit(at, log(w_token / total));
+    }
+
+    // The token among the logits of a part, all of which stay.
+    __device__ __forceinline__ void pick_near(int part, double target, double total) const {
+        constexpr int PER = NL * 64, E = (PER + kRowThreads - 1) / kRowThreads;
+        const int begin = part * PER + threadIdx.x * E;
+        double w[E][VEC];
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const int i = threadIdx.x * E + j < PER ? begin + j : pieces;
+            float x[VEC];
+            r.unpack(r.fetch(i, V), i, V, x);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                w[j][e] = want.weigh(x[e], top);
+                if (!(w[j][e] > kNoWeight && x[e] > -INFINITY)) w[j][e] = 0.0;
+            }
+        }
+        choose(w, begin, target, total);
+    }
+
+    // The same among a block's that stay.  Where these are few, their places in order
+    // first, so that few weights are taken.
+    template <class Stays>
+    __device__ __forceinline__ void pick_listed(int block, double target, double total, Stays stays) const {
+        constexpr int E = kPieces / kRowThreads;
+        const int tid = threadIdx.x, begin = block * kPieces + tid * E;
+        uint4 raw[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) raw[j] = r.fetch(begin + j, V);
+        float x[E][VEC];
+        uint32_t found = 0;
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            r.unpack(raw[j], begin + j, V, x[j]);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (x[j][e] > -INFINITY && stays(x[j][e], (int)r.column(begin + j) + e)) found |= 1u << (j * VEC + e);
+        }
+        const int own = __builtin_popcount(found), upto = (int)sum_upto((uint32_t)own);
+        if ((tid & 63) == 63) sh.at[tid >> 6] = upto;
+        __syncthreads();
+        int at = upto - own, n = 0;
+#pragma unroll
+        for (int w = 0; w < kRowWaves; ++w) {
+            at += w < (tid >> 6) ? sh.at[w] : 0;
+            n += sh.at[w];
+        }
+        constexpr int FEW = 4;  // a thread
+        if (n > FEW * kRowThreads) {
+            double w[E][VEC];
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    w[j][e] = want.weigh(x[j][e], top);
+                    if (!(found >> (j * VEC + e) & 1) || !(w[j][e] > kNoWeight)) w[j][e] = 0.0;
+                }
+            return choose(w, begin, target, total);
+        }
+        for (; found; found &= found - 1, ++at) sh.list[at] = (int)r.column(begin) + __builtin_ctz(found);
+        __syncthreads();
+        const int each = (n + kRowThreads - 1) / kRowThreads, from = tid * each, to = min(from + each, n);
+        int places[FEW];
+        double w[FEW], own_sum = 0.0, here;
+#pragma unroll
+        for (int j = 0; j < FEW; ++j) places[j] = from + j < to ? sh.list[from + j] : 0;
+        float y[FEW];
+#pragma unroll
+        for (int j = 0; j < FEW; ++j) y[j] = value(places[j]);
+#pragma unroll
+        for (int j = 0; j < FEW; ++j) {
+            w[j] = 0.0;
+            if (j >= each) break;
+            w[j] = want.weigh(y[j], top);
+            if (!(from + j < to && w[j] > kNoWeight)) w[j] = 0.0;
+            own_sum += w[j];
+        }
+        double sum = scan(own_sum, sh, &here), w_token = 0.0;
+        if (tid != holder(sum, own_sum, target, sh)) return;
+        int token_at = -1;
+        bool done = false;
+#pragma unroll
+        for (int j = 0; j < FEW; ++j) {
+            if (done || !(w[j] > 0.0)) continue;
+            sum += w[j];
+            token_at = places[j];
+            w_token = w[j];
+            done = sum > target;
+        }
+        emit(token_at, log(w_token / total));
+    }
+
+    // The weights of the row's logits that stay, summed by block, a wave each in turn, and
+    // their sum; own: what the thread's blocks [from, to) hold, the sum before it is returned.
+    template <class Stays>
+    __device__ __forceinline__ double weigh_blocks(Stays stays, int& from, int& to, double& own,
+                                                   double& total) const {
+        constexpr int AT = 4;
+        const int tid = threadIdx.x, lane = tid & 63, blocks = (pieces + kPieces - 1) / kPieces;
+        double* by = reinterpret_cast<double*>(sh.mass);
+        __syncthreads();
+        for (int g = tid >> 6; g < blocks; g += kRowWaves) {
+            double s = 0.0;
+            for (int i0 = g * kPieces + lane; i0 < (g + 1) * kPieces; i0 += AT * 64) {
+                uint4 raw[AT];
+#pragma unroll
+                for (int j = 0; j < AT; ++j) raw[j] = r.fetch(i0 + 64 * j, V);
+#pragma unroll
+                for (int j = 0; j < AT; ++j) {
+                    float x[VEC];
+                    r.unpack(raw[j], i0 + 64 * j, V, x);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        if (!(x[e] > -INFINITY && stays(x[e], (int)r.column(i0 + 64 * j) + e))) continue;
+                        const double w = want.weigh(x[e], top);
+                        s += w > kNoWeight ? w : 0.0;
+                    }
+                }
+            }
+            s = last_lane(sum_upto(s));
+            if (lane == 0) by[g] = s;
+        }
+        __syncthreads();
+        const int each = (blocks + kRowThreads - 1) / kRowThreads;
+        from = tid * each;
+        to = min(from + each, blocks);
+        own = 0.0;
+        for (int g = from; g < to; ++g) own += by[g];
+        return scan(own, sh, &total);
+    }
+
+    // The token among the row's logits that stay: the first whose sum exceeds u times the
+    // sum of all.
+    template <class Stays>
+    __device__ __forceinline__ void pick(Stays stays) const {
+        const double* by = reinterpret_cast<const double*>(sh.mass);
+        int from, to;
+        double own, total;
+        double sum = weigh_blocks(stays, from, to, own, total);
+        const double target = want.u * total;
+        if ((int)threadIdx.x == holder(sum, own, target, sh)) {
+            for (int g = from; g < to; ++g) {
+                if (!(by[g] > 0.0)) continue;
+                sh.found[0] = sum;
+                sh.hits = g;
+                sum += by[g];
+                if (sum > target) break;
+            }
+        }
+        __syncthreads();
+        pick_listed(sh.hits, target - sh.found[0], total, stays);
     }
 
     // the first of the largest: its part, then its place
@@ -686,9 +791,7 @@ struct Sampler {
             sh.hits = part;
         }
         __syncthreads();
-        const int begin = sh.hits * (NL * 64);
-        pick_near(begin, min(begin + NL * 64, pieces), target - sh.found[0], total,
-                  [](float, int) { return true; });
+        pick_near(sh.hits, target - sh.found[0], total);
     }
 
     // Any filters on any row, by passes over it.  The first cut lies in [least, over), with
@@ -723,11 +826,9 @@ struct Sampler {
         for (int again = 0; again < 2; ++again) {  // top-k, then top-p
             if (again ? want.p == 1.0 : want.k == 0) continue;
             if (again && want.k) {
-                double own = 0.0;
-                in_order([&](float x, int i) {
-                    if (keep.keeps(x, i)) own += want.weigh(x, top);
-                });
-                scan(own, sh, &total);
+                int from, to;
+                double own;
+                weigh_blocks([&](float x, int i) { return keep.keeps(x, i); }, from, to, own, total);
                 above = 0.0;
                 least = value_of(keep.key);
                 most = top;
@@ -1198,8 +1299,8 @@ struct Sampler {
         const int block = holder(at, own, target, sh);
         if (tid == block) sh.found[0] = at;
         __syncthreads();
-        pick_near(block * kPieces, min((block + 1) * kPieces, pieces), target - sh.found[0], stay,
-                  [&](float v, int i) { return v >= over || (v >= least && v >= floor && keep.keeps(v, i)); });
+        pick_listed(block, target - sh.found[0], stay,
+                    [&](float v, int i) { return v >= over || (v >= least && v >= floor && keep.keeps(v, i)); });
         return true;
     }
 };
