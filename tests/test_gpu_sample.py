@@ -336,6 +336,49 @@ def test_the_largest_vocabulary(ge, dtype):
     check(ge, x, u, k=full(1 << 21, torch.int32), p=full(0.9))
 
 
+@pytest.mark.parametrize("dtype", KINDS)
+def test_the_largest_vocabulary_behind_a_boundary(ge, dtype):
+    """A row that begins inside 16 bytes reaches into one block more."""
+    dev = torch.device("cuda:0")
+    V, first = 1 << 22, 7 if dtype == "bf16" else 3
+    say("sample largest vocabulary at element", first, dtype)
+    buf = torch.full((V + 16,), -9.0, dtype=KINDS[dtype], device=dev)
+    buf[first + V - 3:first + V] = 5.0
+    x = buf[first:first + V][None]
+    f = lambda v, kind=torch.float32: torch.tensor([v], dtype=kind, device=dev)  # noqa: E731
+    for u in (0.0, 0.3, 0.7, 1 - 2.0 ** -24):
+        check(ge, x, f(u))
+        check(ge, x, f(u), k=f(2, torch.int32))
+        check(ge, x, f(u), p=f(0.9))
+        check(ge, x, f(u), k=f(4_000_000, torch.int32), p=f(0.99))
+    buf.fill_(1.0)
+    for u in (0.5, 1 - 2.0 ** -24):
+        check(ge, x, f(u), p=f(0.75))
+        check(ge, x, f(u), k=f(4_194_301, torch.int32))
+
+
+def test_cuts_at_zeros_subnormals_and_the_ends_of_the_range(ge):
+    dev = torch.device("cuda:0")
+    tiny, huge = 2.0 ** -149, 3.0e38
+    for V in (40, 900, 20011, 70001):
+        g = torch.Generator(device=dev)
+        g.manual_seed(V)
+        for values in ((0.0, -0.0, tiny, -tiny), (0.0, -0.0), (-0.0, -1e-38, 1e-38, -tiny),
+                       (0.0, -huge, -torch.finfo(torch.float32).max, -INF), (huge, -huge, 1.0, -INF)):
+            say("sample zeros and ends", V, values)
+            which = torch.randint(0, len(values), (3, V), generator=g, device=dev)
+            x = torch.tensor(values, device=dev)[which]
+            u = torch.rand(3, generator=g, device=dev)
+            full = lambda v, kind=torch.float32: torch.full((3,), v, dtype=kind, device=dev)  # noqa: E731
+            for k in (1, 7, V // 4, V // 3, V - 2):
+                check(ge, x, u, k=full(k, torch.int32))
+                check(ge, x, u, t=full(1e38), k=full(k, torch.int32), p=full(0.9))
+            for p in (0.1, 0.5, 0.9):
+                check(ge, x, u, p=full(p))
+                check(ge, x, u, t=full(1e-40), p=full(p))
+                check(ge, x, u, t=full(1e38), p=full(p), m=full(0.5))
+
+
 def test_refusals(ge):
     dev = torch.device("cuda:0")
     x, u, _ = draw(dev, 3, 40, torch.float32, 1)
