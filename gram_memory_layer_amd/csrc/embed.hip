@@ -10,7 +10,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "internal.h"
+#include "lanes.h"
 
 namespace engram {
 namespace {
@@ -139,14 +139,14 @@ struct __attribute__((aligned(8))) Pair {
 
 // the wave's lanes that hold the same digit as this one
 __device__ __forceinline__ uint64_t same_digit(uint32_t digit) {
-    uint64_t mask = ~0ull;
+    uint64_t other = 0;
 #pragma unroll
     for (int b = 0; b < kMaxDigit; ++b) {
-        const bool set = (digit >> b) & 1;
-        const uint64_t vote = __ballot(set);
-        mask &= set ? vote : ~vote;
+        const uint64_t vote = __ballot((digit >> b) & 1);
+        const uint32_t own = (uint32_t)((int32_t)(digit << (31 - b)) >> 31);
+        other |= (uint64_t)((uint32_t)(vote >> 32) ^ own) << 32 | ((uint32_t)vote ^ own);
     }
-    return mask;
+    return ~other;
 }
 
 // Where each of the chunk's pairs goes, counting from its digit's first place:
@@ -195,12 +195,7 @@ __device__ __forceinline__ void scan_bins(uint32_t* value, int bins, uint32_t* w
         x[i] = b < bins ? value[b] : 0;
         sum += x[i];
     }
-    uint32_t upto = sum;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t y = __shfl_up(upto, o, 64);
-        if (lane >= o) upto += y;
-    }
+    const uint32_t upto = sum_upto(sum);
     if (lane == 63) wave_sum[wave] = upto;
     __syncthreads();
     uint32_t before = upto - sum;
