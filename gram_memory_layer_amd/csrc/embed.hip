@@ -7,6 +7,16 @@
 // The gradient's positions are sorted by id (stable, so a row's positions are
 // in order), and each row's sum is taken in fp32 in an order that the sizes
 // and the ids alone decide: the same on every run, and no atomics on values.
+//
+// All of it is bound by memory, or by the latencies of the launches where there is
+// little.  Measured: 4096 rows of 5120 to four streams 28 us, 185 MB, 6.5 TB/s (it writes
+// much more than it reads); the gradient of 4096 positions of four streams to 129,280
+// fp32 rows of 5120 428 us, of which 371 are the 2.65 GB of zeros and rows (7.1 TB/s) and 48
+// the sums (168 MB read, 5 TB/s with what they write); 32,768 positions of 2056, added to what is
+// there, 96-100 us: 24 the sort, 63 the sums (274 MB, 4.4 TB/s), 7-17 the rows that
+// reach over tiles; 98,304 positions of 64 47 us: 30 the sort, whose four launches on 48
+// workgroups are chains of latencies, 17 the sums, 4 the joining.  Elementary
+// torch operations (index_add_ in fp32): 186, 670, 610 and 61.
 #include <algorithm>
 #include <type_traits>
 
@@ -77,7 +87,8 @@ struct Eight<uint16_t> {
 };
 
 // ---------------------------------------------------------------- lookup
-// A thread eight values of a position: read once, stored for every stream.
+// A thread eight values of a position: read once, stored for every stream, past the
+// caches (what is written is larger than they are, or read by another kernel much later).
 template <class T, class O>
 __global__ void __launch_bounds__(256) embed_kernel(const T* __restrict__ table, int64_t rows,
                                                     int dim, const int32_t* __restrict__ ids,
@@ -123,7 +134,8 @@ hipError_t run_embed(const void* table, int64_t rows, int dim, const int32_t* id
 // ---------------------------------------------------------------- positions by id
 // Sorted pairs (key, position): a key is the id, or `rows` for a position that
 // adds nothing (a pad, a bad id); these come last.  A radix sort from the low
-// digit up, each pass stable.
+// digit up, each pass stable, in as few digits of at most 11 bits as the keys need
+// (two up to four million rows): a pass costs two launches, 11-17 us.
 constexpr int kChunk = 2048;        // positions a workgroup sorts
 constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / 64;
@@ -244,8 +256,8 @@ struct SortArgs {
 };
 
 // Up to kRankMost positions: a position's place is the number of pairs before it,
-// counted by a wave, the keys of all in LDS.  (A radix sort of 4096 in one
-// workgroup took 16 us.)
+// counted by a wave, the keys of all in LDS.  (4096 positions 11 us; a radix sort of
+// them in one workgroup took 16.)
 constexpr int kRankMost = 8192;
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) sort_rank_kernel(const SortArgs a,
@@ -426,8 +438,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(
 }
 
 // ---------------------------------------------------------------- sums
-// A tile is `tile` places of the sorted pairs; a thread takes eight columns of
-// one, adds the positions up in order and stores a row's sum where the row
+// A tile is `tile` places of the sorted pairs (equal work whatever the ids); a thread
+// takes eight columns of one, adds the positions up in order and stores a row's sum where the row
 // ends.  A row that reaches over the tile's ends leaves a part instead: in
 // part[t][0] where it began in an earlier tile, in part[t][1] where it begins
 // here and goes on; the latter tile is listed, and a second kernel adds the
@@ -473,17 +485,19 @@ __device__ __forceinline__ void put_part(float* to, const float (&sum)[8]) {
     *reinterpret_cast<f32x4*>(to + 4) = f32x4{sum[4], sum[5], sum[6], sum[7]};
 }
 
+// The tile's sums.  Where a row begins in it that goes on, one of its threads gives 1 (0
+// otherwise), or 2 where that reaches kMany tiles further; t, key: the tile, the row.
 template <class D, class W, int STREAMS, bool ONCE>
-__device__ __forceinline__ void sum_tile(const SumArgs<D, W>& a) {
+__device__ __forceinline__ int sum_tile(const SumArgs<D, W>& a, uint32_t& t, uint32_t& key) {
     const uint32_t per_row = (uint32_t)a.dim / 8;
     const uint32_t item = blockIdx.x * 256 + threadIdx.x;
-    const uint32_t t = item / per_row;
-    if (t >= a.tiles) return;
+    t = item / per_row;
+    if (t >= a.tiles) return 0;
     const int c = (int)(item - t * per_row) * 8;
     constexpr int BATCH = STREAMS == 1 ? kBatchOne : kBatch;
     const int streams = STREAMS ? STREAMS : a.streams;
     const int64_t start = (int64_t)t * a.tile;
-    uint32_t key = a.pair[start].key;
+    key = a.pair[start].key;
     bool begun = t == 0 || a.pair[start - 1].key != key;  // the row begins in this tile
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (int j0 = 0; j0 < a.tile; j0 += BATCH) {
@@ -548,16 +562,31 @@ __device__ __forceinline__ void sum_tile(const SumArgs<D, W>& a) {
         }
         key = k[BATCH];
     }
-    const uint32_t at_end = a.pair[start + a.tile - 1].key;
-    if (at_end == a.rows || a.pair[start + a.tile].key != at_end) return;
+    key = a.pair[start + a.tile - 1].key;
+    if (key == a.rows || a.pair[start + a.tile].key != key) return 0;
     put_part(a.part + ((int64_t)t * 2 + (begun ? 1 : 0)) * a.dim + c, sum);
-    if (begun && c == 0) {
-        const bool many = t + kMany < a.tiles && a.pair[start + (int64_t)kMany * a.tile].key == at_end;
-        uint32_t at = atomicAdd(a.owners + (many ? 1 : 0), 1u);
-        if (many) at = a.tiles - 1 - at;
-        a.owners[2 + 2 * at] = t;
-        a.owners[3 + 2 * at] = at_end;
-    }
+    if (!begun || c != 0) return 0;
+    return t + kMany < a.tiles && a.pair[start + (int64_t)kMany * a.tile].key == key ? 2 : 1;
+}
+
+// The workgroup's tiles into the lists, by one addition to each counter.  (One a tile: 429 us where
+// 786,432 positions of 64 columns fill 98,304 tiles, one a workgroup 158.)
+template <class D, class W>
+__device__ __forceinline__ void list_tiles(const SumArgs<D, W>& a, int kind, uint32_t t, uint32_t key) {
+    __shared__ uint32_t number[2], first[2];
+    const int tid = threadIdx.x;
+    if (tid < 2) number[tid] = 0;
+    if (!__syncthreads_or(kind)) return;
+    uint32_t at = 0;
+    if (kind) at = atomicAdd(&number[kind - 1], 1u);
+    __syncthreads();
+    if (tid < 2 && number[tid]) first[tid] = atomicAdd(a.owners + tid, number[tid]);
+    __syncthreads();
+    if (!kind) return;
+    at += first[kind - 1];
+    if (kind == 2) at = a.tiles - 1 - at;
+    a.owners[2 + 2 * at] = t;
+    a.owners[3 + 2 * at] = key;
 }
 
 // the first place in pair[lo, hi) whose key is at least k
@@ -715,9 +744,11 @@ __device__ __forceinline__ void fill_run(const Pair* pair, int64_t n, int64_t ro
 template <class D, class W, int STREAMS, bool ONCE>
 __global__ void __launch_bounds__(256) grad_sum_kernel(const SumArgs<D, W> a, uint32_t sum_blocks,
                                                        int64_t n, int64_t row0, int each) {
-    if (blockIdx.x < sum_blocks)
-        sum_tile<D, W, STREAMS, ONCE>(a);
-    else
+    if (blockIdx.x < sum_blocks) {
+        uint32_t t, key;
+        const int kind = sum_tile<D, W, STREAMS, ONCE>(a, t, key);
+        list_tiles(a, kind, t, key);
+    } else
         fill_run<W>(a.pair, n, a.rows, each, row0 + (int64_t)(blockIdx.x - sum_blocks) * each,
                     a.dim, a.dtable);
 }
@@ -731,7 +762,8 @@ __global__ void __launch_bounds__(THREADS) fill_kernel(const Fill zeros) {
 // where only rows that ids name are written (each = 0), 256 (row, eight columns) pairs.
 constexpr int kFewMost = 64;
 constexpr int64_t kMuchBytes = 256 << 20;  // zeros by small workgroups
-constexpr int64_t kFewBytes = 32 << 20;  // a gradient that one launch fills and sums
+constexpr int64_t kFewBytes = 64 << 20;    // a gradient that one launch fills and sums (32 positions, rows of 1024:
+                                           // 49 MB 11.2 us, by two launches 13.6; 82 MB 17.3 both; 164 MB 33 and 27)
 template <class D, class W>
 __global__ void __launch_bounds__(256) grad_few_kernel(
     const D* __restrict__ dout, const int32_t* __restrict__ ids, int n, int streams, int64_t rows,

@@ -10,6 +10,22 @@
 //
 // The sums of weights decide which tokens come out, so weights and sums are held
 // in 64 bits.
+//
+// Two kernels, none of which sorts.  The first reads the logits once, many
+// workgroups a row, and leaves per part of 2048 its largest logit and sum of
+// weights, and, for rows with a filter, per block of 8192 a histogram of its
+// weights (top-k: numbers) over buckets of the logits.  The second, a workgroup
+// a row, joins these: the cut of top-k or top-p lies in one bucket, and only what
+// may stay before it, or where that is much the bucket and the block that holds
+// the random number, is read again.
+//
+// Measured (129,280 logits a row): one row with top-k 50 and top-p 0.95 6.0 + 12.0
+// us, a chain of latencies; 64 fp32 rows with top-p 0.9 17.9 + 36 us, of the first one
+// half at the memory's rate would be 7 and the rest are the 64-bit exponentials and the
+// histogram, of the second the flat rows, 517 KB read by one compute unit; 512 bf16
+// rows without a filter 52-57 + 9 us, bound by the exponentials (22 instructions a logit, the
+// vector units busy 80% of the time; their bytes take 28).  Elementary torch
+// operations, with a sort in 64 bits: 350, 2100 and 3050 us.
 #include "lanes.h"
 #include "logits.h"
 
@@ -23,16 +39,22 @@ constexpr int kBlock = kBlockWaves * kPart;   // logits a workgroup
 constexpr int kBuckets = 512;                 // of 1/24 of exp's argument (of 1/8 where logits are only
                                               // counted), from a block's largest logit down;
 constexpr int kRest = kBuckets - 1;           // the last one takes all below, too
-constexpr int kXcds = 8;                      // workgroups go to these in turn: a row's all to one, so
-                                              // that its logits are in the cache of the last one's
+constexpr int kXcds = 8;                      // workgroups go to these in turn: a row's all to one, where
+                                              // its second kernel's workgroup finds them in the cache
 constexpr int kCopies = 4;                    // of the buckets in LDS: lanes that meet in one wait for each other
+                                              // (64 rows with top-p 0.5, and equal ones with min-p: 29 and 45
+                                              // us; one copy: 34 and 62)
 constexpr int kGroup = 4;                     // lanes whose largest logit is kept
 constexpr int kRowThreads = 512;
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kBinBits = 9, kBins = 1 << kBinBits;  // a thread each
 constexpr int kList = 8192;                   // candidates in LDS,
-constexpr int kManyBefore = 1024;
-constexpr int kSome = 64, kRanked = 256;       // that are ranked by counting, by a wave or all
+constexpr int kManyBefore = 1024;             // logits before the cut's bucket that are listed with it (64
+                                              // fp32 rows with top-p 0.5 and 0.9: 29 and 48 us; 64 of them:
+                                              // 41 and 48; as many as the list holds: 29 and 59)
+constexpr int kSome = 64, kRanked = 256;      // that are ranked by counting, by a wave or all (top-k 150:
+                                              // 27 us, found by narrowing down 36; one row with top-p
+                                              // 0.9: 18.7, ranked by all 20.2)
 constexpr int kHits = 16 * kRowThreads;       // groups of a row looked at together
 constexpr int kMostBlocks = 256;              // of a row whose buckets are joined
 
@@ -156,7 +178,10 @@ __device__ __forceinline__ float largest(float x) {
 
 // One wave a part, four of them a block.  Rows without a filter need a part's largest
 // logit and its sum of weights; rows with one also how much weight, or where that is
-// not asked for how many logits, lie in each bucket.
+// not asked for how many logits, lie in each bucket.  A wave's 2048 logits are all on
+// their way at once and stay in registers, as the weights need the block's largest first;
+// a block's histogram (fixed point, so that the order of the additions does not
+// matter) is small against its logits (4 KB a block of 16 or 32).
 template <class T, bool FILTERS>
 __global__ void __launch_bounds__(64 * kBlockWaves) sample_part_kernel(
     const T* __restrict__ logits, int64_t ld, const Request q, int64_t rows, int V, const Found out) {
@@ -588,7 +613,8 @@ struct Sampler {
     }
 
     // The same among a block's that stay.  Where these are few, their places in order
-    // first, so that few weights are taken.
+    // first, so that few weights are taken (one row, normal, top-p 0.5: 34.2 us, all
+    // weighed 35.4).
     template <class Stays>
     __device__ __forceinline__ void pick_listed(int block, double target, double total, Stays stays) const {
         constexpr int E = kPieces / kRowThreads;
@@ -1040,6 +1066,7 @@ struct Sampler {
                 sh.hit[at] = (uint16_t)(__builtin_ctz(hit) * kRowThreads + tid);
             __syncthreads();
             const int hits = sh.hits;
+            // (64 rows, normal, top-p 0.9: 51 us, by groups 56)
             if (g0 == 0 && 2 * hits > min(n_groups, kHits)) return in_turn(least, most);
             // where the row's ends or no group are a piece is all -infinity until its
             // logits are looked at one by one
@@ -1175,7 +1202,6 @@ struct Sampler {
         const double n_above = sh.found[1], here = sh.found[2];
         // The logits up to the cut's bucket, where the list holds them; without top-k those of
         // the bucket, as the blocks' buckets say what lies before it.
-        // (a long list takes longer than one bucket's and a block)
         const bool few_before = n_above + here <= (weights && last < kRest && here <= kList ? kManyBefore : kList);
         if (last < kRest) least = least_of(most - last);
         if (!few_before) {
@@ -1280,6 +1306,9 @@ struct Sampler {
     }
 };
 
+// A workgroup a row: of 36 us for 64 flat rows 14 go into reading a row's logits again, which
+// is what a compute unit takes in (37 GB/s a row; two batches of loads ahead: no
+// faster), 4 into the cut, 6 into the token's block, and 7 into joining the histograms.
 template <class T, bool FILTERS>
 __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(
     const T* __restrict__ logits, int64_t ld, const Request q, int V, const Found in,
@@ -1351,7 +1380,7 @@ hipError_t run_sample(const void* logits, int64_t ld, const Request& q, int64_t 
                       hipStream_t s) {
     Found f;
     layout(B, V, scratch, &f);
-    // (without any filter kernels that hold fewer registers)
+    // (without any filter kernels that hold fewer registers: 512 rows 59 -> 55 us)
     const bool filters = q.top_k || q.top_p || q.min_p;
     auto part = filters ? sample_part_kernel<T, true> : sample_part_kernel<T, false>;
     part<<<dim3((uint32_t)((B + kXcds - 1) / kXcds * kXcds * f.blocks)), dim3(64 * kBlockWaves), 0, s>>>(
