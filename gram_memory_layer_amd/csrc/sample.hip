@@ -412,9 +412,10 @@ struct Cut {
 // Logits and their weights in whole numbers of 2^-scale, so that they add up to the same
 // in any order.  Each: each(f) calls f(logit, index, units) for its logits above -infinity,
 // spread over the workgroup's threads; units() are the weight.
-// RUNS: neighbours are often equal.
-template <bool RUNS, class Each>
+// RUNS: neighbours are often equal.  T: what the logits were (bf16: half of a key says which).
+template <class T, bool RUNS, class Each>
 struct Narrow {
+    static constexpr int DROP = sizeof(T) == 2 ? 16 : 0;
     const Each& each;
     const Want& want;
     const float top;
@@ -484,13 +485,26 @@ struct Narrow {
             hi = min(hi, lo + ((1u << shift) - 1));
         }
     }
-    // The cut that keeps the first k of those that `in` keeps (k > 0), or those before
-    // which less than target (in units) lies; all of them lie in [least, most].
-    __device__ __forceinline__ Cut cut(const Cut in, int k, double target, float most, float least, int V) const {
-        uint32_t at = ~key_of(most), idx = 0;
+    // the index of the r-th of the logits with this key that `in` keeps
+    __device__ __forceinline__ uint32_t index_of(uint32_t key, const Cut in, uint64_t r, int V) const {
+        uint32_t idx = 0;
         uint64_t n, m, ties;
-        if (!find(at, ~max(in.key, key_of(least)), k == 0,
-                  [&](float x, int i) { return in.keeps(x, i) ? ~key_of(x) : ~0u; },
+        return find(idx, (uint32_t)V - 1, false,
+                    [&](float x, int i) { return key_of(x) == key && in.keeps(x, i) ? (uint32_t)i : ~0u; },
+                    [&](uint64_t a, uint64_t) { return a >= r; }, n, m, ties)
+                   ? idx
+                   : ~0u;
+    }
+    // The cut that keeps the first k of those that `in` keeps (k > 0), or those before
+    // which less than target (in units) lies; all of them lie in [least, most].  index:
+    // as index_of.
+    template <class Index>
+    __device__ __forceinline__ Cut cut(const Cut in, int k, double target, float most, float least, int V,
+                                       Index index) const {
+        uint32_t at = ~key_of(most) >> DROP;
+        uint64_t n, m, ties;
+        if (!find(at, ~max(in.key, key_of(least)) >> DROP, k == 0,
+                  [&](float x, int i) { return in.keeps(x, i) ? ~key_of(x) >> DROP : ~0u; },
                   [&](uint64_t a, uint64_t b) { return k ? a >= (uint64_t)k : (double)b >= target; },
                   n, m, ties)) {
             // all of them do not reach it (by a rounding, or there are fewer)
@@ -499,25 +513,21 @@ struct Narrow {
             return all;
         }
         Cut out;
-        out.key = ~at;
+        out.key = ~(at << DROP);
+        if (DROP && (out.key & 0x80000000u)) out.key &= ~0xFFFFu;  // (the lower half is clear from zero on)
         out.idx = in.key == out.key ? in.idx : ~0u;
         // how many of the equal ones at the cut stay, and the last of these
         double stay = (double)k - (double)n;
         if (k == 0) stay = ceil((target - (double)m) / (want.weigh(value_of(out.key), top) / unit));
         const uint64_t r = stay < 1.0 ? 1 : stay > 0x1p31 ? (uint64_t)1 << 31 : (uint64_t)stay;
-        if (r < ties && find(idx, (uint32_t)V - 1, false,
-                             [&](float x, int i) {
-                                 return key_of(x) == out.key && in.keeps(x, i) ? (uint32_t)i : ~0u;
-                             },
-                             [&](uint64_t a, uint64_t) { return a >= r; }, n, m, ties))
-            out.idx = idx;
+        if (r < ties) out.idx = index(out.key, in, r);
         return out;
     }
 };
-template <bool RUNS, class Each>
-__device__ __forceinline__ Narrow<RUNS, Each> narrow(const Each& each, const Want& want, float top, int scale,
-                                               Shared& sh) {
-    return Narrow<RUNS, Each>{each, want, top, ldexp(1.0, -scale), sh};
+template <class T, bool RUNS, class Each>
+__device__ __forceinline__ Narrow<T, RUNS, Each> narrow(const Each& each, const Want& want, float top, int scale,
+                                                        Shared& sh) {
+    return Narrow<T, RUNS, Each>{each, want, top, ldexp(1.0, -scale), sh};
 }
 // a weight in whole numbers of 2^-scale, magic = 2^(52 - scale)
 __device__ __forceinline__ uint64_t units_of(double w, double magic) {
@@ -612,26 +622,25 @@ struct Sampler {
         choose(w, begin, target, total);
     }
 
-    // The same among a block's that stay.  Where these are few, their places in order
-    // first, so that few weights are taken (one row, normal, top-p 0.5: 34.2 us, all
-    // weighed 35.4).
+    // A block's logits that stay: 16 neighbours x a thread, a bit each; their places in
+    // order into the list, where they are at most `most`; how many there are.
+    static constexpr int NEAR = kPieces / kRowThreads;
     template <class Stays>
-    __device__ __forceinline__ void pick_listed(int block, double target, double total, Stays stays) const {
-        constexpr int E = kPieces / kRowThreads;
-        const int tid = threadIdx.x, begin = block * kPieces + tid * E;
-        uint4 raw[E];
+    __device__ __forceinline__ int list_block(int block, int most, float (&x)[NEAR][VEC], uint32_t& stay,
+                                              Stays stays) const {
+        const int tid = threadIdx.x, begin = block * kPieces + tid * NEAR;
+        uint4 raw[NEAR];
 #pragma unroll
-        for (int j = 0; j < E; ++j) raw[j] = r.fetch(begin + j, V);
-        float x[E][VEC];
-        uint32_t found = 0;
+        for (int j = 0; j < NEAR; ++j) raw[j] = r.fetch(begin + j, V);
+        stay = 0;
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
+        for (int j = 0; j < NEAR; ++j) {
             r.unpack(raw[j], begin + j, V, x[j]);
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
-                if (x[j][e] > -INFINITY && stays(x[j][e], (int)r.column(begin + j) + e)) found |= 1u << (j * VEC + e);
+                if (x[j][e] > -INFINITY && stays(x[j][e], (int)r.column(begin + j) + e)) stay |= 1u << (j * VEC + e);
         }
-        const int own = __builtin_popcount(found), upto = (int)sum_upto((uint32_t)own);
+        const int own = __builtin_popcount(stay), upto = (int)sum_upto((uint32_t)own);
         if ((tid & 63) == 63) sh.at[tid >> 6] = upto;
         __syncthreads();
         int at = upto - own, n = 0;
@@ -640,20 +649,34 @@ struct Sampler {
             at += w < (tid >> 6) ? sh.at[w] : 0;
             n += sh.at[w];
         }
+        if (n > most) return n;
+        for (uint32_t left = stay; left; left &= left - 1, ++at)
+            sh.list[at] = (int)r.column(begin) + __builtin_ctz(left);
+        __syncthreads();
+        return n;
+    }
+
+    // The same among a block's that stay.  Where these are few, their places in order
+    // first, so that few weights are taken (one row, normal, top-p 0.5: 34.2 us, all
+    // weighed 35.4).
+    template <class Stays>
+    __device__ __forceinline__ void pick_listed(int block, double target, double total, Stays stays) const {
         constexpr int FEW = 4;  // a thread
+        const int tid = threadIdx.x;
+        float x[NEAR][VEC];
+        uint32_t stay;
+        const int n = list_block(block, FEW * kRowThreads, x, stay, stays);
         if (n > FEW * kRowThreads) {
-            double w[E][VEC];
+            double w[NEAR][VEC];
 #pragma unroll
-            for (int j = 0; j < E; ++j)
+            for (int j = 0; j < NEAR; ++j)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     w[j][e] = want.weigh(x[j][e], top);
-                    if (!(found >> (j * VEC + e) & 1) || !(w[j][e] > kNoWeight)) w[j][e] = 0.0;
+                    if (!(stay >> (j * VEC + e) & 1) || !(w[j][e] > kNoWeight)) w[j][e] = 0.0;
                 }
-            return choose(w, begin, target, total);
+            return choose(w, block * kPieces + tid * NEAR, target, total);
         }
-        for (; found; found &= found - 1, ++at) sh.list[at] = (int)r.column(begin) + __builtin_ctz(found);
-        __syncthreads();
         const int each = (n + kRowThreads - 1) / kRowThreads, from = tid * each, to = min(from + each, n);
         int places[FEW];
         double w[FEW], own_sum = 0.0, here;
@@ -685,11 +708,10 @@ struct Sampler {
         emit(token_at, log(w_token / total));
     }
 
-    // The weights of the row's logits that stay, summed by block, a wave each in turn, and
-    // their sum; own: what the thread's blocks [from, to) hold, the sum before it is returned.
-    template <class Stays>
-    __device__ __forceinline__ double weigh_blocks(Stays stays, int& from, int& to, double& own,
-                                                   double& total) const {
+    // Numbers of the row's logits summed by block, a wave each in turn; total: all of them.
+    // The block that holds the share-th part of it (at >= 0: that holds `at`), and what lies before.
+    template <class Of>
+    __device__ __forceinline__ int sum_blocks(Of of, double share, double at, double& before, double& total) const {
         constexpr int AT = 4;
         const int tid = threadIdx.x, lane = tid & 63, blocks = (pieces + kPieces - 1) / kPieces;
         double* by = reinterpret_cast<double*>(sh.mass);
@@ -705,35 +727,20 @@ struct Sampler {
                     float x[VEC];
                     r.unpack(raw[j], i0 + 64 * j, V, x);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        if (!(x[e] > -INFINITY && stays(x[e], (int)r.column(i0 + 64 * j) + e))) continue;
-                        const double w = want.weigh(x[e], top);
-                        s += w > kNoWeight ? w : 0.0;
-                    }
+                    for (int e = 0; e < VEC; ++e)
+                        if (x[e] > -INFINITY) s += of(x[e], (int)r.column(i0 + 64 * j) + e);
                 }
             }
             s = last_lane(sum_upto(s));
             if (lane == 0) by[g] = s;
         }
         __syncthreads();
-        const int each = (blocks + kRowThreads - 1) / kRowThreads;
-        from = tid * each;
-        to = min(from + each, blocks);
-        own = 0.0;
+        const int each = (blocks + kRowThreads - 1) / kRowThreads, from = tid * each, to = min(from + each, blocks);
+        double own = 0.0;
         for (int g = from; g < to; ++g) own += by[g];
-        return scan(own, sh, &total);
-    }
-
-    // The token among the row's logits that stay: the first whose sum exceeds u times the
-    // sum of all.
-    template <class Stays>
-    __device__ __forceinline__ void pick(Stays stays) const {
-        const double* by = reinterpret_cast<const double*>(sh.mass);
-        int from, to;
-        double own, total;
-        double sum = weigh_blocks(stays, from, to, own, total);
-        const double target = want.u * total;
-        if ((int)threadIdx.x == holder(sum, own, target, sh)) {
+        double sum = scan(own, sh, &total);
+        const double target = at >= 0.0 ? at : share * total;
+        if (tid == holder(sum, own, target, sh)) {
             for (int g = from; g < to; ++g) {
                 if (!(by[g] > 0.0)) continue;
                 sh.found[0] = sum;
@@ -743,7 +750,26 @@ struct Sampler {
             }
         }
         __syncthreads();
-        pick_listed(sh.hits, target - sh.found[0], total, stays);
+        before = sh.found[0];
+        return sh.hits;
+    }
+    // (for it: the weight of a logit that stays)
+    template <class Stays>
+    __device__ __forceinline__ auto weight_of(Stays stays) const {
+        return [=, this](float x, int i) {
+            if (!stays(x, i)) return 0.0;
+            const double w = want.weigh(x, top);
+            return w > kNoWeight ? w : 0.0;
+        };
+    }
+
+    // The token among the row's logits that stay: the first whose sum exceeds u times the
+    // sum of all.
+    template <class Stays>
+    __device__ __forceinline__ void pick(Stays stays) const {
+        double before, total;
+        const int block = sum_blocks(weight_of(stays), want.u, -1.0, before, total);
+        pick_listed(block, want.u * total - before, total, stays);
     }
 
     // the first of the largest: its part, then its place
@@ -795,49 +821,68 @@ struct Sampler {
         pick_near(sh.hits, target - sh.found[0], total);
     }
 
-    // Any filters on any row, by passes over it.  The first cut lies in [least, over), with
-    // `above` (logits for top-k, else weight) before these.
+    // Any filters on any row, by passes over it: the cut's key, the last of the equal ones, and
+    // the weights by block.  The first cut lies in [least, over), with `above` (logits for
+    // top-k, else weight) before these.  (64 rows: bf16 with top-p 0.9 at temperature 2 202
+    // us, narrowing by whole keys and indices 362; equal fp32 ones 225 and 289.)
     __device__ __forceinline__ void by_passes(double total, float least, float over, double above) const {
         const int scale = min(50, 30 + __builtin_clz(V));
         const double magic = ldexp(1.0, 52 - scale);
-        uint32_t lo = ~0u, hi = 0;
-        every([&](float x, int) {
-            if (x < least || x >= over) return;
-            lo = min(lo, key_of(x));
-            hi = max(hi, key_of(x));
-        });
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            sh.range[0] = ~0u;
-            sh.range[1] = 0;
+        float most = fminf(below(over), top);
+        if constexpr (sizeof(T) == 4) {  // (bf16 has few keys: a pass less, or none more)
+            uint32_t lo = ~0u, hi = 0;
+            every([&](float x, int) {
+                if (x < least || x >= over) return;
+                lo = min(lo, key_of(x));
+                hi = max(hi, key_of(x));
+            });
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                sh.range[0] = ~0u;
+                sh.range[1] = 0;
+            }
+            __syncthreads();
+            atomicMin(&sh.range[0], lo);
+            atomicMax(&sh.range[1], hi);
+            __syncthreads();
+            least = value_of(sh.range[0]);
+            most = value_of(sh.range[1]);
         }
-        __syncthreads();
-        atomicMin(&sh.range[0], lo);
-        atomicMax(&sh.range[1], hi);
-        __syncthreads();
-        least = value_of(sh.range[0]);
-        float most = value_of(sh.range[1]);
         auto each = [&](auto f) {
             every([&](float x, int i) {
                 if (x >= least && x <= most) f(x, i, [&] { return units_of(want.weigh(x, top), magic); });
             });
         };
-        const auto row = narrow<true>(each, want, top, scale, sh);
+        const auto row = narrow<T, true>(each, want, top, scale, sh);
         Cut keep;
         for (int again = 0; again < 2; ++again) {  // top-k, then top-p
             if (again ? want.p == 1.0 : want.k == 0) continue;
             if (again && want.k) {
-                int from, to;
-                double own;
-                weigh_blocks([&](float x, int i) { return keep.keeps(x, i); }, from, to, own, total);
+                double before;
+                sum_blocks(weight_of([=](float x, int i) { return keep.keeps(x, i); }), 0.0, -1.0, before, total);
                 above = 0.0;
                 least = value_of(keep.key);
                 most = top;
             }
             keep = row.cut(keep, again ? 0 : want.k - (int)above, again ? (want.p * total - above) / row.unit : 0.0,
-                           most, least, V);
+                           most, least, V, [&](uint32_t key, const Cut in, uint64_t number) {
+                               const float v = value_of(key);  // by blocks: the one that holds it, then there
+                               auto equal = [=](float x, int i) {
+                                   return x == v && (in.key < key || (uint32_t)i <= in.idx);
+                               };
+                               double before, ties;
+                               const int block = sum_blocks([=](float x, int i) { return equal(x, i) ? 1.0 : 0.0; },
+                                                            0.0, (double)number - 0.5, before, ties);
+                               float x[NEAR][VEC];
+                               uint32_t stay;
+                               list_block(block, kList, x, stay, equal);
+                               const uint32_t idx = (uint32_t)sh.list[(int)((double)number - before) - 1];
+                               __syncthreads();  // (before the list is written again)
+                               return idx;
+                           });
         }
-        pick([&](float x, int i) { return keep.keeps(x, i) && x >= floor; });
+        const float lowest = floor;
+        pick([=](float x, int i) { return keep.keeps(x, i) && x >= lowest; });
     }
 
     // Up to 64 candidates, the first of the order, in LDS: one wave, a candidate a lane.
@@ -1242,19 +1287,20 @@ struct Sampler {
             for (int j = 0; j < E; ++j)
                 if (tid + j * kRowThreads < listed) f(x[j], idx[j], [&] { return w[j]; });
         };
-        const auto list = narrow<false>(each, want, top, 50, sh);
+        const auto list = narrow<T, false>(each, want, top, 50, sh);
         auto sum_of = [&](auto stays) {
             uint64_t sum = 0;
             each([&](float v, int i, auto units) { sum += stays(v, i, units()) ? units() : 0; });
             return (double)total_of(sum, sh);
         };
+        auto index = [&](uint32_t key, const Cut in, uint64_t number) { return list.index_of(key, in, number, V); };
         Cut keep;
         double target = (want.p * total - above) / list.unit;
         if (want.k) {
-            keep = list.cut(keep, want.k, 0.0, top, least, V);
+            keep = list.cut(keep, want.k, 0.0, top, least, V, index);
             if (want.p < 1.0) target = want.p * sum_of([&](float v, int i, uint64_t) { return keep.keeps(v, i); });
         }
-        if (want.p < 1.0 && (few_before || cut_here)) keep = list.cut(keep, 0, target, fminf(over, top), least, V);
+        if (want.p < 1.0 && (few_before || cut_here)) keep = list.cut(keep, 0, target, fminf(over, top), least, V, index);
         if (few_before) {
             auto stays = [&](float v, int i) {
                 return keep.keeps(v, i) && v >= floor && want.weigh(v, top) > kNoWeight;
