@@ -1020,23 +1020,20 @@ struct Sampler {
         for (; found; found &= found - 1, ++at)
             if (at < kList) sh.list[at] = place_of(__builtin_ctz(found));
     }
-    // the logits above low and not above high, a bit each: a difference's sign (four
-    // instructions a logit; two comparisons, joined, and a bit take ten issue slots)
-    __device__ __forceinline__ uint32_t found_in(const uint4 (&raw)[AT], float low, float high) const {
-        uint32_t found = 0;
+    // A piece's logits above low and not above high, a bit each below found's: a
+    // difference's sign (four instructions a logit).
+    __device__ __forceinline__ uint32_t found_in(uint32_t found, const uint4& raw, float low, float high) const {
+        float v[VEC];
+        r.values(raw, v);
+        if (low == -INFINITY) {  // (a difference would be none)
+            found <<= VEC;
 #pragma unroll
-        for (int j = AT - 1; j >= 0; --j) {
-            float v[VEC];
-            r.values(raw[j], v);
-            if (low == -INFINITY) {  // (a difference would be none)
+            for (int e = 0; e < VEC; ++e) found |= v[e] > low && v[e] <= high ? 1u << e : 0u;
+        } else {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) found |= v[e] > low && v[e] <= high ? 1u << (j * VEC + e) : 0u;
-            } else {
-#pragma unroll
-                for (int e = VEC - 1; e >= 0; --e)
-                    found = __builtin_amdgcn_alignbit(
-                        found, __float_as_uint(low - v[e]) ^ __float_as_uint(high - v[e]), 31);
-            }
+            for (int e = VEC - 1; e >= 0; --e)
+                found = __builtin_amdgcn_alignbit(
+                    found, __float_as_uint(low - v[e]) ^ __float_as_uint(high - v[e]), 31);
         }
         return found;
     }
@@ -1059,21 +1056,22 @@ struct Sampler {
             }
         }
         const float low = below(least), high = below(most);
-        uint4 raw[AT], next[AT];
-        auto fetch = [&](int i0) {
-#pragma unroll
-            for (int j = 0; j < AT; ++j) {
-                const int i = min(i0 + j * kRowThreads, end - 1);
-                next[j] = *reinterpret_cast<const uint4*>(r.src + (i * VEC - r.before));
-            }
+        const char* const base = reinterpret_cast<const char*>(r.src - r.before);
+        auto piece = [&](int i) {
+            return *reinterpret_cast<const uint4*>(base + (uint32_t)min(i, end - 1) * 16u);
         };
         if (end > begin) {
-            fetch(begin + tid);
-            for (int i0 = begin + tid; __any(i0 < end); i0 += AT * kRowThreads) {
+            uint4 raw[AT];
 #pragma unroll
-                for (int j = 0; j < AT; ++j) raw[j] = next[j];
-                fetch(i0 + AT * kRowThreads);
-                uint32_t found = found_in(raw, low, high);
+            for (int j = 0; j < AT; ++j) raw[j] = piece(begin + tid + j * kRowThreads);
+            for (int i0 = begin + tid; __any(i0 < end); i0 += AT * kRowThreads) {
+                uint32_t found = 0;
+#pragma unroll
+                for (int j = AT - 1; j >= 0; --j) {  // (a load after each piece: eight at once hold the waves up)
+                    found = found_in(found, raw[j], low, high);
+                    raw[j] = piece(i0 + (AT + j) * kRowThreads);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
                 const int there = i0 < end ? (end - i0 + kRowThreads - 1) / kRowThreads : 0;
                 if (there < AT) found &= (1u << there * VEC) - 1;
                 list(found, [&](int bit) {
@@ -1131,7 +1129,9 @@ struct Sampler {
                             part |= 1u << j;
                     }
                 }
-                uint32_t found = found_in(raw, low, high);
+                uint32_t found = 0;
+#pragma unroll
+                for (int j = AT - 1; j >= 0; --j) found = found_in(found, raw[j], low, high);
                 while (part) {
                     const int j = __builtin_ctz(part);
                     const int col = ((g0 + sh.hit[h0 + j * HOP]) * kGroup + lane) * VEC - r.before;
