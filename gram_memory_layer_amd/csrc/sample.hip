@@ -20,9 +20,9 @@
 // the random number, is read again.
 //
 // Measured (129,280 logits a row): one row with top-k 50 and top-p 0.95 6.0 + 12.0
-// us, a chain of latencies; 64 fp32 rows with top-p 0.9 17.9 + 36 us, of the first one
-// half at the memory's rate would be 7 and the rest are the 64-bit exponentials and the
-// histogram, of the second the flat rows, 517 KB read by one compute unit; 512 bf16
+// us, a chain of latencies; 64 fp32 rows with top-p 0.9 17.1 + 35 us, the first one bound
+// by the 64-bit exponentials and the histogram (its bytes take 7), the second one by
+// the flat rows, whose 517 KB one compute unit reads; 512 bf16
 // rows without a filter 52-57 + 9 us, bound by the exponentials (22 instructions a logit, the
 // vector units busy 80% of the time; their bytes take 28).  Elementary torch
 // operations, with a sort in 64 bits: 350, 2100 and 3050 us.
@@ -1352,9 +1352,8 @@ struct Sampler {
     }
 };
 
-// A workgroup a row: of 36 us for 64 flat rows 14 go into reading a row's logits again, which
-// is what a compute unit takes in (37 GB/s a row; two batches of loads ahead: no
-// faster), 4 into the cut, 6 into the token's block, and 7 into joining the histograms.
+// A workgroup a row: of 35 us for 64 flat rows 12 go into reading a row's logits again, 4 into the
+// cut, 6 into the token's block, and 7 into joining the histograms.
 template <class T, bool FILTERS>
 __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(
     const T* __restrict__ logits, int64_t ld, const Request q, int V, const Found in,

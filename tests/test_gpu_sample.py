@@ -379,6 +379,29 @@ def test_cuts_at_zeros_subnormals_and_the_ends_of_the_range(ge):
                 check(ge, x, u, t=full(1e38), p=full(p), m=full(0.5))
 
 
+@pytest.mark.parametrize("dtype", KINDS)
+@pytest.mark.parametrize("values", [(1.0, 1.0078125, 0.99609375), (-2.0, -2.015625, -1.9921875), (0.0, -0.0, 2.0 ** -126)])
+def test_more_logits_at_the_cut_than_the_list_holds(ge, dtype, values):
+    """A few values, each many times: cuts among equal ones, top-p's among those that top-k cut."""
+    dev = torch.device("cuda:0")
+    for V in (30011, 129280):
+        say("sample many equal", V, dtype, values)
+        g = torch.Generator(device=dev)
+        g.manual_seed(V)
+        x = torch.tensor(values, device=dev)[torch.randint(0, 3, (4, V), generator=g, device=dev)].to(KINDS[dtype])
+        x[1, ::5] = -INF
+        x[2, ::7] = -5.0
+        u = torch.rand(4, generator=g, device=dev)
+        full = lambda v, kind=torch.float32: torch.full((4,), v, dtype=kind, device=dev)  # noqa: E731
+        for p in (0.2, 0.5, 0.97):
+            check(ge, x, u, p=full(p))
+            check(ge, x, u, t=full(3.0), p=full(p), m=full(0.2))
+        for k in (8193, 12345, V // 2, V - 5):
+            check(ge, x, u, k=full(k, torch.int32))
+            for p in (0.3, 0.9, 0.9999):
+                check(ge, x, u, k=full(k, torch.int32), p=full(p))
+
+
 def test_refusals(ge):
     dev = torch.device("cuda:0")
     x, u, _ = draw(dev, 3, 40, torch.float32, 1)
