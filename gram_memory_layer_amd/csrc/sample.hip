@@ -23,7 +23,7 @@
 // us, a chain of latencies; 64 fp32 rows with top-p 0.9 17.1 + 35 us, the first one bound
 // by the 64-bit exponentials and the histogram (its bytes take 7), the second one by
 // the flat rows, whose 517 KB one compute unit reads; 512 bf16
-// rows without a filter 52-57 + 9 us, bound by the exponentials (22 instructions a logit, the
+// rows without a filter 54 + 9 us, bound by the exponentials (21 instructions a logit, the
 // vector units busy 80% of the time; their bytes take 28).  Elementary torch
 // operations, with a sort in 64 bits: 350, 2100 and 3050 us.
 #include "lanes.h"
@@ -217,23 +217,45 @@ __global__ void __launch_bounds__(64 * kBlockWaves) sample_part_kernel(
     }
     const Want want(q, row, V);
     float own[NL], top = -INFINITY, low = INFINITY;
-    bool bad = false;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
         own[i] = v[i][0];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            bad |= !(v[i][e] < INFINITY);
             own[i] = fmaxf(own[i], v[i][e]);
             low = fminf(low, v[i][e]);
         }
         top = fmaxf(top, own[i]);
     }
     top = largest(top);
+    const bool filtered = FILTERS && want.filtered();
+    auto sum_all = [&] {
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s += weight((double)v[i][e] - (double)top, want.c);
+        return s;
+    };
+    if constexpr (!FILTERS) {
+        // (no logit weighs nothing; a NaN, which neither bound shows, makes the sum one)
+        if (want.whole_sum() && fabsf(top) < INFINITY && __all((double)low - (double)top >= want.least)) {
+            const double s = last_lane(sum_upto(sum_all()));
+            if (lane == 0) {
+                out.tops[row * out.blocks * kBlockWaves + part] = s == s ? top : (float)s;
+                out.sums[row * out.blocks * kBlockWaves + part] = s;
+            }
+            return;
+        }
+    }
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) bad |= !(v[i][e] < INFINITY);
     bad = __any(bad);
     if (lane == 0)
         out.tops[row * out.blocks * kBlockWaves + part] = bad ? __uint_as_float(0x7FC00000u) : top;
-    const bool filtered = FILTERS && want.filtered();
     if (filtered) {
         for (int b = tid; b < kBuckets * kCopies; b += NT) bucket[b] = 0;
         if (lane == 0) wave_top[wave] = top;
@@ -245,11 +267,8 @@ __global__ void __launch_bounds__(64 * kBlockWaves) sample_part_kernel(
     double s = 0.0;
     if (!filtered) {
         if (!want.whole_sum() || bad) return;
-        if (__all(((double)low - (double)top) >= want.least)) {
-#pragma unroll
-            for (int i = 0; i < NL; ++i)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) s += weight((double)v[i][e] - (double)top, want.c);
+        if (FILTERS && __all((double)low - (double)top >= want.least)) {
+            s = sum_all();
         } else {
 #pragma unroll
             for (int i = 0; i < NL; ++i)

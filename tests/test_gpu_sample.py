@@ -215,6 +215,25 @@ def test_masked_logits_and_bad_values(ge, dtype):
     check(ge, x, u, k=full(9, torch.int32), p=full(0.5), bits=ge.ERRBIT_LOGIT)
 
 
+@pytest.mark.parametrize("dtype", KINDS)
+def test_bad_values_anywhere_without_a_filter(ge, dtype):
+    dev = torch.device("cuda:0")
+    V = 20000
+    places = (0, 5, 1023, 2048, 3001, 8191, 8192, 12345, 16384, V - 1)
+    for bad in (float("nan"), -float("nan"), INF):
+        say("sample bad value", bad, dtype)
+        x, u, _ = draw(dev, len(places) + 1, V, KINDS[dtype], 8)
+        for b, v in enumerate(places):
+            x[b, v] = bad
+        check(ge, x, u, bits=ge.ERRBIT_LOGIT)
+        check(ge, x, u, t=torch.full((len(places) + 1,), 0.7, device=dev), bits=ge.ERRBIT_LOGIT)
+    x, u, _ = draw(dev, len(places), V, KINDS[dtype], 9)
+    for b, v in enumerate(places):
+        x[b, v] = -INF
+        x[b, (v + 4000) % V] = torch.finfo(KINDS[dtype]).min
+    check(ge, x, u)
+
+
 def test_parameters_out_of_range(ge):
     dev = torch.device("cuda:0")
     say("sample parameters")
