@@ -3,6 +3,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <initializer_list>
+
 #include "internal.h"
 
 namespace engram {
@@ -616,10 +618,17 @@ engram_status engram_beam_reorder(void* const* states, const int64_t* row_bytes,
 
 // ---------------------------------------------------------------- the vocabulary's two ends
 
-// whether out, which a call writes, reaches into what it reads at `in`
-static bool overlap(const void* out, int64_t out_bytes, const void* in, int64_t in_bytes) {
-    const char *a = (const char*)out, *b = (const char*)in;
-    return a < b + in_bytes && b < a + out_bytes;
+// What a call reads or writes (at null: nothing), and whether one reaches into others
+struct Span {
+    const void* at;
+    int64_t bytes;
+};
+static bool overlap(const Span& a, std::initializer_list<Span> others) {
+    for (const Span& b : others)
+        if (a.at && b.at && (const char*)a.at < (const char*)b.at + b.bytes &&
+            (const char*)b.at < (const char*)a.at + a.bytes)
+            return true;
+    return false;
 }
 
 // the sizes of a lookup and its gradient: 0, or the status that refuses them
@@ -641,9 +650,9 @@ engram_status engram_embed(const void* table, int32_t table_f32, int64_t rows, i
     if (!table || !ids || !out) return ENGRAM_ERR_INVALID_ARG;
     if (!aligned16(table) || !aligned16(out) || ((uintptr_t)ids & 3u) != 0)
         return ENGRAM_ERR_INVALID_ARG;
-    const int64_t out_bytes = n * streams * dim * (out_f32 ? 4 : 2);
-    if (overlap(out, out_bytes, table, rows * dim * (table_f32 ? 4 : 2)) ||
-        overlap(out, out_bytes, ids, n * 4))
+    const Span to{out, n * streams * dim * (out_f32 ? 4 : 2)}, from{ids, n * 4},
+        read{table, rows * dim * (table_f32 ? 4 : 2)};
+    if (overlap(to, {read, from}) || overlap(Span{err, 4}, {read, from, to}))
         return ENGRAM_ERR_INVALID_ARG;
     return from_hip(engram::launch_embed(table, table_f32 != 0, rows, dim, ids, n, scale, streams,
                                          out, out_f32 != 0, err, (hipStream_t)stream));
@@ -672,12 +681,13 @@ engram_status engram_embed_grad(const void* dout, int32_t dout_f32, const int32_
     if (n > 0) {
         if (!dout || !ids || !aligned16(dout) || ((uintptr_t)ids & 3u) != 0)
             return ENGRAM_ERR_INVALID_ARG;
-        if (scratch == nullptr || scratch_bytes < engram_embed_grad_scratch_size(n, rows, dim) ||
-            ((uintptr_t)scratch & 255u) != 0)
+        const size_t need = engram_embed_grad_scratch_size(n, rows, dim);
+        if (scratch == nullptr || scratch_bytes < need || ((uintptr_t)scratch & 255u) != 0)
             return ENGRAM_ERR_WORKSPACE;
-        const int64_t bytes = rows * dim * (dtable_f32 ? 4 : 2);
-        if (overlap(dtable, bytes, dout, n * streams * dim * (dout_f32 ? 4 : 2)) ||
-            overlap(dtable, bytes, ids, n * 4))
+        const Span to{dtable, rows * dim * (dtable_f32 ? 4 : 2)}, from{ids, n * 4},
+            read{dout, n * streams * dim * (dout_f32 ? 4 : 2)}, kept{scratch, (int64_t)need};
+        if (overlap(to, {read, from}) || overlap(kept, {read, from, to}) ||
+            overlap(Span{err, 4}, {read, from, to, kept}))
             return ENGRAM_ERR_INVALID_ARG;
     }
     return from_hip(engram::launch_embed_grad(dout, dout_f32 != 0, ids, n, streams, rows, dim,
@@ -712,19 +722,17 @@ engram_status engram_sample(const void* logits, int32_t logits_f32, int64_t ld, 
         (((uintptr_t)u | (uintptr_t)temperature | (uintptr_t)top_k | (uintptr_t)top_p |
           (uintptr_t)min_p | (uintptr_t)tokens | (uintptr_t)logprobs) & 3u) != 0)
         return ENGRAM_ERR_INVALID_ARG;
-    if (scratch == nullptr || scratch_bytes < engram_sample_scratch_size(B, V) ||
-        ((uintptr_t)scratch & 255u) != 0)
+    const size_t need = engram_sample_scratch_size(B, V);
+    if (scratch == nullptr || scratch_bytes < need || ((uintptr_t)scratch & 255u) != 0)
         return ENGRAM_ERR_WORKSPACE;
-    const int64_t bytes = (int64_t)B * 4;  // rows are read while others' tokens are written
-    for (const void* out : {(const void*)tokens, (const void*)logprobs}) {
-        if (out == nullptr) continue;
-        for (const void* in : {(const void*)u, (const void*)temperature, (const void*)top_k,
-                               (const void*)top_p, (const void*)min_p})
-            if (in != nullptr && overlap(out, bytes, in, bytes)) return ENGRAM_ERR_INVALID_ARG;
-        if (overlap(out, bytes, logits, ((B - 1) * ld + V) * (logits_f32 ? 4 : 2)))
-            return ENGRAM_ERR_INVALID_ARG;
-    }
-    if (logprobs && overlap(logprobs, bytes, tokens, bytes)) return ENGRAM_ERR_INVALID_ARG;
+    const int64_t each = (int64_t)B * 4;  // rows are read while others' tokens are written
+    const Span read{logits, ((B - 1) * ld + V) * (logits_f32 ? 4 : 2)}, a{u, each}, b{temperature, each},
+        c{top_k, each}, d{top_p, each}, e{min_p, each}, to{tokens, each}, lp{logprobs, each},
+        kept{scratch, (int64_t)need};
+    if (overlap(to, {read, a, b, c, d, e}) || overlap(lp, {read, a, b, c, d, e, to}) ||
+        overlap(kept, {read, a, b, c, d, e, to, lp}) ||
+        overlap(Span{err, 4}, {read, a, b, c, d, e, to, lp, kept}))
+        return ENGRAM_ERR_INVALID_ARG;
     return from_hip(engram::launch_sample(logits, logits_f32 != 0, ld, u, temperature, top_k,
                                           top_p, min_p, B, V, tokens, logprobs, scratch, err,
                                           (hipStream_t)stream));

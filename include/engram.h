@@ -415,7 +415,8 @@ engram_status engram_beam_reorder(void* const* states, const int64_t* row_bytes,
  * the layer's streams, and the rows' gradient.  As above, the pages do not describe
  * these calls, and a scratch argument may be reused by the next call on the same
  * stream and by captured graphs that are replayed one after the other.  Outputs
- * that overlap what a call reads are refused (ENGRAM_ERR_INVALID_ARG). */
+ * (err is one) and scratch that overlap each other or what a call reads are
+ * refused (ENGRAM_ERR_INVALID_ARG). */
 
 /* The next token of every row of logits from a given random number.  With x the
  * row and

@@ -114,3 +114,47 @@ def test_outputs_that_overlap_inputs_are_refused():
             if name != out:
                 assert sample(**{out: places[name] + 8}) == 1 and sample(**{out: places[name] - 8}) == 1, (out, name)
         assert sample(**{out: at[0] + 2 * 2900 - 4}) == 1 and sample(**{out: at[0] - 8}) == 1, out
+
+
+def test_scratch_that_overlaps_anything_is_refused():
+    """Scratch is written and read by every launch of a call, err by some; each call here has one overlap, of
+    its first or its last bytes."""
+    lib = ge.load()
+    at = [(i + 1) << 34 for i in range(10)]
+    n, rows, dim, streams = 100, 1000, 64, 2
+    need = ge.engram_embed_grad_scratch_size(n, rows, dim)
+    held = {"dout": n * streams * dim * 2, "ids": n * 4, "dt": rows * dim * 4}
+    places = dict(zip(held, at))
+
+    def grad(scratch, err=None, **where):
+        p = {**places, **where}
+        return lib.engram_embed_grad(p["dout"], 0, p["ids"], n, streams, rows, dim, 1.0, -1, 0, p["dt"], 1, scratch,
+                                     1 << 30, err, None)
+    for name, size in held.items():
+        first = at[9] + (need - 4 if name == "ids" else need - 16)
+        assert grad(at[9], **{name: first}) == 1, name
+        assert grad(places[name] + size // 256 * 256 - (0 if size % 256 else 256)) == 1, name
+        for err in (places[name], places[name] + size - 4):
+            assert grad(at[9], err) == 1, name
+    assert grad(at[9], at[9]) == 1 and grad(at[9], at[9] + need - 4) == 1
+
+    B, V, ld = 3, 900, 1000
+    need = ge.engram_sample_scratch_size(B, V)
+    held = {"logits": ((B - 1) * ld + V) * 2, **{name: B * 4 for name in ("u", "t", "k", "p", "m", "tok", "lp")}}
+    places = dict(zip(held, at))
+
+    def sample(scratch, err=None, **where):
+        p = {**places, **where}
+        return lib.engram_sample(p["logits"], 0, ld, p["u"], p["t"], p["k"], p["p"], p["m"], B, V, p["tok"], p["lp"],
+                                 scratch, 1 << 30, err, None)
+    for name, size in held.items():
+        assert sample(at[9], **{name: at[9] + need - 4}) == 1, name
+        assert sample(places[name]) == 1, name
+        for err in (places[name], places[name] + size - 4):
+            assert sample(at[9], err) == 1, name
+    assert sample(at[9], at[9]) == 1 and sample(at[9], at[9] + need - 4) == 1
+
+    def embed(err):
+        return lib.engram_embed(at[0], 0, rows, dim, at[1], n, 1.0, streams, at[2], 0, err, None)
+    for err in (at[0], at[0] + rows * dim * 2 - 4, at[1], at[1] + n * 4 - 4, at[2], at[2] + n * streams * dim * 2 - 4):
+        assert embed(err) == 1
