@@ -26,6 +26,8 @@
 // rows without a filter 54 + 9 us, bound by the exponentials (21 instructions a logit, the
 // vector units busy 80% of the time; their bytes take 28).  Elementary torch
 // operations, with a sort in 64 bits: 350, 2100 and 3050 us.
+#include <type_traits>
+
 #include "lanes.h"
 #include "logits.h"
 
@@ -292,11 +294,12 @@ __global__ void __launch_bounds__(64 * kBlockWaves) sample_part_kernel(
                     const float x = v[i][e];
                     const double w = want.weigh(x, top);
                     s += w;
-                    // whole numbers of 2^-48, in any order: 2^13 of them at most
+                    // whole numbers of 2^-50, in any order: 2^13 of them at most, and off by 2^-38 of
+                    // the block's largest together
                     if (x > -INFINITY)
                         atomicAdd(&bucket[min(most - want.bucket(x), kRest) * kCopies + copy],
-                                  (unsigned long long)(__double_as_longlong(w + 16.0) -
-                                                       __double_as_longlong(16.0)));
+                                  (unsigned long long)(__double_as_longlong(w + 4.0) -
+                                                       __double_as_longlong(4.0)));
                 }
         } else {
 #pragma unroll
@@ -316,19 +319,66 @@ __global__ void __launch_bounds__(64 * kBlockWaves) sample_part_kernel(
 #pragma unroll
             for (int j = 0; j < kCopies; ++j)
                 all += weights ? bucket[b * kCopies + j] : number[b * kCopies + j];
-            out.buckets[block * kBuckets + b] = (double)all * (weights ? 0x1p-48 : 1.0);
+            out.buckets[block * kBuckets + b] = (double)all * (weights ? 0x1p-50 : 1.0);
         }
     }
     s = last_lane(sum_upto(s));
     if (lane == 0) out.sums[row * out.blocks * kBlockWaves + part] = s;
 }
 
+// Sums of weights, of 1 at most each, in whole numbers, the same in any order, and how many
+// there are.  Of up to 2^13 of them (WIDE = false) in one word, units 2^-50: off by 2^-38 at most
+// together, where the row's largest weighs 1.
+template <bool WIDE>
+struct Sum {
+    uint64_t upper = 0, lower = 0;
+    static __device__ __forceinline__ uint64_t units_of(double w) {
+        return (uint64_t)(__double_as_longlong(w + 4.0) - __double_as_longlong(4.0));
+    }
+    static __device__ __forceinline__ uint64_t upper_of(uint64_t units) { return units; }
+    static __device__ __forceinline__ uint64_t lower_of(uint64_t) { return 1; }
+    __device__ __forceinline__ uint64_t number() const { return lower; }
+    __device__ __forceinline__ double value() const { return (double)upper * 0x1p-50; }
+    __device__ __forceinline__ bool reaches(double target) const { return (double)upper >= target * 0x1p50; }
+};
+// Of up to 2^22 in two words, units 2^-60, what is below cut off (2^-38 together, too): upper
+// parts of 2^-41, and lower ones of 19 bits, whose sums take 41 below the number.  (In one word
+// the unit would be 2^-41, and a row's weights below it, which count as nothing then, can be
+// 2^-19 together.)
+template <>
+struct Sum<true> {
+    static constexpr int kLow = 19, kNumber = 41;
+    static constexpr uint64_t kLowMask = (1ull << kLow) - 1, kSumMask = (1ull << kNumber) - 1;
+    uint64_t upper = 0, lower = 0;
+    static __device__ __forceinline__ uint64_t units_of(double w) {
+        const uint64_t b = (uint64_t)__double_as_longlong(w);
+        const uint32_t e = 1023u - (uint32_t)(b >> 52);
+        return e < 64 ? ((b & 0xFFFFFFFFFFFFFull) | 1ull << 52) << 8 >> e : 0;
+    }
+    static __device__ __forceinline__ uint64_t upper_of(uint64_t units) { return units >> kLow; }
+    static __device__ __forceinline__ uint64_t lower_of(uint64_t units) {
+        return (units & kLowMask) | 1ull << kNumber;
+    }
+    __device__ __forceinline__ uint64_t number() const { return lower >> kNumber; }
+    // the lower parts' carry on to the upper ones
+    __device__ __forceinline__ uint64_t high() const { return upper + ((lower & kSumMask) >> kLow); }
+    __device__ __forceinline__ double low() const { return (double)(uint32_t)(lower & kLowMask); }
+    __device__ __forceinline__ double value() const { return (double)high() * 0x1p-41 + low() * 0x1p-60; }
+    // compared exactly, so that what holds of a sum holds of larger ones
+    __device__ __forceinline__ bool reaches(double target) const {
+        if (!(target > 0.0)) return true;
+        const double t = target * 0x1p41, whole = floor(t);
+        const uint64_t h = high(), w = (uint64_t)whole;
+        return h > w || (h == w && low() >= (t - whole) * 0x1p19);
+    }
+};
+
 // What the threads of a row's workgroup exchange
 struct Shared {
     double sum[kRowWaves];
     uint64_t whole[2][kRowWaves];
-    uint32_t count[kBins];
-    uint64_t mass[kBins + 1];  // (a row's blocks are at most that many)
+    uint64_t count[kBins];     // Sums' lower words,
+    uint64_t mass[kBins + 1];  // and upper ones (a row's blocks are at most that many)
     int first, last, hits, listed, at[kRowWaves];
     uint32_t range[2];
     bool none;
@@ -428,32 +478,35 @@ struct Cut {
     }
 };
 
-// Logits and their weights in whole numbers of 2^-scale, so that they add up to the same
+// Logits and their weights in whole numbers, so that they add up to the same
 // in any order.  Each: each(f) calls f(logit, index, units) for its logits above -infinity,
 // spread over the workgroup's threads; units() are the weight.
-// RUNS: neighbours are often equal.  T: what the logits were (bf16: half of a key says which).
+// RUNS: neighbours are often equal, and there may be a whole row of them.  T: what the
+// logits were (bf16: half of a key says which).
 template <class T, bool RUNS, class Each>
 struct Narrow {
+    using Sums = Sum<RUNS>;
+    using Lower = std::conditional_t<RUNS, uint64_t, uint32_t>;  // a lower word in LDS
     static constexpr int DROP = sizeof(T) == 2 ? 16 : 0;
     const Each& each;
     const Want& want;
     const float top;
-    const double unit;  // 2^-scale
     Shared& sh;
 
     // The first place (of those in [lo, hi], what place(logit, index) is; ~0: no candidate) up
-    // to which reached(number, weight) holds of the candidates; passes over them narrow it
-    // down by a factor of kBins each.  False where it is never reached.  n, m: what
+    // to which reached(sum) holds of the candidates; passes over them narrow it
+    // down by a factor of kBins each.  False where it is never reached.  before: what
     // lies before the place, ties: the candidates at it.
     template <class Place, class Reached>
     __device__ __forceinline__ bool find(uint32_t& lo, uint32_t hi, bool weights, Place place, Reached reached,
-                         uint64_t& n, uint64_t& m, uint64_t& ties) const {
+                         Sums& before, uint64_t& ties) const {
         const int tid = threadIdx.x;
-        n = m = 0;
+        Lower* const count = reinterpret_cast<Lower*>(sh.count);
+        before = Sums();
         while (true) {
             const int shift = lo < hi ? max(0, 32 - kBinBits - __builtin_clz(hi - lo)) : 0;
             __syncthreads();
-            sh.count[tid] = 0;
+            count[tid] = 0;
             sh.mass[tid] = 0;
             if (tid == 0) sh.none = true;
             __syncthreads();
@@ -468,64 +521,70 @@ struct Narrow {
                     const uint64_t w_one = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(w >> 32)) << 32 |
                                            (uint32_t)__builtin_amdgcn_readfirstlane((int)w);
                     if (__ballot(bin == one && w == w_one) == here) {
-                        if ((uint32_t)__builtin_ctzll(here) == (tid & 63)) {
-                            const uint32_t number = __builtin_popcountll(here);
-                            atomicAdd(&sh.count[one], number);
-                            if (weights)
-                                atomicAdd((unsigned long long*)&sh.mass[one], (unsigned long long)(w_one * number));
-                        }
+                        if ((uint32_t)__builtin_ctzll(here) == (tid & 63))
+                            add(one, w_one, __builtin_popcountll(here), weights);
                         return;
                     }
                 }
-                atomicAdd(&sh.count[bin], 1u);
-                if (weights) atomicAdd((unsigned long long*)&sh.mass[bin], (unsigned long long)w);
+                add(bin, w, 1, weights);
             });
             __syncthreads();
-            const uint64_t own_n = sh.count[tid], own_m = sh.mass[tid];
-            uint64_t before_n = own_n, before_m = own_m;
-            scan(before_n, before_m, sh);
-            // (whole numbers: one thread's share is the first that reaches)
-            if (own_n > 0 && reached(n + before_n + own_n, m + before_m + own_m) &&
-                !(before_n > 0 && reached(n + before_n, m + before_m))) {
-                sh.above[0] = n + before_n;
-                sh.above[1] = m + before_m;
-                sh.above[2] = own_n;
+            const uint64_t own_u = sh.mass[tid], own_l = count[tid];
+            uint64_t u = own_u, l = own_l;
+            scan(u, l, sh);
+            const Sums from{before.upper + u, before.lower + l}, to{from.upper + own_u, from.lower + own_l};
+            // (one thread's share is the first that reaches)
+            if (own_l > 0 && reached(to) && !(l > 0 && reached(from))) {
+                sh.above[0] = from.upper;
+                sh.above[1] = from.lower;
+                sh.above[2] = own_l;
                 sh.first = tid;
                 sh.none = false;
             }
             __syncthreads();
             if (sh.none) return false;
             const int at = sh.first;
-            n = sh.above[0];
-            m = sh.above[1];
-            ties = sh.above[2];
+            before = Sums{sh.above[0], sh.above[1]};
+            ties = Sums{0, sh.above[2]}.number();
             lo += (uint32_t)at << shift;
             if (shift == 0) return true;
             hi = min(hi, lo + ((1u << shift) - 1));
         }
     }
+    // a weight, so many times
+    __device__ __forceinline__ void add(uint32_t bin, uint64_t units, uint32_t number, bool weights) const {
+        const uint64_t u = Sums::upper_of(units) * number, l = Sums::lower_of(units) * number;
+        if (RUNS && weights)
+            atomicAdd((unsigned long long*)&sh.count[bin], (unsigned long long)l);
+        else if (RUNS)  // (a number alone lies in the upper half)
+            atomicAdd(reinterpret_cast<uint32_t*>(sh.count) + 2 * bin + 1, (uint32_t)(l >> 32));
+        else
+            atomicAdd(reinterpret_cast<uint32_t*>(sh.count) + bin, (uint32_t)l);
+        if (weights) atomicAdd((unsigned long long*)&sh.mass[bin], (unsigned long long)u);
+    }
     // the index of the r-th of the logits with this key that `in` keeps
     __device__ __forceinline__ uint32_t index_of(uint32_t key, const Cut in, uint64_t r, int V) const {
         uint32_t idx = 0;
-        uint64_t n, m, ties;
+        Sums before;
+        uint64_t ties;
         return find(idx, (uint32_t)V - 1, false,
                     [&](float x, int i) { return key_of(x) == key && in.keeps(x, i) ? (uint32_t)i : ~0u; },
-                    [&](uint64_t a, uint64_t) { return a >= r; }, n, m, ties)
+                    [&](const Sums& upto) { return upto.number() >= r; }, before, ties)
                    ? idx
                    : ~0u;
     }
     // The cut that keeps the first k of those that `in` keeps (k > 0), or those before
-    // which less than target (in units) lies; all of them lie in [least, most].  index:
-    // as index_of.
+    // which less than target lies; all of them lie in [least, most].  index: as index_of.
     template <class Index>
     __device__ __forceinline__ Cut cut(const Cut in, int k, double target, float most, float least, int V,
                                        Index index) const {
         uint32_t at = ~key_of(most) >> DROP;
-        uint64_t n, m, ties;
+        Sums before;
+        uint64_t ties;
         if (!find(at, ~max(in.key, key_of(least)) >> DROP, k == 0,
                   [&](float x, int i) { return in.keeps(x, i) ? ~key_of(x) >> DROP : ~0u; },
-                  [&](uint64_t a, uint64_t b) { return k ? a >= (uint64_t)k : (double)b >= target; },
-                  n, m, ties)) {
+                  [&](const Sums& upto) { return k ? upto.number() >= (uint64_t)k : upto.reaches(target); },
+                  before, ties)) {
             // all of them do not reach it (by a rounding, or there are fewer)
             Cut all = in;
             if (key_of(least) > in.key) all.key = key_of(least), all.idx = ~0u;
@@ -536,21 +595,16 @@ struct Narrow {
         if (DROP && (out.key & 0x80000000u)) out.key &= ~0xFFFFu;  // (the lower half is clear from zero on)
         out.idx = in.key == out.key ? in.idx : ~0u;
         // how many of the equal ones at the cut stay, and the last of these
-        double stay = (double)k - (double)n;
-        if (k == 0) stay = ceil((target - (double)m) / (want.weigh(value_of(out.key), top) / unit));
+        double stay = (double)k - (double)before.number();
+        if (k == 0) stay = ceil((target - before.value()) / want.weigh(value_of(out.key), top));
         const uint64_t r = stay < 1.0 ? 1 : stay > 0x1p31 ? (uint64_t)1 << 31 : (uint64_t)stay;
         if (r < ties) out.idx = index(out.key, in, r);
         return out;
     }
 };
 template <class T, bool RUNS, class Each>
-__device__ __forceinline__ Narrow<T, RUNS, Each> narrow(const Each& each, const Want& want, float top, int scale,
-                                                        Shared& sh) {
-    return Narrow<T, RUNS, Each>{each, want, top, ldexp(1.0, -scale), sh};
-}
-// a weight in whole numbers of 2^-scale, magic = 2^(52 - scale)
-__device__ __forceinline__ uint64_t units_of(double w, double magic) {
-    return (uint64_t)(__double_as_longlong(w + magic) - __double_as_longlong(magic));
+__device__ __forceinline__ Narrow<T, RUNS, Each> narrow(const Each& each, const Want& want, float top, Shared& sh) {
+    return Narrow<T, RUNS, Each>{each, want, top, sh};
 }
 
 // One workgroup a row.
@@ -845,8 +899,6 @@ struct Sampler {
     // top-k, else weight) before these.  (64 rows: bf16 with top-p 0.9 at temperature 2 202
     // us, narrowing by whole keys and indices 362; equal fp32 ones 225 and 289.)
     __device__ __forceinline__ void by_passes(double total, float least, float over, double above) const {
-        const int scale = min(50, 30 + __builtin_clz(V));
-        const double magic = ldexp(1.0, 52 - scale);
         float most = fminf(below(over), top);
         if constexpr (sizeof(T) == 4) {  // (bf16 has few keys: a pass less, or none more)
             uint32_t lo = ~0u, hi = 0;
@@ -869,10 +921,10 @@ struct Sampler {
         }
         auto each = [&](auto f) {
             every([&](float x, int i) {
-                if (x >= least && x <= most) f(x, i, [&] { return units_of(want.weigh(x, top), magic); });
+                if (x >= least && x <= most) f(x, i, [&] { return Sum<true>::units_of(want.weigh(x, top)); });
             });
         };
-        const auto row = narrow<T, true>(each, want, top, scale, sh);
+        const auto row = narrow<T, true>(each, want, top, sh);
         Cut keep;
         for (int again = 0; again < 2; ++again) {  // top-k, then top-p
             if (again ? want.p == 1.0 : want.k == 0) continue;
@@ -883,7 +935,7 @@ struct Sampler {
                 least = value_of(keep.key);
                 most = top;
             }
-            keep = row.cut(keep, again ? 0 : want.k - (int)above, again ? (want.p * total - above) / row.unit : 0.0,
+            keep = row.cut(keep, again ? 0 : want.k - (int)above, again ? want.p * total - above : 0.0,
                            most, least, V, [&](uint32_t key, const Cut in, uint64_t number) {
                                const float v = value_of(key);  // by blocks: the one that holds it, then there
                                auto equal = [=](float x, int i) {
@@ -1300,41 +1352,43 @@ struct Sampler {
             x[j] = value(idx[j]);
         }
 #pragma unroll
-        for (int j = 0; j < E; ++j) w[j] = units_of(want.weigh(x[j], top), 4.0);
+        for (int j = 0; j < E; ++j) w[j] = Sum<false>::units_of(want.weigh(x[j], top));
         auto each = [&](auto f) {
 #pragma unroll
             for (int j = 0; j < E; ++j)
                 if (tid + j * kRowThreads < listed) f(x[j], idx[j], [&] { return w[j]; });
         };
-        const auto list = narrow<T, false>(each, want, top, 50, sh);
+        const auto list = narrow<T, false>(each, want, top, sh);
         auto sum_of = [&](auto stays) {
-            uint64_t sum = 0;
-            each([&](float v, int i, auto units) { sum += stays(v, i, units()) ? units() : 0; });
-            return (double)total_of(sum, sh);
+            Sum<false> sum;
+            each([&](float v, int i, auto units) { sum.upper += stays(v, i) ? units() : 0; });
+            sum.upper = total_of(sum.upper, sh);
+            return sum.value();
         };
         auto index = [&](uint32_t key, const Cut in, uint64_t number) { return list.index_of(key, in, number, V); };
         Cut keep;
-        double target = (want.p * total - above) / list.unit;
+        double target = want.p * total - above;
         if (want.k) {
             keep = list.cut(keep, want.k, 0.0, top, least, V, index);
-            if (want.p < 1.0) target = want.p * sum_of([&](float v, int i, uint64_t) { return keep.keeps(v, i); });
+            if (want.p < 1.0) target = want.p * sum_of([&](float v, int i) { return keep.keeps(v, i); });
         }
         if (want.p < 1.0 && (few_before || cut_here)) keep = list.cut(keep, 0, target, fminf(over, top), least, V, index);
         if (few_before) {
             auto stays = [&](float v, int i) {
                 return keep.keeps(v, i) && v >= floor && want.weigh(v, top) > kNoWeight;
             };
-            const double sum = sum_of([&](float v, int i, uint64_t) { return stays(v, i); });
+            const double sum = sum_of(stays);
             const double number = want.u * sum;
             uint32_t first = 0;
-            uint64_t n_first, m_first, ties;
+            Sum<false> before_first;
+            uint64_t ties;
             // (a number of 0 takes the first one, however little it weighs)
             list.find(first, (uint32_t)V - 1, true,
                       [&](float v, int i) { return stays(v, i) ? (uint32_t)i : ~0u; },
-                      [&](uint64_t, uint64_t b) { return number == 0.0 || (double)b > number; }, n_first,
-                      m_first, ties);
+                      [&](const Sum<false>& upto) { return number == 0.0 || upto.value() > number; },
+                      before_first, ties);
             each([&](float v, int i, auto) {
-                if ((uint32_t)i == first) emit(i, log(want.weigh(v, top) / (sum * list.unit)));
+                if ((uint32_t)i == first) emit(i, log(want.weigh(v, top) / sum));
             });
             return true;
         }
@@ -1358,7 +1412,7 @@ struct Sampler {
             if (lane == 0) sh.blocks[g] = s * sh.factor[g];
         }
         __syncthreads();
-        own = tid < blocks ? sh.blocks[tid] + (double)sh.mass[tid] * list.unit : 0.0;
+        own = tid < blocks ? sh.blocks[tid] + Sum<false>{sh.mass[tid], 0}.value() : 0.0;
         double stay;
         const double at = scan(own, sh, &stay);
         target = want.u * stay;

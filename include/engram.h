@@ -428,8 +428,8 @@ engram_status engram_beam_reorder(void* const* states, const int64_t* row_bytes,
  *   min_p  of these, one stays if w >= min_p (w of the largest is 1),
  * token is the first v of those that stay, v rising, whose sum of w up to and with
  * v exceeds u times the sum of all that stay; logprob = log(w(token) / that sum).
- * Weights and sums in 64 bits (each weight to 2e-12 of itself); a w below 2^-999
- * is none.
+ * Weights in 64 bits (each to 2e-12 of itself), their sums to 1e-11 of the sum of
+ * all of them; a w below 2^-999 is none.
  *   logits bf16 (logits_f32 = 0) or fp32, B rows of V, ld >= V elements apart;
  *          rows may start at any element; a logit of -infinity never stays.
  *   u      fp32 [B], in [0, 1).
