@@ -264,6 +264,13 @@ __global__ void __launch_bounds__(64 * kBlockWaves) sample_part_kernel(
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kBlockWaves; ++w) top = fmaxf(top, wave_top[w]);
+        // (the one thing that is read of blocks without a logit above -infinity, too)
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const float g = largest_of_4(own[i]);
+            if ((lane & (kGroup - 1)) == 0)
+                out.groups[row * out.blocks * (NT * NL / kGroup) + (from + lane + 64 * i) / kGroup] = g;
+        }
     }
     if (top == -INFINITY) return;  // (the whole block, where it has a barrier ahead)
     double s = 0.0;
@@ -280,12 +287,6 @@ __global__ void __launch_bounds__(64 * kBlockWaves) sample_part_kernel(
     } else {
         const int most = want.bucket(top), copy = lane & (kCopies - 1);
         const bool weights = want.whole_sum();
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const float g = largest_of_4(own[i]);
-            if ((lane & (kGroup - 1)) == 0)
-                out.groups[row * out.blocks * (NT * NL / kGroup) + (from + lane + 64 * i) / kGroup] = g;
-        }
         if (weights) {
 #pragma unroll
             for (int i = 0; i < NL; ++i)

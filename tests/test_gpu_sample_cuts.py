@@ -1,4 +1,5 @@
-"""engram_sample where a cut falls among logits that weigh little each and much together.
+"""engram_sample where a cut falls among logits that weigh little each and much together,
+and on scratch that held other numbers.
 
 The header promises sums to 1e-11 of the row's.  So a cut is the formula's for a border moved
 by at most that, and the token the formula's for a number moved by at most that, too: both
@@ -62,3 +63,32 @@ def test_a_cut_among_small_weights(ge, V, logits, dtype):  # noqa: F811
             if which[int(got)] == which[least] == which[most]:
                 want = float(np.log(share))
                 assert abs(float(lp) - want) <= 2.0 ** -24 * abs(want) + 1e-10
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+def test_what_scratch_held_decides_nothing(ge, dtype):  # noqa: F811
+    """Blocks of 8192 logits that a mask leaves empty: what the second kernel reads of them (the largest logits of
+    groups, scratch's last array) is written by the first, so that no work depends on what was there."""
+    dev = torch.device("cuda:0")
+    say("sample scratch", dtype)
+    B, V = 3, 65000
+    groups = B * 8 * (2048 if dtype == "f32" else 1024) // 4
+    x = torch.full((B, V), -float("inf"), dtype=KINDS[dtype], device=dev)
+    x[0, 30000:30100] = torch.arange(100, device=dev) / 64
+    x[1, ::20000] = 1.0
+    x[2, V - 9:] = -2.0
+    full = lambda v, kind=torch.float32: torch.full((B,), v, dtype=kind, device=dev)  # noqa: E731
+    size = ge.engram_sample_scratch_size(B, V)
+    last = B * 8 * 2048
+    for kw in (dict(top_p=full(0.9)), dict(top_k=full(7, torch.int32)), dict(min_p=full(0.3))):
+        seen = []
+        for held in (0x00, 0x7F, 0xFF):  # 0x7F7F7F7F: 3.4e38, above every logit
+            scratch = torch.full((size,), held, dtype=torch.uint8, device=dev)
+            seen.append(ge.engram_sample(x, full(0.7), scratch=scratch, **kw))
+            found = scratch[size - last:].view(torch.float32)[:groups].view(B, 8, -1)
+            dead = torch.ones(B, 8, dtype=torch.bool, device=dev)
+            dead[0, 3] = dead[2, 7] = False
+            dead[1, [0, 2, 4, 7]] = False
+            assert (found[dead] == -float("inf")).all(), held
+        for got in seen[1:]:
+            assert torch.equal(got[0], seen[0][0]) and torch.equal(got[1], seen[0][1])
