@@ -498,8 +498,10 @@ struct Narrow {
     // to which reached(sum) holds of the candidates; passes over them narrow it
     // down by a factor of kBins each.  False where it is never reached.  before: what
     // lies before the place, ties: the candidates at it.
-    template <class Place, class Reached>
-    __device__ __forceinline__ bool find(uint32_t& lo, uint32_t hi, bool weights, Place place, Reached reached,
+    // WEIGHTS: they are summed, otherwise candidates are only counted (known when run, both
+    // take longer: equal fp32 logits with top-p 231 us for 211, with top-k 178 for 141).
+    template <bool WEIGHTS, class Place, class Reached>
+    __device__ __forceinline__ bool find(uint32_t& lo, uint32_t hi, Place place, Reached reached,
                          Sums& before, uint64_t& ties) const {
         const int tid = threadIdx.x;
         Lower* const count = reinterpret_cast<Lower*>(sh.count);
@@ -515,7 +517,7 @@ struct Narrow {
                 const uint32_t at = place(x, i);
                 if (at < lo || at > hi) return;
                 const uint32_t bin = (at - lo) >> shift;
-                const uint64_t w = weights ? units() : 0;
+                const uint64_t w = WEIGHTS ? units() : 0;
                 if constexpr (RUNS) {  // equal logits, or near indices: the wave's together
                     const uint64_t here = __ballot(1);
                     const uint32_t one = __builtin_amdgcn_readfirstlane(bin);
@@ -523,11 +525,11 @@ struct Narrow {
                                            (uint32_t)__builtin_amdgcn_readfirstlane((int)w);
                     if (__ballot(bin == one && w == w_one) == here) {
                         if ((uint32_t)__builtin_ctzll(here) == (tid & 63))
-                            add(one, w_one, __builtin_popcountll(here), weights);
+                            add<WEIGHTS>(one, w_one, __builtin_popcountll(here));
                         return;
                     }
                 }
-                add(bin, w, 1, weights);
+                add<WEIGHTS>(bin, w, 1);
             });
             __syncthreads();
             const uint64_t own_u = sh.mass[tid], own_l = count[tid];
@@ -553,22 +555,26 @@ struct Narrow {
         }
     }
     // a weight, so many times
-    __device__ __forceinline__ void add(uint32_t bin, uint64_t units, uint32_t number, bool weights) const {
+    template <bool WEIGHTS>
+    __device__ __forceinline__ void add(uint32_t bin, uint64_t units, uint32_t number) const {
+        uint32_t* const numbers = reinterpret_cast<uint32_t*>(sh.count);
+        if constexpr (!WEIGHTS) {  // (a number alone lies in the word's upper half)
+            atomicAdd(numbers + (RUNS ? 2 * bin + 1 : bin), number << (RUNS ? 9 : 0));
+            return;
+        }
         const uint64_t u = Sums::upper_of(units) * number, l = Sums::lower_of(units) * number;
-        if (RUNS && weights)
+        if constexpr (RUNS)
             atomicAdd((unsigned long long*)&sh.count[bin], (unsigned long long)l);
-        else if (RUNS)  // (a number alone lies in the upper half)
-            atomicAdd(reinterpret_cast<uint32_t*>(sh.count) + 2 * bin + 1, (uint32_t)(l >> 32));
         else
-            atomicAdd(reinterpret_cast<uint32_t*>(sh.count) + bin, (uint32_t)l);
-        if (weights) atomicAdd((unsigned long long*)&sh.mass[bin], (unsigned long long)u);
+            atomicAdd(numbers + bin, (uint32_t)l);
+        atomicAdd((unsigned long long*)&sh.mass[bin], (unsigned long long)u);
     }
     // the index of the r-th of the logits with this key that `in` keeps
     __device__ __forceinline__ uint32_t index_of(uint32_t key, const Cut in, uint64_t r, int V) const {
         uint32_t idx = 0;
         Sums before;
         uint64_t ties;
-        return find(idx, (uint32_t)V - 1, false,
+        return find<false>(idx, (uint32_t)V - 1,
                     [&](float x, int i) { return key_of(x) == key && in.keeps(x, i) ? (uint32_t)i : ~0u; },
                     [&](const Sums& upto) { return upto.number() >= r; }, before, ties)
                    ? idx
@@ -582,10 +588,12 @@ struct Narrow {
         uint32_t at = ~key_of(most) >> DROP;
         Sums before;
         uint64_t ties;
-        if (!find(at, ~max(in.key, key_of(least)) >> DROP, k == 0,
-                  [&](float x, int i) { return in.keeps(x, i) ? ~key_of(x) >> DROP : ~0u; },
-                  [&](const Sums& upto) { return k ? upto.number() >= (uint64_t)k : upto.reaches(target); },
-                  before, ties)) {
+        const uint32_t last = ~max(in.key, key_of(least)) >> DROP;
+        auto place = [&](float x, int i) { return in.keeps(x, i) ? ~key_of(x) >> DROP : ~0u; };
+        if (!(k ? find<false>(at, last, place, [&](const Sums& upto) { return upto.number() >= (uint64_t)k; },
+                              before, ties)
+                : find<true>(at, last, place, [&](const Sums& upto) { return upto.reaches(target); }, before,
+                             ties))) {
             // all of them do not reach it (by a rounding, or there are fewer)
             Cut all = in;
             if (key_of(least) > in.key) all.key = key_of(least), all.idx = ~0u;
@@ -897,8 +905,8 @@ struct Sampler {
 
     // Any filters on any row, by passes over it: the cut's key, the last of the equal ones, and
     // the weights by block.  The first cut lies in [least, over), with `above` (logits for
-    // top-k, else weight) before these.  (64 rows: bf16 with top-p 0.9 at temperature 2 202
-    // us, narrowing by whole keys and indices 362; equal fp32 ones 225 and 289.)
+    // top-k, else weight) before these.  (64 rows: bf16 with top-p 0.9 at temperature 2 187
+    // us, equal fp32 ones 211; narrowing by whole keys and indices, in an earlier form, 362 and 289.)
     __device__ __forceinline__ void by_passes(double total, float least, float over, double above) const {
         float most = fminf(below(over), top);
         if constexpr (sizeof(T) == 4) {  // (bf16 has few keys: a pass less, or none more)
@@ -1384,7 +1392,7 @@ struct Sampler {
             Sum<false> before_first;
             uint64_t ties;
             // (a number of 0 takes the first one, however little it weighs)
-            list.find(first, (uint32_t)V - 1, true,
+            list.template find<true>(first, (uint32_t)V - 1,
                       [&](float v, int i) { return stays(v, i) ? (uint32_t)i : ~0u; },
                       [&](const Sum<false>& upto) { return number == 0.0 || upto.value() > number; },
                       before_first, ties);
