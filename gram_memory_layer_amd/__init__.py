@@ -934,7 +934,9 @@ def engram_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=Non
 def engram_embed(table, ids, scale=1.0, streams=None, out=None, dtype=None, err=None):
     """Embedding rows with a scale: table bf16 or fp32 [rows, dim], ids int32
     [...] -> out [..., dim], or with streams [..., streams, dim] (every stream the
-    same), of type `dtype` (the table's if neither it nor out is given)."""
+    same), of type `dtype` (the table's if neither it nor out is given).  As with all
+    calls here autograd does not see it, whatever the table requires:
+    engram_embed_grad gives the table's gradient."""
     L = load()
     t32 = _float(table, "table")
     dev, shape = table.device, table.shape

@@ -11,11 +11,11 @@
 // All of it is bound by memory, or by the latencies of the launches where there is
 // little.  Measured: 4096 rows of 5120 to four streams 28 us, 185 MB, 6.5 TB/s (it writes
 // much more than it reads); the gradient of 4096 positions of four streams to 129,280
-// fp32 rows of 5120 428 us, of which 371 are the 2.65 GB of zeros and rows (7.1 TB/s) and 48
-// the sums (168 MB read, 5 TB/s with what they write); 32,768 positions of 2056, added to what is
-// there, 96-100 us: 24 the sort, 63 the sums (274 MB, 4.4 TB/s), 7-17 the rows that
-// reach over tiles; 98,304 positions of 64 47 us: 30 the sort, whose four launches on 48
-// workgroups are chains of latencies, 17 the sums, 4 the joining.  Elementary
+// fp32 rows of 5120 430 us, of which 374 are the 2.65 GB of zeros and rows (7.1 TB/s) and 49
+// the sums (168 MB read, 4.7 TB/s with what they write); 32,768 positions of 2056, added to what is
+// there, 95-102 us: 23 the sort, 64 the sums (274 MB, 4.3 TB/s), 15.5 the rows that
+// reach over tiles; 98,304 positions of 64 46 us: 28 the sort, whose four launches on 48
+// workgroups are chains of latencies, 16 the sums, 4 the joining.  Elementary
 // torch operations (index_add_ in fp32): 186, 670, 610 and 61.
 #include <algorithm>
 #include <type_traits>
@@ -165,7 +165,7 @@ __device__ __forceinline__ uint64_t same_digit(uint32_t digit) {
 // Where each of the chunk's pairs goes, counting from its digit's first place:
 // the pairs of a wave are kEach rows of 64, in order.  Leaves in count[bin] the
 // chunk's number of pairs of that digit, in wave_count[w][bin] those of the
-// waves before w.  count and wave_count hold zeros on entry.
+// waves before w.  wave_count holds zeros on entry.
 __device__ __forceinline__ void rank_chunk(const uint32_t (&digit)[kEach], int bits,
                                            uint16_t (&rank)[kEach],
                                            uint16_t (*wave_count)[kMaxBins],
@@ -1010,6 +1010,9 @@ hipError_t run_grad(const void* dout, const int32_t* ids, int64_t n, int streams
         constexpr int S = decltype(streams_)::value;
         return once ? grad_sum_kernel<D, W, S, true> : grad_sum_kernel<D, W, S, false>;
     };
+    // (3 and 5 to 8 streams by one kernel, a load at a time and through the caches: 4096
+    // positions of 5120 in bf16, added to fp32 rows, 62, 73 and 113 us with 3, 5 and 8; 53, 60 and
+    // 70 with 1, 2 and 4.  Of 1024: 25, 30 and 38; 19, 19 and 24)
     auto k = streams == 1   ? kernel(std::integral_constant<int, 1>())
              : streams == 2 ? kernel(std::integral_constant<int, 2>())
              : streams == 4 ? kernel(std::integral_constant<int, 4>())

@@ -9,7 +9,7 @@
 //   exceeds u times the sum of all that stay.
 //
 // The sums of weights decide which tokens come out, so weights and sums are held
-// in 64 bits.
+// in 64 bits, or in whole numbers where additions come in any order.
 //
 // Two kernels, none of which sorts.  The first reads the logits once, many
 // workgroups a row, and leaves per part of 2048 its largest logit and sum of
@@ -19,11 +19,11 @@
 // may stay before it, or where that is much the bucket and the block that holds
 // the random number, is read again.
 //
-// Measured (129,280 logits a row): one row with top-k 50 and top-p 0.95 6.0 + 12.0
-// us, a chain of latencies; 64 fp32 rows with top-p 0.9 17.1 + 35 us, the first one bound
+// Measured (129,280 logits a row): one row with top-k 50 and top-p 0.95 6.1 + 11.7
+// us, a chain of latencies; 64 fp32 rows with top-p 0.9 17.8 + 35 us, the first one bound
 // by the 64-bit exponentials and the histogram (its bytes take 7), the second one by
 // the flat rows, whose 517 KB one compute unit reads; 512 bf16
-// rows without a filter 54 + 9 us, bound by the exponentials (21 instructions a logit, the
+// rows without a filter 55 + 9 us, bound by the exponentials (21 instructions a logit, the
 // vector units busy 80% of the time; their bytes take 28).  Elementary torch
 // operations, with a sort in 64 bits: 350, 2100 and 3050 us.
 #include <type_traits>
@@ -58,7 +58,9 @@ constexpr int kSome = 64, kRanked = 256;      // that are ranked by counting, by
                                               // 27 us, found by narrowing down 36; one row with top-p
                                               // 0.9: 18.7, ranked by all 20.2)
 constexpr int kHits = 16 * kRowThreads;       // groups of a row looked at together
-constexpr int kMostBlocks = 256;              // of a row whose buckets are joined
+constexpr int kMostBlocks = 256;              // of a row whose buckets are joined: longer ones' filters go by passes
+                                              // (2 fp32 rows with top-k 50: of 2^21 - 8 logits 99 us, of 2^22
+                                              // 6.2 ms)
 
 // exp(d / T) for d <= 0, by c = log2(e) / T: 2^n * 2^f, f in [-1/2, 1/2], 2^f by a
 // polynomial of degree eight with the least relative error (1.1e-12, by Remez'

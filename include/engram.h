@@ -443,7 +443,8 @@ engram_status engram_beam_reorder(void* const* states, const int64_t* row_bytes,
  * A row whose logits are all -infinity has token -1 and logprob -infinity; so has
  * one with a NaN or +infinity among its logits (ENGRAM_ERRBIT_LOGIT), or with a
  * parameter outside the ranges above, a NaN one too (ENGRAM_ERRBIT_SAMPLE).
- * 1 <= V <= 2^22, B <= 65535, about B * V < 2^37.  scratch:
+ * 1 <= V <= 2^22, B <= 65535, about B * V < 2^37; rows of more than 2^21 - 7 take
+ * milliseconds where a filter is on.  scratch:
  * engram_sample_scratch_size bytes (0 where sizes are refused), 256-byte aligned;
  * contents on entry do not matter. */
 size_t engram_sample_scratch_size(int32_t B, int32_t V);
@@ -471,8 +472,8 @@ engram_status engram_embed(const void* table, int32_t table_f32, int64_t rows, i
  *   dtable[v] = scale * sum over i with ids[i] = v, and s, of dout[i][s]
  * with accumulate = 0, every row written (zeros where no id names it), or that
  * added to the row that is there with accumulate = 1, where rows that no id
- * names are not touched.  Sums in fp32 in an order that n, dim and the ids
- * decide (the same on every run); scale and the addition are one rounding to
+ * names are not touched.  Sums in fp32 in an order that the sizes, pad_id and the
+ * ids decide (the same on every run); scale and the addition are one rounding to
  * fp32, then, for a bf16 dtable, one to bf16.
  *   dout   bf16 (dout_f32 = 0) or fp32 [n, streams, dim];
  *   ids    int32 [n]; positions with pad_id (-1: none) add nothing, and those with an
